@@ -19,12 +19,15 @@ LIB_PATH = os.path.join(_PKG, "_lib", "libmoegmm.so")
 PREC = {"bf16": 0, "mxfp8": 1, "nvfp4": 2}
 ACT = {"swiglu": 0, "clamped_swiglu": 1, "geglu": 2, "srelu": 3}
 EXTRA_BIAS, EXTRA_SCALE = 1, 2  # moe_layer_desc_t.extras bits
+DTYPE = {"bf16": 0, "fp32": 1}  # moe_dtype_t
 DEVERR = {0: "none", 1: "capacity", 2: "timeout", 3: "bad_id"}
 
 KERNEL_NAMES = ("route_topk", "assign_rows", "gather_x", "gemm_fc1_fprop", "gemm_fc2_fprop",
                 "combine_y", "gather_dy", "gemm_fc2_dgrad", "dprob_reduce", "gemm_fc2_wgrad",
                 "gemm_fc1_dgrad", "combine_dx", "gemm_fc1_wgrad", "mxfp8_quantize", "pack_fc1",
-                "extras_reduce", "nvfp4_amax", "nvfp4_quantize", "route_export")
+                "extras_reduce", "nvfp4_amax", "nvfp4_quantize", "route_export", "router_loss",
+                "router_grad", "layernorm_fwd", "layernorm_bwd", "layernorm_reduce", "grad_norm",
+                "grad_scale", "fp8_quantize", "fp8_gemm")
 # moe_ws_layout_t.nv_amax slots (fp32 [16], first 10 used)
 NV_AMAX = ("x", "xt", "w1", "w2", "a", "at", "dy", "dyt", "dz", "dzt")
 
@@ -34,7 +37,11 @@ EXPORTS = ("moe_timeline_begin", "moe_timeline_end", "moe_workspace_size", "moe_
            "moe_last_error_string", "moe_selftest_wait_timeout", "moe_selftest_gemm_timeout",
            "moe_route_export",
            "moe_grouped_mlp_fwd_ex",
-           "moe_grouped_mlp_bwd_ex", "nvfp4_amax", "nvfp4_quantize")
+           "moe_grouped_mlp_bwd_ex", "nvfp4_amax", "nvfp4_quantize",
+           "moe_router_loss_workspace", "moe_router_loss_fwd", "moe_router_loss_bwd",
+           "moe_layernorm_fwd", "moe_layernorm_workspace", "moe_layernorm_bwd",
+           "moe_grad_clip_workspace", "moe_grad_clip", "fp8_block_quantize_rows",
+           "fp8_block_quantize_weight", "fp8_block_gemm")
 
 
 class LayerDesc(ctypes.Structure):
@@ -66,6 +73,7 @@ _P = ctypes.c_void_p
 _I32 = ctypes.c_int32
 _I64 = ctypes.c_int64
 _SZ = ctypes.c_size_t
+_F32 = ctypes.c_float
 _DP = ctypes.POINTER(LayerDesc)
 
 
@@ -103,6 +111,24 @@ def load():
         "moe_grouped_mlp_fwd_ex": (_I32, [_DP, _I32, _P, _P, _P, _P, _P, _P, _SZ, _P]),
         "moe_grouped_mlp_bwd_ex": (_I32, [_DP, _I32, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P,
                                           _SZ, _P]),
+        "moe_router_loss_workspace": (_SZ, [_I32]),
+        "moe_router_loss_fwd": (_I32, [_P, _I64, _P, _P, _I32, _I32, _I32, _F32, _P, _P, _P, _P,
+                                       _P, _SZ, _P]),
+        "moe_router_loss_bwd": (_I32, [_P, _I64, _P, _P, _P, _P, _I32, _I32, _I32, _F32, _P, _P,
+                                       _P, _P, _I64, _P]),
+        "moe_layernorm_fwd": (_I32, [_P, _I64, _P, _P, _P, _I64, _P, _P, _I64, _I64, _F32, _I32,
+                                     _I32, _P]),
+        "moe_layernorm_workspace": (_SZ, [_I64, _I64]),
+        "moe_layernorm_bwd": (_I32, [_P, _I64, _P, _I64, _P, _P, _P, _P, _I64, _P, _P, _I64, _I64,
+                                     _I32, _I32, _P, _SZ, _P]),
+        "moe_grad_clip_workspace": (_SZ, []),
+        "moe_grad_clip": (_I32, [_I32, _P, _P, _P, _P, _F32, _P, _P, _SZ, _P]),
+        "fp8_block_quantize_rows": (_I32, [_P, _I64, _I64, _I64, _P, _I64, _P, _I64, _P, _I64, _P,
+                                           _I64, _P]),
+        "fp8_block_quantize_weight": (_I32, [_P, _I64, _I64, _I64, _P, _I64, _P, _P, _I64, _P,
+                                             _P]),
+        "fp8_block_gemm": (_I32, [_P, _I64, _P, _I64, _P, _I64, _P, _I64, _I32, _P, _I64, _I32,
+                                  _I64, _I64, _I64, _P, _P]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -275,6 +301,79 @@ def moe_route_export(desc, ws, ws_bytes, T, offsets=None, row_of=None, src_of=No
                                    _ptr(offsets), _ptr(row_of), _ptr(src_of), _ptr(row_prob),
                                    _stream(stream)))
 
+def moe_router_loss_workspace(E) -> int:
+    n = load().moe_router_loss_workspace(E)
+    if n == 0:
+        raise MoeError(1, load().moe_last_error_string().decode())
+    return n
+
+
+def moe_router_loss_fwd(logits, ld_logits, topk_ids, token_mask, T, E, k, coef, loss, counts,
+                        mean_prob, n_valid, ws, ws_bytes, stream=None):
+    _check(load().moe_router_loss_fwd(_ptr(logits), ld_logits, _ptr(topk_ids), _ptr(token_mask), T,
+                                      E, k, coef, _ptr(loss), _ptr(counts), _ptr(mean_prob),
+                                      _ptr(n_valid), _ptr(ws), ws_bytes, _stream(stream)))
+
+
+def moe_router_loss_bwd(logits, ld_logits, topk_ids, topk_probs, d_probs, token_mask, T, E, k,
+                        coef, d_loss, counts, n_valid, d_logits, ld_d, stream=None):
+    _check(load().moe_router_loss_bwd(_ptr(logits), ld_logits, _ptr(topk_ids), _ptr(topk_probs),
+                                      _ptr(d_probs), _ptr(token_mask), T, E, k, coef,
+                                      _ptr(d_loss), _ptr(counts), _ptr(n_valid), _ptr(d_logits),
+                                      ld_d, _stream(stream)))
+
+
+def moe_layernorm_fwd(x, ldx, gamma, beta, y, ldy, mean, rstd, M, N, eps, x_dtype, w_dtype,
+                      stream=None):
+    """x_dtype, w_dtype: values of DTYPE."""
+    _check(load().moe_layernorm_fwd(_ptr(x), ldx, _ptr(gamma), _ptr(beta), _ptr(y), ldy,
+                                    _ptr(mean), _ptr(rstd), M, N, eps, x_dtype, w_dtype,
+                                    _stream(stream)))
+
+
+def moe_layernorm_workspace(M, N) -> int:
+    n = load().moe_layernorm_workspace(M, N)
+    if n == 0:
+        raise MoeError(1, load().moe_last_error_string().decode())
+    return n
+
+
+def moe_layernorm_bwd(dy, lddy, x, ldx, gamma, mean, rstd, dx, lddx, dgamma, dbeta, M, N, x_dtype,
+                      w_dtype, ws, ws_bytes, stream=None):
+    _check(load().moe_layernorm_bwd(_ptr(dy), lddy, _ptr(x), ldx, _ptr(gamma), _ptr(mean),
+                                    _ptr(rstd), _ptr(dx), lddx, _ptr(dgamma), _ptr(dbeta), M, N,
+                                    x_dtype, w_dtype, _ptr(ws), ws_bytes, _stream(stream)))
+
+
+def moe_grad_clip_workspace() -> int:
+    return load().moe_grad_clip_workspace()
+
+
+def moe_grad_clip(n, grads, outs, numel, dtypes, max_norm, norm, ws, ws_bytes, stream=None):
+    """grads, outs (or None), numel, dtypes: ctypes arrays in host memory (include/moegmm.h)."""
+    _check(load().moe_grad_clip(n, grads, outs, numel, dtypes, max_norm, _ptr(norm), _ptr(ws),
+                                ws_bytes, _stream(stream)))
+
+
+def fp8_block_quantize_rows(x, ldx, M, N, q_row=None, ld_qrow=0, s_row=None, ld_srow=0, q_col=None,
+                            ld_qcol=0, s_col=None, ld_scol=0, stream=None):
+    _check(load().fp8_block_quantize_rows(_ptr(x), ldx, M, N, _ptr(q_row), ld_qrow, _ptr(s_row),
+                                          ld_srow, _ptr(q_col), ld_qcol, _ptr(s_col), ld_scol,
+                                          _stream(stream)))
+
+
+def fp8_block_quantize_weight(w, ldw, N, K, q, ldq, s, qt=None, ldqt=0, st=None, stream=None):
+    _check(load().fp8_block_quantize_weight(_ptr(w), ldw, N, K, _ptr(q), ldq, _ptr(s), _ptr(qt),
+                                            ldqt, _ptr(st), _stream(stream)))
+
+
+def fp8_block_gemm(a, lda, sa, ld_sa, b, ldb, sb, ld_sb, b_scale, c, ldc, c_dtype, M, N, K,
+                   err=None, stream=None):
+    """b_scale: 1 for 128 x 128 blocks of b, 0 for 1 x 128; c_dtype: a value of DTYPE."""
+    _check(load().fp8_block_gemm(_ptr(a), lda, _ptr(sa), ld_sa, _ptr(b), ldb, _ptr(sb), ld_sb,
+                                 b_scale, _ptr(c), ldc, c_dtype, M, N, K, _ptr(err),
+                                 _stream(stream)))
+
 
 def moe_get_error(desc, ws, stream=None) -> int:
     """Synchronous convenience: enqueue the copy, synchronise the stream, return the code."""
@@ -423,3 +522,258 @@ def pack_w1(w1_logical, gated=True, ilv=64, stream=None):
     out = torch.empty(E, N1, H, dtype=w1_logical.dtype, device=w1_logical.device)
     moe_pack_fc1_weight(w1_logical, out, E, H, F, gated, ilv, 0, stream)
     return out
+
+
+# ------------------------------------------------------------------ operators around the layer
+def _dtype_code(dtype) -> int:
+    import torch
+    code = {torch.bfloat16: 0, torch.float32: 1}.get(dtype)
+    if code is None:
+        raise ValueError(f"dtype must be bfloat16 or float32, not {dtype}")
+    return code
+
+
+def _expect(t, name, dtype, shape, rows=False):
+    """A tensor argument's type, shape and strides: contiguous, or (rows) any row stride."""
+    if t.dtype != dtype or t.shape != shape:
+        raise ValueError(f"{name}: expected {dtype} {tuple(shape)}, "
+                         f"got {t.dtype} {tuple(t.shape)}")
+    if not t.is_contiguous():
+        if not rows or (t.shape[1] > 1 and t.stride(1) != 1) or (
+                t.shape[0] > 1 and t.stride(0) < t.shape[1]):
+            raise ValueError(f"{name}: strides {t.stride()} are not supported")
+    return t
+
+
+def _ld(t) -> int:
+    """Row stride of a two-dimensional tensor (its width where it has a single row)."""
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+class RouterLoss:
+    """Load-balance loss of a top-k router over up to T_max tokens, and the gradient of the
+    router's logits (moe_router_loss_fwd / _bwd). Owns the results' buffers: they hold the last
+    call's values. The backward takes counts from the last forward."""
+
+    def __init__(self, E, k, T_max, coef=0.01, device="cuda"):
+        import torch
+        dev = torch.device(device)
+        self.E, self.k, self.T_max, self.coef = E, k, T_max, float(coef)
+        self.ws_bytes = moe_router_loss_workspace(E)
+        self.ws = torch.empty(self.ws_bytes, dtype=torch.uint8, device=dev)
+        self.loss = torch.zeros(1, dtype=torch.float32, device=dev)
+        self.counts = torch.zeros(E, dtype=torch.int32, device=dev)
+        self.mean_prob = torch.zeros(E, dtype=torch.float32, device=dev)
+        self.n_valid = torch.zeros(1, dtype=torch.int32, device=dev)
+        self.d_logits = torch.empty(T_max, E, dtype=torch.float32, device=dev)
+
+    def _tokens(self, logits, topk_ids, token_mask):
+        import torch
+        T = logits.shape[0]
+        if T > self.T_max:
+            raise ValueError(f"{T} tokens, but T_max is {self.T_max}")
+        _expect(logits, "logits", torch.float32, (T, self.E), rows=True)
+        _expect(topk_ids, "topk_ids", torch.int32, (T, self.k))
+        if token_mask is not None:
+            if token_mask.dtype not in (torch.bool, torch.uint8):
+                raise ValueError("token_mask must be bool or uint8")
+            _expect(token_mask, "token_mask", token_mask.dtype, (T,))
+        return T
+
+    def forward(self, logits, topk_ids, token_mask=None, stream=None):
+        """logits fp32 [T, E], topk_ids int32 [T, k], token_mask bool [T] (False: left out).
+        Returns (loss [1], counts int32 [E], mean_prob [E])."""
+        T = self._tokens(logits, topk_ids, token_mask)
+        moe_router_loss_fwd(logits, _ld(logits), topk_ids, token_mask, T, self.E, self.k,
+                            self.coef, self.loss, self.counts, self.mean_prob, self.n_valid,
+                            self.ws, self.ws_bytes, stream)
+        return self.loss, self.counts, self.mean_prob
+
+    def backward(self, logits, topk_ids, topk_probs=None, d_probs=None, token_mask=None,
+                 d_loss=None, stream=None):
+        """topk_probs and d_probs fp32 [T, k] (the layer's routing probabilities and the
+        gradient its backward gives them), d_loss fp32 [1] (None: 1). Returns d_logits [T, E]."""
+        import torch
+        T = self._tokens(logits, topk_ids, token_mask)
+        for t, name in ((topk_probs, "topk_probs"), (d_probs, "d_probs")):
+            if t is not None:
+                _expect(t, name, torch.float32, (T, self.k))
+        if d_loss is not None:
+            _expect(d_loss, "d_loss", torch.float32, d_loss.shape)
+            if d_loss.numel() != 1:
+                raise ValueError("d_loss must hold one value")
+        moe_router_loss_bwd(logits, _ld(logits), topk_ids, topk_probs, d_probs, token_mask, T,
+                            self.E, self.k, self.coef, d_loss, self.counts, self.n_valid,
+                            self.d_logits, self.E, stream)
+        return self.d_logits[:T]
+
+
+class LayerNorm:
+    """Layer norm over N features of up to M_max rows (moe_layernorm_fwd / _bwd). Owns the
+    results' buffers: they hold the last call's values."""
+
+    def __init__(self, N, M_max, dtype=None, weight_dtype=None, eps=1e-5, device="cuda"):
+        import torch
+        dev = torch.device(device)
+        self.dtype = torch.bfloat16 if dtype is None else dtype
+        self.weight_dtype = self.dtype if weight_dtype is None else weight_dtype
+        self._codes = _dtype_code(self.dtype), _dtype_code(self.weight_dtype)
+        self.N, self.M_max, self.eps = N, M_max, float(eps)
+        self.device = dev
+        self.y = torch.empty(M_max, N, dtype=self.dtype, device=dev)
+        self.mean = torch.empty(M_max, dtype=torch.float32, device=dev)
+        self.rstd = torch.empty(M_max, dtype=torch.float32, device=dev)
+        self.dx = None
+
+    def _rows(self, x, name):
+        if x.dim() != 2 or x.shape[0] > self.M_max:
+            raise ValueError(f"{name}: expected at most {self.M_max} rows of {self.N}")
+        return _expect(x, name, self.dtype, (x.shape[0], self.N), rows=True).shape[0]
+
+    def _weight(self, w, name):
+        return None if w is None else _expect(w, name, self.weight_dtype, (self.N,))
+
+    def forward(self, x, gamma=None, beta=None, stream=None):
+        """Returns (y [M, N], mean [M], rstd [M])."""
+        M = self._rows(x, "x")
+        moe_layernorm_fwd(x, _ld(x), self._weight(gamma, "gamma"), self._weight(beta, "beta"),
+                          self.y, self.N, self.mean, self.rstd, M, self.N, self.eps,
+                          *self._codes, stream)
+        return self.y[:M], self.mean[:M], self.rstd[:M]
+
+    def backward(self, dy, x, gamma=None, mean=None, rstd=None, stream=None):
+        """mean, rstd: the forward's (None: those of the last forward). Returns
+        (dx [M, N], dgamma [N], dbeta [N])."""
+        import torch
+        M = self._rows(x, "x")
+        if self._rows(dy, "dy") != M:
+            raise ValueError("dy and x differ in rows")
+        mean = self.mean if mean is None else _expect(mean, "mean", torch.float32, (M,))
+        rstd = self.rstd if rstd is None else _expect(rstd, "rstd", torch.float32, (M,))
+        if self.dx is None:
+            self.dx = torch.empty(self.M_max, self.N, dtype=self.dtype, device=self.device)
+            self.dgamma = torch.empty(self.N, dtype=self.weight_dtype, device=self.device)
+            self.dbeta = torch.empty(self.N, dtype=self.weight_dtype, device=self.device)
+            self.ws_bytes = moe_layernorm_workspace(self.M_max, self.N)
+            self.ws = torch.empty(self.ws_bytes, dtype=torch.uint8, device=self.device)
+        moe_layernorm_bwd(dy, _ld(dy), x, _ld(x), self._weight(gamma, "gamma"), mean, rstd,
+                          self.dx, self.N, self.dgamma, self.dbeta, M, self.N, *self._codes,
+                          self.ws, self.ws_bytes, stream)
+        return self.dx[:M], self.dgamma, self.dbeta
+
+
+class GradClip:
+    """Global norm of a fixed list of gradient tensors, and clipping in place or into `outs`
+    (moe_grad_clip). Holds references to the tensors: their memory stays where it is."""
+
+    def __init__(self, grads, outs=None):
+        import torch
+        self.grads = list(grads)
+        self.outs = self.grads if outs is None else list(outs)
+        if len(self.outs) != len(self.grads):
+            raise ValueError("outs must have one tensor for each gradient")
+        for g, o in zip(self.grads, self.outs):
+            if not g.is_contiguous() or not o.is_contiguous():
+                raise ValueError("gradients and outs must be contiguous")
+            if g.dtype != o.dtype or g.shape != o.shape:
+                raise ValueError("an out differs from its gradient in type or shape")
+        n = self.n = len(self.grads)
+        dev = self.grads[0].device if n else torch.device("cuda")
+        self._in = (_P * n)(*[g.data_ptr() for g in self.grads])
+        self._out = (_P * n)(*[o.data_ptr() for o in self.outs])
+        self._numel = (_I64 * n)(*[g.numel() for g in self.grads])
+        self._types = (_I32 * n)(*[_dtype_code(g.dtype) for g in self.grads])
+        self.norm = torch.zeros(1, dtype=torch.float32, device=dev)
+        self.ws_bytes = moe_grad_clip_workspace()
+        self.ws = torch.empty(self.ws_bytes, dtype=torch.uint8, device=dev)
+
+    def clip(self, max_norm, stream=None):
+        """Returns the norm [1] (on the device). max_norm = inf only takes the norm."""
+        outs = None if max_norm == math.inf else self._out
+        moe_grad_clip(self.n, self._in, outs, self._numel, self._types, max_norm, self.norm,
+                      self.ws, self.ws_bytes, stream)
+        return self.norm
+
+
+def _up(n, m) -> int:
+    return (n + m - 1) // m * m
+
+
+class Fp8Linear:
+    """Dense layer y = x w^T in E4M3 with a scale for each block of 128 (fp8_block_*): w [N, K]
+    bf16, x [M, K] bf16 with M <= M_max. Keeps the quantised weight (set_weight) and, for
+    training, the quantised transposes of the last forward's x. Owns the results' buffers."""
+
+    def __init__(self, N, K, M_max, train=True, device="cuda"):
+        import torch
+        dev = torch.device(device)
+        self.N, self.K, self.M_max, self.train = N, K, M_max, train
+        self.nb, self.kb = -(-N // 128), -(-K // 128)
+        self._kp, self._np, self._mp = _up(K, 16), _up(N, 16), _up(max(M_max, 1), 16)
+
+        def codes(rows, cols):
+            return torch.empty(max(rows, 1), cols, dtype=torch.uint8, device=dev)
+
+        def scales(blocks, n):
+            return torch.empty(max(blocks, 1), n, dtype=torch.float32, device=dev)
+
+        mb = -(-M_max // 128)
+        self.wq, self.ws = codes(N, self._kp), scales(self.nb, self.kb)
+        self.xq, self.xs = codes(M_max, self._kp), scales(self.kb, self._mp)
+        self.y = torch.empty(M_max, N, dtype=torch.bfloat16, device=dev)
+        self.err = torch.zeros(1, dtype=torch.int32, device=dev)
+        self.M = None
+        if train:
+            self.wqt, self.wst = codes(K, self._np), scales(self.kb, self.nb)
+            self.xqt, self.xst = codes(K, self._mp), scales(mb, _up(K, 4))
+            self.dyq, self.dys = codes(M_max, self._np), scales(self.nb, self._mp)
+            self.dyqt, self.dyst = codes(N, self._mp), scales(mb, _up(N, 4))
+            self.dx = torch.empty(M_max, K, dtype=torch.bfloat16, device=dev)
+            self.dw = torch.empty(N, K, dtype=torch.bfloat16, device=dev)
+
+    def set_weight(self, w, stream=None):
+        """Quantise w bf16 [N, K] (both orders for training); again whenever w has changed."""
+        import torch
+        _expect(w, "w", torch.bfloat16, (self.N, self.K), rows=True)
+        if self.train:
+            fp8_block_quantize_weight(w, _ld(w), self.N, self.K, self.wq, self._kp, self.ws,
+                                      self.wqt, self._np, self.wst, stream)
+        else:
+            fp8_block_quantize_weight(w, _ld(w), self.N, self.K, self.wq, self._kp, self.ws,
+                                      stream=stream)
+
+    def forward(self, x, stream=None):
+        """x bf16 [M, K] -> y bf16 [M, N]."""
+        import torch
+        M = x.shape[0]
+        if M > self.M_max:
+            raise ValueError(f"{M} rows, but M_max is {self.M_max}")
+        _expect(x, "x", torch.bfloat16, (M, self.K), rows=True)
+        if self.train:
+            fp8_block_quantize_rows(x, _ld(x), M, self.K, self.xq, self._kp, self.xs, self._mp,
+                                    self.xqt, self._mp, self.xst, _up(self.K, 4), stream)
+        else:
+            fp8_block_quantize_rows(x, _ld(x), M, self.K, self.xq, self._kp, self.xs, self._mp,
+                                    stream=stream)
+        fp8_block_gemm(self.xq, self._kp, self.xs, self._mp, self.wq, self._kp, self.ws, self.kb,
+                       1, self.y, self.N, 0, M, self.N, self.K, self.err, stream)
+        self.M = M
+        return self.y[:M]
+
+    def backward(self, dy, stream=None):
+        """dy bf16 [M, N] of the last forward's rows -> (dx bf16 [M, K], dw bf16 [N, K])."""
+        import torch
+        if not self.train or self.M is None:
+            raise ValueError("backward needs a layer made with train=True and a forward")
+        M = self.M
+        _expect(dy, "dy", torch.bfloat16, (M, self.N), rows=True)
+        if M == 0:
+            return self.dx[:0], self.dw.zero_()
+        fp8_block_quantize_rows(dy, _ld(dy), M, self.N, self.dyq, self._np, self.dys, self._mp,
+                                self.dyqt, self._mp, self.dyst, _up(self.N, 4), stream)
+        fp8_block_gemm(self.dyq, self._np, self.dys, self._mp, self.wqt, self._np, self.wst,
+                       self.nb, 1, self.dx, self.K, 0, M, self.K, self.N, self.err, stream)
+        fp8_block_gemm(self.dyqt, self._mp, self.dyst, _up(self.N, 4), self.xqt, self._mp,
+                       self.xst, _up(self.K, 4), 0, self.dw, self.K, 0, self.N, self.K, M,
+                       self.err, stream)
+        return self.dx[:M], self.dw

@@ -42,7 +42,7 @@ void count_launch(cudaStream_t s, int kid) {
 
 static thread_local std::string g_last_error;
 
-static moe_status_t fail(moe_status_t st, const char* fmt, ...) {
+moe_status_t fail(moe_status_t st, const char* fmt, ...) {
   char buf[512];
   va_list ap;
   va_start(ap, fmt);
@@ -86,11 +86,11 @@ int max_resident_pairs(const void* kernel, const cudaLaunchConfig_t* cfg) {
   return n;
 }
 
-static moe_status_t cuda_fail(cudaError_t e, const char* where) {
+moe_status_t cuda_fail(cudaError_t e, const char* where) {
   return fail(MOE_ERR_CUDA, "%s: %s", where, cudaGetErrorString(e));
 }
 
-static int device_sms() {
+int device_sms() {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return 0;
   static int cache[64] = {0};

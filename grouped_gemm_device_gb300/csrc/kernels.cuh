@@ -36,8 +36,30 @@ cudaError_t launch_kernel(void (*k)(KArgs...), dim3 grid, dim3 block, size_t sme
   cfg.numAttrs = n;
   return cudaLaunchKernelEx(&cfg, k, std::forward<Args>(args)...);
 }
-// set the message returned by moe_last_error_string for this thread (api.cu)
+// Launch `k` as a later kernel of the same call: with programmatic stream serialization, so that
+// its CTAs are scheduled while the call's previous kernel finishes. `k` starts with
+// MOE_GRIDDEP_ENTRY, so it touches memory only after that kernel has completed.
+template <typename... KArgs, typename... Args>
+cudaError_t launch_chained(void (*k)(KArgs...), dim3 grid, dim3 block, size_t smem,
+                           cudaStream_t s, Args&&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, k, std::forward<Args>(args)...);
+}
+// host-side helpers of the C entry points (api.cu): record this thread's error message and return
+// its status; the SM count of the current device
 void set_last_error(const char* msg);
+moe_status_t fail(moe_status_t st, const char* fmt, ...);
+moe_status_t cuda_fail(cudaError_t e, const char* where);
+int device_sms();
 
 // route.cu
 __global__ void route_topk_kernel(const float* logits, int T, int E, int k, int32_t* ids,

@@ -1,8 +1,9 @@
 /*
  * moegmm.h - C ABI of the GB300 (sm_103a) fused grouped expert MLP of a Mixture-of-Experts
  * layer: routing + permutation, fused FC1 -> GLU -> probability scale -> FC2 forward, the
- * matching backward (BF16, MXFP8 or NVFP4 GEMM operands), and the standalone MXFP8 and NVFP4
- * quantisers.
+ * matching backward (BF16, MXFP8 or NVFP4 GEMM operands), the standalone MXFP8 and NVFP4
+ * quantisers, and the operators around the layer in a training or serving step: the router's
+ * balance loss, layer norm, gradient clipping, and a dense FP8 product with block-128 scales.
  *
  * Sources (by page title and section):
  *   [NV-blog] NVIDIA technical blog "Boosting MoE Training Throughput with Advanced Fusion
@@ -360,6 +361,132 @@ moe_status_t moe_pack_fc1_weight(const void *w1_src, void *w1_dst, int32_t E, in
                                  int32_t F, int32_t gated, int32_t ilv, int32_t inverse,
                                  moe_stream_t stream);
 
+/* ------------------------------------------------------------------------------------------
+ * Operators around the expert layer: the router's balance loss, layer norm, gradient clipping
+ * and a dense product in 8-bit floating point with a scale for each block of 128. They take no
+ * layer description; the conventions at the top of this file hold (caller-owned device memory,
+ * no synchronisation, graph-capturable, checks before any launch). Results do not depend on the
+ * timing of the launch: sums are taken in a fixed order.
+ * ------------------------------------------------------------------------------------------ */
+typedef enum { MOE_DT_BF16 = 0, MOE_DT_FP32 = 1 } moe_dtype_t;
+
+/* Load-balance loss of a top-k router and the counts it is made of. With p[t] the softmax of
+ * token t's E logits, over the n tokens whose mask is set:
+ *   counts[e]    = number of (token, slot) pairs with topk_ids == e
+ *   mean_prob[e] = (1/n) sum_t p[t][e],     f[e] = E * counts[e] / (k * n)
+ *   loss         = coef * sum_e f[e] * mean_prob[e]       (1 * coef for a uniform router)
+ *   logits     fp32 [T, E], row stride ld_logits >= E. NaN is read as -inf; a logit equal to its
+ *              row's maximum has weight 1 before normalisation (the softmax's limit for infinite
+ *              maxima), as in moe_route_permute
+ *   topk_ids   int32 [T, k]; an id outside [0, E) is a dropped slot and counts nowhere
+ *   token_mask uint8 [T], 0 = left out (padding), or NULL: all tokens count
+ *   loss fp32 [1], counts int32 [E], mean_prob fp32 [E], n_valid int32 [1]: outputs. Without a
+ *              valid token all four are 0.
+ * E in [1, 256], k in [1, min(E, 8)], T >= 0. ws: moe_router_loss_workspace(E) bytes, 16-byte
+ * aligned, no initial value needed. */
+size_t moe_router_loss_workspace(int32_t E);
+moe_status_t moe_router_loss_fwd(const float *logits, int64_t ld_logits, const int32_t *topk_ids,
+                                 const uint8_t *token_mask, int32_t T, int32_t E, int32_t k,
+                                 float coef, float *loss, int32_t *counts, float *mean_prob,
+                                 int32_t *n_valid, void *ws, size_t ws_bytes,
+                                 moe_stream_t stream);
+/* Gradient of the router's logits: the loss's (f held constant, as it is piecewise constant)
+ * and, with topk_probs and d_probs, that of the chosen probabilities w = softmax over the k
+ * chosen logits (d_probs as moe_grouped_mlp_bwd returns it), g = *d_loss (NULL: 1):
+ *   d_logits[t][e] = mask[t] * g * coef / n * p[t][e] * (f[e] - sum_i p[t][i] f[i])
+ *                  + sum over slots j with topk_ids[t][j] == e of w[j] * (d[j] - sum_i w[i] d[i])
+ *   topk_probs, d_probs fp32 [T, k], both or neither NULL (the mask does not apply to them)
+ *   counts, n_valid     as written by moe_router_loss_fwd (device memory)
+ *   d_logits            fp32 [T, E], row stride ld_d >= E, written whole */
+moe_status_t moe_router_loss_bwd(const float *logits, int64_t ld_logits, const int32_t *topk_ids,
+                                 const float *topk_probs, const float *d_probs,
+                                 const uint8_t *token_mask, int32_t T, int32_t E, int32_t k,
+                                 float coef, const float *d_loss, const int32_t *counts,
+                                 const int32_t *n_valid, float *d_logits, int64_t ld_d,
+                                 moe_stream_t stream);
+
+/* Layer norm over the last dimension: mean and rstd = 1 / sqrt(var + eps) of each row (biased
+ * variance about the mean), y = (x - mean) * rstd * gamma + beta.
+ *   x, y         [M, N] of x_dtype, row strides ldx, ldy >= N; y may be x
+ *   gamma, beta  [N] of w_dtype, each may be NULL (1, 0)
+ *   mean, rstd   fp32 [M] out, each may be NULL (a backward pass needs both)
+ * x_dtype BF16 with w_dtype BF16 or FP32, or both FP32. eps >= 0. M >= 0, N >= 1. */
+moe_status_t moe_layernorm_fwd(const void *x, int64_t ldx, const void *gamma, const void *beta,
+                               void *y, int64_t ldy, float *mean, float *rstd, int64_t M,
+                               int64_t N, float eps, int32_t x_dtype, int32_t w_dtype,
+                               moe_stream_t stream);
+/* Its backward pass from the saved mean and rstd, with h = (x - mean) * rstd, u = dy * gamma:
+ *   dx = rstd * (u - mean_n(u) - h * mean_n(u * h)),  dgamma = sum_m dy * h,  dbeta = sum_m dy
+ *   dx            [M, N] of x_dtype, row stride lddx; may be dy or x
+ *   dgamma, dbeta [N] of w_dtype out, each may be NULL; summed in fp32 in a fixed order
+ *                 (zeros for M = 0)
+ * ws: moe_layernorm_workspace(M, N) bytes, 16-byte aligned (may be NULL when both weight
+ * gradients are). */
+size_t moe_layernorm_workspace(int64_t M, int64_t N);
+moe_status_t moe_layernorm_bwd(const void *dy, int64_t lddy, const void *x, int64_t ldx,
+                               const void *gamma, const float *mean, const float *rstd, void *dx,
+                               int64_t lddx, void *dgamma, void *dbeta, int64_t M, int64_t N,
+                               int32_t x_dtype, int32_t w_dtype, void *ws, size_t ws_bytes,
+                               moe_stream_t stream);
+
+/* Global gradient norm over n tensors, and clipping:
+ *   norm = sqrt(sum over all elements of g^2),  c = min(1, max_norm / (norm + 1e-6)),  out = c*g
+ * A NaN anywhere makes norm and c NaN; an infinite element makes c 0 (and itself NaN). Finite
+ * gradients of any magnitude have a finite sum: squares that leave fp32's range are taken in fp64,
+ * and the partial sums are fp64. norm is rounded to fp32 at the end.
+ *   grads   HOST array of n device pointers (element-aligned; a 16-byte aligned start is not
+ *           needed), numel HOST array of their element counts (>= 0), dtypes HOST array of
+ *           moe_dtype_t
+ *   outs    HOST array of n device pointers of the same types, or NULL: in place. outs[i] may
+ *           equal grads[i]; otherwise tensors must not overlap. In place, c = 1 writes nothing.
+ *   max_norm > 0; +inf: the norm alone is taken and outs must be NULL
+ *   norm    fp32 [1] device, out
+ * The three arrays are read before the call returns. n in [0, 65536].
+ * ws: moe_grad_clip_workspace() bytes, 16-byte aligned, no initial value needed. */
+size_t moe_grad_clip_workspace(void);
+moe_status_t moe_grad_clip(int32_t n, const void *const *grads, void *const *outs,
+                           const int64_t *numel, const int32_t *dtypes, float max_norm,
+                           float *norm, void *ws, size_t ws_bytes, moe_stream_t stream);
+
+/* E4M3 with one fp32 scale for each block of 128 (the layout of block-scaled FP8 checkpoints):
+ *   a = max(amax of the block, 2^-100),  s = a / 448,  code = E4M3(v * (448 / a)),
+ * each step one IEEE fp32 operation, codes rounded to nearest even and saturating; the value
+ * represented is code * s. Blocks at an edge are short. A NaN stays NaN; a block with an infinity
+ * becomes NaN as a whole once multiplied by its (infinite) scale.
+ *
+ * Blocks of 1 x 128 (activations, gradients) of x bf16 [M, N], row stride ldx >= N:
+ *   q_row e4m3 [M, N], row stride ld_qrow; s_row fp32 [ceil(N/128), M], row stride ld_srow
+ *         (the scale of row m, block b at s_row[b * ld_srow + m])
+ *   q_col e4m3 [N, M] = the transpose, blocks along M, row stride ld_qcol;
+ *         s_col fp32 [ceil(M/128), N], row stride ld_scol
+ * Either pair may be NULL. Both are made from one read of x. */
+moe_status_t fp8_block_quantize_rows(const void *x, int64_t ldx, int64_t M, int64_t N,
+                                     uint8_t *q_row, int64_t ld_qrow, float *s_row,
+                                     int64_t ld_srow, uint8_t *q_col, int64_t ld_qcol,
+                                     float *s_col, int64_t ld_scol, moe_stream_t stream);
+/* Blocks of 128 x 128 (weights) of w bf16 [N, K], row stride ldw >= K:
+ *   q  e4m3 [N, K], row stride ldq;   s  fp32 [ceil(N/128), ceil(K/128)]
+ *   qt e4m3 [K, N] = the transpose (the same codes), row stride ldqt;
+ *   st fp32 [ceil(K/128), ceil(N/128)]
+ * qt and st may both be NULL. */
+moe_status_t fp8_block_quantize_weight(const void *w, int64_t ldw, int64_t N, int64_t K,
+                                       uint8_t *q, int64_t ldq, float *s, uint8_t *qt,
+                                       int64_t ldqt, float *st, moe_stream_t stream);
+/* C[m][n] = sum_b sa[b][m] * sb * sum_{k in block b} a[m][k] * bq[n][k], fp32 accumulation.
+ *   a   e4m3 [M, K], row stride lda;  sa fp32 [ceil(K/128), M], row stride ld_sa
+ *   b   e4m3 [N, K], row stride ldb;  b_scale 1: sb fp32 [ceil(N/128), ceil(K/128)] (128 x 128
+ *       blocks, row stride ld_sb); b_scale 0: sb fp32 [ceil(K/128), N] (1 x 128 blocks, ld_sb)
+ *   c   [M, N] of c_dtype (BF16 or FP32), row stride ldc
+ * a, b 16-byte aligned with lda, ldb multiples of 16; sa (and sb for b_scale 0) 16-byte aligned
+ * with ld_sa (ld_sb) a multiple of 4; sb 4-byte aligned otherwise. M, N < 2^31 - 256, K < 2^31 -
+ * 256. A linear layer y = x w^T is (q_row of x) x (q of w); its input gradient (q_row of dy) x
+ * (qt of w); its weight gradient (q_col of dy) x (q_col of x).
+ *   err device int32 or NULL: MOE_DEVERR_TIMEOUT if a bounded wait inside gave up (sticky) */
+moe_status_t fp8_block_gemm(const uint8_t *a, int64_t lda, const float *sa, int64_t ld_sa,
+                            const uint8_t *b, int64_t ldb, const float *sb, int64_t ld_sb,
+                            int32_t b_scale, void *c, int64_t ldc, int32_t c_dtype, int64_t M,
+                            int64_t N, int64_t K, int32_t *err, moe_stream_t stream);
+
 /* Enqueue a copy of the device error word into *host_code (pinned or pageable host int);
  * the value is valid once the stream has been synchronised. */
 moe_status_t moe_get_error(const moe_layer_desc_t *desc, const void *ws, int32_t *host_code,
@@ -417,7 +544,16 @@ typedef enum {
   MOE_K_NVFP4_AMAX = 16,
   MOE_K_NVFP4_QUANTIZE = 17,
   MOE_K_ROUTE_EXPORT = 18,
-  MOE_K_COUNT = 19
+  MOE_K_ROUTER_LOSS = 19,
+  MOE_K_ROUTER_GRAD = 20,
+  MOE_K_LAYERNORM_FWD = 21,
+  MOE_K_LAYERNORM_BWD = 22,
+  MOE_K_LAYERNORM_REDUCE = 23,
+  MOE_K_GRAD_NORM = 24,
+  MOE_K_GRAD_SCALE = 25,
+  MOE_K_FP8_QUANTIZE = 26,
+  MOE_K_FP8_GEMM = 27,
+  MOE_K_COUNT = 28
 } moe_kernel_id_t;
 
 /* Launch timeline, for measurement. Between moe_timeline_begin and moe_timeline_end the
