@@ -10,7 +10,7 @@
 //
 // One CTA: warp 0 loads (TMA, K-major 128-byte-swizzled boxes of 128 bytes; the 1 x 128 scales of
 // a k-block as one row of their [k-block, row] matrix), warp 1 issues the MMAs (128 x BN x 32,
-// kind::f8f6f4), warps 2-9 hold the 128 x BN fp32 sums (warp w: TMEM lanes 32 (w % 4).., half of
+// kind::f8f6f4), warps 4-11 hold the 128 x BN fp32 sums (warp w: TMEM lanes 32 (w % 4).., half of
 // the columns). P is the operand on the 128-row side, Q the one on the BN-column side.
 //   Many rows: P = a, Q = b, tiles of 128 x 256; a result row is contiguous in a thread.
 //   Few rows (M <= 128): P = b, Q = a (BN = M rounded up), so that the whole 128-row side is
@@ -26,17 +26,15 @@ namespace {
 constexpr int BM = 128;
 constexpr int BK = 128;              // E4M3 elements (bytes) per k-block
 constexpr int MMA_K = 32;
-constexpr int kEpiWarps = 8;
-constexpr int kThreads = 64 + 32 * kEpiWarps;
+constexpr int kLeadWarps = 4;        // a warpgroup of its own: load, MMA, two idle
 constexpr int kMaxStages = 8;
-constexpr int kMaxSlots = 12;
 constexpr int kMaxSplit = 8;
 
 struct Fp8Args {
   CUtensorMap tmP, tmQ;    // codes [rows, K]
   CUtensorMap tmSP, tmSQ;  // 1 x 128 scales [k-blocks, rows] (those that are vectors)
   const float* sp;         // 128 x 128 scales of P, [ceil(rows/128), k-blocks] (sp_vec = 0)
-  const float* sq;         // the same of Q (QV = 0)
+  const float* sq;         // 128 x 128 scales of Q (QV = 0)
   int64_t ld_sp, ld_sq;
   int sp_vec;
   int swapped;             // P = b, Q = a: C[q][p]
@@ -58,21 +56,36 @@ struct Smem {
   static constexpr int STAGES = BN >= 256 ? 4 : BN >= 128 ? 6 : 8;
   static constexpr int BUFS = BN >= 256 ? 2 : 4;       // TMEM accumulators
   static constexpr int TMEM_COLS = BUFS * BN;          // 64 .. 512, a power of two
-  static constexpr int SLOTS = STAGES + BUFS;          // scale rows in flight
+  // Scale rows in flight. They are counted on the stage's barrier and have none of their own:
+  // a stage is refilled for k-block n once the MMAs of n - STAGES are done, which were issued
+  // after every epilogue warp had freed the buffer of n - STAGES - BUFS, hence was done with the
+  // scales of the k-block before that.
+  static constexpr int SLOTS = STAGES + BUFS + 1;
   static constexpr int SP_BYTES = BM * 4;
   static constexpr int SQ_BYTES = BN * 4 < 128 ? 128 : BN * 4;
   static constexpr int SLOT = SP_BYTES + SQ_BYTES;
+  // Epilogue warps, and the registers of a thread: launched with 168 (384 threads of them fit an
+  // SM), the lead warpgroup keeps 56 and each of the two epilogue warpgroups takes 224, for 128
+  // sums and two TMEM loads of 32 columns in flight. Sixteen warps of 64 columns measured 5%
+  // slower (8192 x 4096 x 14336: 343 us against 325), single loads of 64 columns the same (327).
+  static constexpr int EW = 8;
+  static constexpr int THREADS = 32 * (kLeadWarps + EW);
+  static constexpr int LAUNCH_REGS = 65536 / THREADS / 8 * 8;
+  static constexpr int LEAD_REGS = 56, EPI_REGS = 224;
+  static_assert(32 * (kLeadWarps * LEAD_REGS + EW * EPI_REGS) <= THREADS * LAUNCH_REGS,
+                "register split");
+  static constexpr int GROUPS = EW / 4;                // column groups of a tile
+  static constexpr int CW = BN / GROUPS;               // columns a warp holds
   static constexpr int SLOT_OFF = STAGES * STAGE;
   static constexpr int CTRL_OFF = SLOT_OFF + SLOTS * SLOT;
   static constexpr int TOTAL = CTRL_OFF + 512 + 1024;
   static_assert(TOTAL <= 232448, "shared memory above the per-block limit");
-  static_assert(STAGES <= kMaxStages && SLOTS <= kMaxSlots, "control block");
+  static_assert(STAGES <= kMaxStages, "control block");
   static_assert(STAGES * STAGE >= BM * BN * 4, "the split sums fit in the stages");
 };
 
 struct Ctrl {
   uint64_t full[kMaxStages], empty[kMaxStages];
-  uint64_t sfull[kMaxSlots], sempty[kMaxSlots];
   uint64_t tfull[4], tempty[4];
   uint64_t drain;
   uint32_t tmem_base;
@@ -95,24 +108,22 @@ constexpr uint32_t idesc_f8(int M, int N) {
   return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
-// Two fp32 lanes at a time: acc += {lo, hi} * f, and a * b.
-MOE_DEVICE void fma2(uint64_t& acc, uint32_t lo, uint32_t hi, uint64_t f) {
-  asm("{\n\t.reg .b64 t;\n\tmov.b64 t, {%1, %2};\n\tfma.rn.f32x2 %0, t, %3, %0;\n\t}"
-      : "+l"(acc)
-      : "r"(lo), "r"(hi), "l"(f));
+// True in one lane of a converged warp, the same one every time.
+MOE_DEVICE bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
 }
-MOE_DEVICE uint64_t mul2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
+
+// Waits for this thread's TMEM loads; naming the registers keeps their uses behind the wait.
+template <int W>
+MOE_DEVICE void tmem_wait(uint32_t (&r)[W]) {
+  tmem_ld_wait();
+#pragma unroll
+  for (int i = 0; i < W; ++i) asm volatile("" : "+r"(r[i]));
 }
-MOE_DEVICE uint64_t pack2(float lo, float hi) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-  return r;
-}
-MOE_DEVICE float lo_of(uint64_t v) { return __uint_as_float((uint32_t)v); }
-MOE_DEVICE float hi_of(uint64_t v) { return __uint_as_float((uint32_t)(v >> 32)); }
 
 // W consecutive TMEM columns of this warp's 32 lanes.
 template <int W>
@@ -128,7 +139,7 @@ MOE_DEVICE float ld_shared_cluster(uint32_t addr) {
   return v;
 }
 
-// n (a multiple of 8, at most 32 here per step) consecutive results of one row.
+// W consecutive results of one row.
 template <int W>
 MOE_DEVICE void store_row(const Fp8Args& p, int64_t row, int col, const float (&v)[W]) {
   if (p.c_fp32) {
@@ -180,13 +191,24 @@ MOE_DEVICE void store_swapped(const Fp8Args& p, int prow, int64_t qrow, float v)
   else static_cast<__nv_bfloat16*>(p.c)[qrow * p.ldc + prow] = __float2bfloat16_rn(v);
 }
 
+// First row of P and of Q of a tile. Tiles are dealt in bands of kBand P tiles, Q tile by Q tile,
+// so that the tiles in flight together read about as many rows of one side as of the other.
+constexpr int kBand = 16;
+template <int BN>
+MOE_DEVICE void tile_at(const Fp8Args& p, int tile, int& p0, int& q0) {
+  const int per = kBand * p.tiles_q, band = tile / per, in = tile - band * per;
+  const int rows = min(kBand, p.tiles_p - band * kBand);
+  p0 = (band * kBand + in % rows) * BM;
+  q0 = (in / rows) * BN;
+}
+
 template <int BN, bool QV>
-__global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_constant__ Fp8Args p) {
+__global__ void __launch_bounds__(Smem<BN>::THREADS, 1)
+    fp8_gemm_kernel(const __grid_constant__ Fp8Args p) {
   MOE_GRIDDEP_ENTRY();
   using L = Smem<BN>;
   constexpr int STAGES = L::STAGES, BUFS = L::BUFS, SLOTS = L::SLOTS;
-  constexpr int CW = BN / 2;                  // columns a warp holds
-  constexpr int CH = CW < 32 ? CW : 32;       // columns a TMEM load
+  constexpr int CW = L::CW, CH = CW < 32 ? CW : 32;  // columns a warp holds, a TMEM load takes
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_addr = smem_u32(smem_raw);
   uint8_t* smem = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
@@ -205,13 +227,9 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
       mbar_init(&c.full[s], 1);
       mbar_init(&c.empty[s], 1);
     }
-    for (int s = 0; s < SLOTS; ++s) {
-      mbar_init(&c.sfull[s], 1);
-      mbar_init(&c.sempty[s], kEpiWarps);
-    }
     for (int s = 0; s < BUFS; ++s) {
-      mbar_init(&c.tfull[s], 1);
-      mbar_init(&c.tempty[s], kEpiWarps);
+      mbar_init(&c.tfull[s], 2);  // the MMAs, and the thread that saw the stage's scales land
+      mbar_init(&c.tempty[s], L::EW);
     }
     mbar_init(&c.drain, 1);
     fence_mbar_init();
@@ -230,84 +248,90 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
   tc_fence_after();
   const uint32_t tmem_base = c.tmem_base;
 
-  if (warp == 0) {
-    // ------------------------------------------------------------ TMA producer
-    if (lane == 0) {
-      const uint32_t slot_tx = (p.sp_vec ? L::SP_BYTES : 0) + (QV ? BN * 4 : 0);
-      int stage = 0, slot = 0;
-      uint32_t phase = 0, sphase = 0;
-      int64_t n_full = 0, n_slot = 0;  // loads armed so far
-      bool ok = true;
-      for (int tile = tile0; ok && tile < total; tile += tstep) {
-        const int p0 = (tile % p.tiles_p) * BM, q0 = (tile / p.tiles_p) * BN;
-        for (int kb = kb0; kb < kb1; ++kb) {
-          if (!mbar_wait(&c.empty[stage], phase ^ 1, abort, p.err)) {
-            ok = false;
-            break;
-          }
-          uint8_t* sP = smem + stage * L::STAGE;
-          mbar_arrive_expect_tx(&c.full[stage], L::STAGE);
-          ++n_full;
-          tma_load_2d(sP, &p.tmP, &c.full[stage], kb * BK, p0);
-          tma_load_2d(sP + L::P_BYTES, &p.tmQ, &c.full[stage], kb * BK, q0);
-          if (++stage == STAGES) {
-            stage = 0;
-            phase ^= 1;
-          }
-          if (slot_tx) {
-            if (!mbar_wait(&c.sempty[slot], sphase ^ 1, abort, p.err)) {
+  if (warp < kLeadWarps) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(L::LEAD_REGS));
+    if (warp == 0) {
+      // ------------------------------------------------------------ TMA producer
+      if (lane == 0) {
+        const uint32_t tx = L::STAGE + (p.sp_vec ? L::SP_BYTES : 0) + (QV ? BN * 4 : 0);
+        int stage = 0, slot = 0;
+        uint32_t phase = 0;
+        int64_t loaded = 0;  // k-blocks
+        bool ok = true;
+        for (int tile = tile0; ok && tile < total; tile += tstep) {
+          int p0, q0;
+          tile_at<BN>(p, tile, p0, q0);
+          for (int kb = kb0; kb < kb1; ++kb) {
+            if (!mbar_wait(&c.empty[stage], phase ^ 1, abort, p.err)) {
               ok = false;
               break;
             }
-            uint8_t* s = smem + L::SLOT_OFF + slot * L::SLOT;
-            mbar_arrive_expect_tx(&c.sfull[slot], slot_tx);
-            ++n_slot;
-            if (p.sp_vec) tma_load_2d(s, &p.tmSP, &c.sfull[slot], p0, kb);
-            if (QV) tma_load_2d(s + L::SP_BYTES, &p.tmSQ, &c.sfull[slot], q0, kb);
-            if (++slot == SLOTS) {
-              slot = 0;
-              sphase ^= 1;
+            uint8_t* sP = smem + stage * L::STAGE;
+            uint8_t* sl = smem + L::SLOT_OFF + slot * L::SLOT;
+            uint64_t* bar = &c.full[stage];
+            mbar_arrive_expect_tx(bar, tx);
+            ++loaded;
+            tma_load_2d(sP, &p.tmP, bar, kb * BK, p0);
+            tma_load_2d(sP + L::P_BYTES, &p.tmQ, bar, kb * BK, q0);
+            if (p.sp_vec) tma_load_2d(sl, &p.tmSP, bar, p0, kb);
+            if (QV) tma_load_2d(sl + L::SP_BYTES, &p.tmSQ, bar, q0, kb);
+            if (++stage == STAGES) {
+              stage = 0;
+              phase ^= 1;
             }
+            if (++slot == SLOTS) slot = 0;
           }
         }
+        // every load this thread issued lands before the CTA can exit: the last phase armed on
+        // each barrier (load i of the ring sits at i % STAGES with parity (i / STAGES) & 1)
+        const uint64_t t0 = globaltimer_ns();
+        for (int64_t i = loaded > STAGES ? loaded - STAGES : 0; i < loaded; ++i)
+          while (!mbar_try_wait(smem_u32(&c.full[i % STAGES]), (uint32_t)((i / STAGES) & 1)) &&
+                 globaltimer_ns() - t0 < kWaitLimitNs) {
+          }
       }
-      // every load this thread issued lands before the CTA can exit: the last phase armed on
-      // each barrier (load i of a ring of R sits at i % R with parity (i / R) & 1)
-      const uint64_t t0 = globaltimer_ns();
-      for (int64_t i = n_full > STAGES ? n_full - STAGES : 0; i < n_full; ++i)
-        while (!mbar_try_wait(smem_u32(&c.full[i % STAGES]), (uint32_t)((i / STAGES) & 1)) &&
-               globaltimer_ns() - t0 < kWaitLimitNs) {
-        }
-      for (int64_t i = n_slot > SLOTS ? n_slot - SLOTS : 0; i < n_slot; ++i)
-        while (!mbar_try_wait(smem_u32(&c.sfull[i % SLOTS]), (uint32_t)((i / SLOTS) & 1)) &&
-               globaltimer_ns() - t0 < kWaitLimitNs) {
-        }
-    }
-    __syncwarp();
-  } else if (warp == 1) {
-    // ------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
+      __syncwarp();
+    } else if (warp == 1) {
+      // ------------------------------------------------------------ MMA issuer
+      // The warp stays together and one elected lane issues: addresses and descriptors are then
+      // the same in every lane, which the MMAs' uniform operands need.
+      const uint32_t tmem_u = __shfl_sync(0xFFFFFFFFu, tmem_base, 0);
+      const uint64_t desc_p = smem_desc_sw128(smem_u32(smem), 16, 1024);
+      const int kb_short = p.K % BK ? nkb_all - 1 : -1;
       int stage = 0, buf = 0;
       uint32_t phase = 0, tphase = 0;
       bool ok = true, issued = false;
       for (int tile = tile0; ok && tile < total; tile += tstep) {
         for (int kb = kb0; kb < kb1; ++kb) {
-          if (!mbar_wait(&c.tempty[buf], tphase ^ 1, abort, p.err) ||
-              !mbar_wait(&c.full[stage], phase, abort, p.err)) {
+          const bool got = mbar_wait(&c.tempty[buf], tphase ^ 1, abort, p.err) &&
+                           mbar_wait(&c.full[stage], phase, abort, p.err);
+          if (!__all_sync(0xFFFFFFFFu, got)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t sP = smem_u32(smem + stage * L::STAGE);
-          const uint32_t sQ = sP + L::P_BYTES;
-          const int rem = p.K - kb * BK;
-          const int nsub = rem >= BK ? BK / MMA_K : (rem + MMA_K - 1) / MMA_K;
-          for (int ks = 0; ks < nsub; ++ks)
-            mma_f8_ss(tmem_base + buf * BN, smem_desc_sw128(sP + ks * MMA_K, 16, 1024),
-                      smem_desc_sw128(sQ + ks * MMA_K, 16, 1024), idesc_f8(BM, BN), ks != 0);
+          const uint64_t dp = desc_p + (uint32_t)(stage * (L::STAGE >> 4));
+          const uint64_t dq = dp + (L::P_BYTES >> 4);
+          const uint32_t d = tmem_u + buf * BN;
+          if (elect_one()) {
+            if (kb != kb_short) {
+#pragma unroll
+              for (int ks = 0; ks < BK / MMA_K; ++ks)
+                mma_f8_ss(d, dp + ks * (MMA_K >> 4), dq + ks * (MMA_K >> 4), idesc_f8(BM, BN),
+                          ks != 0);
+            } else {
+              const int nsub = (p.K - kb * BK + MMA_K - 1) / MMA_K;
+#pragma unroll 1
+              for (int ks = 0; ks < nsub; ++ks)
+                mma_f8_ss(d, dp + ks * (MMA_K >> 4), dq + ks * (MMA_K >> 4), idesc_f8(BM, BN),
+                          ks != 0);
+            }
+            mma_commit(&c.empty[stage]);
+            mma_commit(&c.tfull[buf]);
+            mbar_arrive(&c.tfull[buf]);
+          }
+          __syncwarp();
           issued = true;
-          mma_commit(&c.empty[stage]);
-          mma_commit(&c.tfull[buf]);
           if (++stage == STAGES) {
             stage = 0;
             phase ^= 1;
@@ -319,156 +343,177 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
         }
       }
       if (issued) {
-        mma_commit(&c.drain);
+        if (elect_one()) mma_commit(&c.drain);
+        __syncwarp();
         const uint64_t t0 = globaltimer_ns();
         while (!mbar_try_wait(smem_u32(&c.drain), 0) && globaltimer_ns() - t0 < kWaitLimitNs) {
         }
       }
+      __syncwarp();
     }
-    __syncwarp();
+    if (p.split > 1) {  // the epilogue warps' two cluster barriers
+      cluster_sync_all();
+      cluster_sync_all();
+    }
   } else {
     // ------------------------------------------------------------ epilogue warps
-    const int q = warp & 3, half = (warp - 2) >> 2;
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(L::EPI_REGS));
+    const int q = warp & 3, c0 = ((warp - kLeadWarps) >> 2) * CW;  // lanes, first column
     const int row = q * 32 + lane;  // of the tile's P side
-    const bool slots = p.sp_vec || QV;
+    constexpr int NC = CW / CH;     // TMEM loads a k-block
+    const uint32_t tacc = tmem_base + c0 + ((uint32_t)(q * 32) << 16);
     int buf = 0, slot = 0;
-    uint32_t tphase = 0, sphase = 0;
-    bool ok = true;
+    uint32_t tphase = 0;
+    uint32_t r[2][CH];
+    auto free_buffer = [&]() {  // its sums and scales have been read
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&c.tempty[buf]);
+      if (++buf == BUFS) {
+        buf = 0;
+        tphase ^= 1;
+      }
+    };
+    // Waits for the next k-block and starts its first load. A wait that gives up has raised the
+    // abort flag and the error word; the warps go on through their loops with undefined sums
+    // (every later wait then returns at once), so no branch depends on it.
+    auto next_block = [&]() {
+      mbar_wait(&c.tfull[buf], tphase, abort, p.err);
+      __syncwarp();
+      tc_fence_after();
+      tmem_ld(tacc + buf * BN, r[0]);
+    };
     for (int tile = tile0; tile < total; tile += tstep) {
       __syncwarp();  // rows past the end left the last tile early
-      const int p0 = (tile % p.tiles_p) * BM, q0 = (tile / p.tiles_p) * BN;
-      uint64_t acc[CW / 2];
+      int p0, q0;
+      tile_at<BN>(p, tile, p0, q0);
+      // Scales that are one number a k-block for these rows and columns (P's blocks when it has
+      // no vector, times Q's): lane l holds that of k-block base + l. A column group past the
+      // last column reads the last block's and stores nothing.
+      const float* sp_at = p.sp_vec ? nullptr : p.sp + (int64_t)(p0 >> 7) * p.ld_sp;
+      const float* sq_at =
+          QV ? nullptr : p.sq + (int64_t)(min(q0 + c0, p.rows_q - 1) >> 7) * p.ld_sq;
+      auto block_scales = [&](int base) {
+        const int kb = min(base + lane, kb1 - 1);
+        return (sp_at ? __ldg(sp_at + kb) : 1.0f) * (sq_at ? __ldg(sq_at + kb) : 1.0f);
+      };
+      float bs = block_scales(kb0);
+      float acc[CW];
 #pragma unroll
-      for (int i = 0; i < CW / 2; ++i) acc[i] = 0;
-      // 128 x 128 scales: one number a k-block for the whole tile side (a column half of a
-      // 256-wide tile); a half past the last column reads the last block's and is never stored
-      const float* spb = p.sp + (int64_t)(p0 >> 7) * p.ld_sp;
-      const int qb = min((q0 + half * CW) >> 7, (p.rows_q - 1) >> 7);
-      const float* sqb = QV ? nullptr : p.sq + (int64_t)qb * p.ld_sq;
-      float sp_next = p.sp_vec ? 0.f : __ldg(spb + kb0);
-      float sq_next = QV ? 0.f : __ldg(sqb + kb0);
+      for (int i = 0; i < CW; ++i) acc[i] = 0.f;
+      next_block();
       for (int kb = kb0; kb < kb1; ++kb) {
-        float sp = sp_next, sq = sq_next;
-        if (kb + 1 < kb1) {
-          if (!p.sp_vec) sp_next = __ldg(spb + kb + 1);
-          if (!QV) sq_next = __ldg(sqb + kb + 1);
-        }
-        const uint8_t* sl = smem + L::SLOT_OFF + slot * L::SLOT;
-        // every give-up decision is warp-uniform (full-warp TMEM loads)
-        bool got = true;
-        if (slots) got = mbar_wait(&c.sfull[slot], sphase, abort, p.err);
-        got = got && mbar_wait(&c.tfull[buf], tphase, abort, p.err);
-        if (!__all_sync(0xFFFFFFFFu, got)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        if (p.sp_vec) sp = reinterpret_cast<const float*>(sl)[row];
-        const float* sqv = reinterpret_cast<const float*>(sl + L::SP_BYTES) + half * CW;
-        const uint32_t taddr = tmem_base + buf * BN + half * CW + ((uint32_t)(q * 32) << 16);
-        const uint64_t f = QV ? pack2(sp, sp) : pack2(sp * sq, sp * sq);
+        const int at = (kb - kb0) & 31;
+        if (at == 0 && kb > kb0) bs = block_scales(kb);
+        float f = __shfl_sync(0xFFFFFFFFu, bs, at);
+        const float* sl = reinterpret_cast<const float*>(smem + L::SLOT_OFF + slot * L::SLOT);
+        if (p.sp_vec) f *= sl[row];
+        const float* sqv = sl + L::SP_BYTES / 4 + c0;
+        if (++slot == SLOTS) slot = 0;
 #pragma unroll
-        for (int j = 0; j < CW / CH; ++j) {
-          uint32_t r[CH];
-          tmem_ld(taddr + j * CH, r);
-          tmem_ld_wait();
-#pragma unroll
-          for (int i = 0; i < CH / 2; ++i) {
-            uint64_t g = f;
-            if (QV) g = mul2(f, *reinterpret_cast<const uint64_t*>(sqv + j * CH + 2 * i));
-            fma2(acc[j * (CH / 2) + i], r[2 * i], r[2 * i + 1], g);
+        for (int j = 0; j < NC; ++j) {
+          tmem_wait(r[j & 1]);
+          if (j + 1 < NC) {
+            tmem_ld(tacc + buf * BN + (j + 1) * CH, r[(j + 1) & 1]);
+          } else {
+            free_buffer();
+            // the next k-block's first load, before this one's last columns are added (an odd
+            // number of loads a k-block would put it into the registers being added)
+            if (NC % 2 == 0 && kb + 1 < kb1) next_block();
           }
-        }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&c.tempty[buf]);
-          if (slots) mbar_arrive(&c.sempty[slot]);
-        }
-        if (++buf == BUFS) {
-          buf = 0;
-          tphase ^= 1;
-        }
-        if (slots && ++slot == SLOTS) {
-          slot = 0;
-          sphase ^= 1;
+#pragma unroll
+          for (int i = 0; i < CH; i += 4) {
+            float2 g0 = make_float2(f, f), g1 = g0;
+            if (QV) {
+              const float4 s4 = *reinterpret_cast<const float4*>(sqv + j * CH + i);
+              g0 = __fmul2_rn(g0, make_float2(s4.x, s4.y));
+              g1 = __fmul2_rn(g1, make_float2(s4.z, s4.w));
+            }
+            float* o = &acc[j * CH + i];
+            const uint32_t* x = &r[j & 1][i];
+            const float2 a0 = __ffma2_rn(make_float2(__uint_as_float(x[0]), __uint_as_float(x[1])),
+                                         g0, make_float2(o[0], o[1]));
+            const float2 a1 = __ffma2_rn(make_float2(__uint_as_float(x[2]), __uint_as_float(x[3])),
+                                         g1, make_float2(o[2], o[3]));
+            o[0] = a0.x;
+            o[1] = a0.y;
+            o[2] = a1.x;
+            o[3] = a1.y;
+          }
+          if (NC % 2 == 1 && j + 1 == NC && kb + 1 < kb1) next_block();
         }
       }
-      if (!ok) break;
       if (p.split > 1) {
         // this CTA's sums, column by column, where the stages were (every load has been used)
-        float* st = reinterpret_cast<float*>(smem) + half * CW * BM + row;
+        float* st = reinterpret_cast<float*>(smem) + c0 * BM + row;
 #pragma unroll
-        for (int i = 0; i < CW / 2; ++i) {
-          st[(2 * i) * BM] = lo_of(acc[i]);
-          st[(2 * i + 1) * BM] = hi_of(acc[i]);
-        }
+        for (int i = 0; i < CW; ++i) st[i * BM] = acc[i];
         break;  // one tile a cluster
       }
       if (p0 + row >= p.rows_p) continue;
       if (p.swapped) {
 #pragma unroll
         for (int i = 0; i < CW; ++i) {
-          const int64_t qr = q0 + half * CW + i;
+          const int64_t qr = q0 + c0 + i;
           if (qr < p.rows_q)
-            store_swapped(p, p0 + row, qr, i & 1 ? hi_of(acc[i / 2]) : lo_of(acc[i / 2]));
+            store_swapped(p, p0 + row, qr, acc[i]);
         }
       } else {
 #pragma unroll
         for (int j = 0; j < CW / CH; ++j) {
-          const int col = q0 + half * CW + j * CH;
+          const int col = q0 + c0 + j * CH;
           if (col >= p.rows_q) break;
           float v[CH];
 #pragma unroll
-          for (int i = 0; i < CH / 2; ++i) {
-            v[2 * i] = lo_of(acc[j * (CH / 2) + i]);
-            v[2 * i + 1] = hi_of(acc[j * (CH / 2) + i]);
-          }
+          for (int i = 0; i < CH; ++i) v[i] = acc[j * CH + i];
           store_row<CH>(p, p0 + row, col, v);
         }
       }
     }
-  }
-
-  if (p.split > 1) {
-    // rank r adds columns [r BN / split, (r + 1) BN / split) of every CTA of the cluster, in the
-    // order of the ranks, and stores them
-    __syncthreads();
-    cluster_sync_all();
-    if (warp >= 2 && !*abort) {
-      const int tid = threadIdx.x - 64;
-      const int row = tid & 127, cg = tid >> 7;
-      const int p0 = (tile0 % p.tiles_p) * BM, q0 = (tile0 / p.tiles_p) * BN;
-      const int per = BN / p.split, c_lo = rank * per + cg * (per / 2);
-      const uint32_t base = smem_u32(smem) + (uint32_t)row * 4;
-      uint32_t peer[kMaxSplit];
+    if (p.split > 1) {
+      // rank r adds columns [r BN / split, (r + 1) BN / split) of every CTA of the cluster, in the
+      // order of the ranks, and stores them
+      __syncwarp();
+      cluster_sync_all();
+      if (!*abort) {
+        const int tid = threadIdx.x - 32 * kLeadWarps;
+        const int row = tid & 127, cg = tid >> 7;  // this thread's row, half of the columns
+        int p0, q0;
+        tile_at<BN>(p, tile0, p0, q0);
+        const int per = BN / p.split;
+        const uint32_t base = smem_u32(smem) + (uint32_t)row * 4;
+        uint32_t peer[kMaxSplit];
 #pragma unroll
-      for (int s = 0; s < kMaxSplit; ++s)
-        if (s < p.split) peer[s] = mapa_shared(base, (uint32_t)s);
-      if (p0 + row < p.rows_p) {
-        for (int i = c_lo; i < c_lo + per / 2; ++i) {
-          const int64_t qr = q0 + i;
-          if (qr >= p.rows_q) break;
+        for (int s = 0; s < kMaxSplit; ++s)
+          if (s < p.split) peer[s] = mapa_shared(base, (uint32_t)s);
+        auto sum = [&](int col) {
           float v = 0.f;
 #pragma unroll
           for (int s = 0; s < kMaxSplit; ++s)
-            if (s < p.split) v += ld_shared_cluster(peer[s] + (uint32_t)i * (BM * 4));
+            if (s < p.split) v += ld_shared_cluster(peer[s] + (uint32_t)col * (BM * 4));
+          return v;
+        };
+        if (p0 + row < p.rows_p) {
           if (p.swapped) {
-            store_swapped(p, p0 + row, qr, v);
-          } else if (p.c_fp32) {
-            static_cast<float*>(p.c)[(int64_t)(p0 + row) * p.ldc + qr] = v;
-          } else {
-            static_cast<__nv_bfloat16*>(p.c)[(int64_t)(p0 + row) * p.ldc + qr] =
-                __float2bfloat16_rn(v);
+            const int half = per / 2;
+            for (int i = rank * per + cg * half; i < rank * per + (cg + 1) * half; ++i)
+              if (q0 + i < p.rows_q) store_swapped(p, p0 + row, q0 + i, sum(i));
+          } else {  // 16 columns of a row at a time (per >= 16)
+            for (int i = rank * per + cg * 16; i < (rank + 1) * per && q0 + i < p.rows_q; i += 32) {
+              float v[16];
+#pragma unroll
+              for (int j = 0; j < 16; ++j) v[j] = sum(i + j);
+              store_row<16>(p, p0 + row, q0 + i, v);
+            }
           }
         }
+        __syncwarp();
       }
-      __syncwarp();
+      // no CTA leaves while another may read its sums
+      cluster_sync_all();
     }
-    // no CTA leaves while another may read its sums
-    __syncthreads();
-    cluster_sync_all();
   }
+
   griddep_launch_dependents();
   tc_fence_before();
   __syncthreads();
@@ -513,6 +558,12 @@ cudaError_t launch_gemm(Fp8Args& a, const Operand& P, const Operand& Q, cudaStre
       (QV && !tmap_scales(&a.tmSQ, Q.s, Q.rows, kb, Q.ld_s, BN)))
     return cudaErrorInvalidValue;
   auto kern = fp8_gemm_kernel<BN, QV>;
+  // the register split waits for registers that the launch must have: checked once
+  static const int regs = [&] {
+    cudaFuncAttributes at;
+    return cudaFuncGetAttributes(&at, kern) == cudaSuccess ? at.numRegs : 0;
+  }();
+  if (regs < Smem<BN>::LAUNCH_REGS) return cudaErrorInvalidConfiguration;
   cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kern), Smem<BN>::TOTAL);
   if (e != cudaSuccess) return e;
   const int tiles = a.tiles_p * a.tiles_q;
@@ -523,7 +574,7 @@ cudaError_t launch_gemm(Fp8Args& a, const Operand& P, const Operand& Q, cudaStre
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   const int grid = a.split > 1 ? tiles * a.split : std::min(tiles, sms);
-  e = launch_kernel(kern, dim3((unsigned)grid), dim3(kThreads), Smem<BN>::TOTAL, s, attr,
+  e = launch_kernel(kern, dim3((unsigned)grid), dim3(Smem<BN>::THREADS), Smem<BN>::TOTAL, s, attr,
                     a.split > 1 ? 1 : 0, a);
   count_launch(s, MOE_K_FP8_GEMM);
   return e;
@@ -545,7 +596,8 @@ Plan choose(int64_t rows_p, int64_t rows_q, int64_t nkb, bool swapped, int sms) 
   for (int i = swapped ? 0 : 2; i < 5; ++i) {
     const int64_t tiles = tp * ((rows_q + widths[i] - 1) / widths[i]);
     for (int split = 1; split <= kMaxSplit; split *= 2) {
-      if (split > 1 && (tiles * split > sms || split > nkb)) break;
+      if (split > 1 && (tiles * split > sms || split > nkb || (!swapped && widths[i] / split < 16)))
+        break;
       const int64_t waves = split > 1 ? 1 : (tiles + sms - 1) / sms;
       const int64_t t =
           waves * ((nkb + split - 1) / split * kb_cycles[i] + 2000) + (split > 1 ? 1500 : 0);
