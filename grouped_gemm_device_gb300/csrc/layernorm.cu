@@ -7,13 +7,17 @@
 // Bound by HBM: the forward reads and writes M N elements once, the backward reads x and dy and
 // writes dx once. A row stays in registers between its statistics and its use, so the variance is
 // taken about the mean (two passes over registers, not E[x^2] - mean^2). Statistics, sums and the
-// weight-gradient partials are fp32.
+// weight-gradient partials are fp32. Widening bf16 runs at half the rate of the products, so it is
+// done once a value where the registers allow.
 #include "kernels.cuh"
 
 namespace moe {
 namespace {
 
-constexpr int kMaxParts = 160;  // backward blocks at most: rows of the partial weight gradients
+// Backward blocks at most (rows of the partial weight gradients), by the row's length: short rows
+// leave small partials and run more blocks.
+constexpr int64_t kShortRow = 1024;
+int64_t max_parts(int64_t N) { return N <= kShortRow ? 960 : 480; }
 
 template <typename T>
 MOE_DEVICE float to_f(T v) {
@@ -26,16 +30,46 @@ MOE_DEVICE T from_f(float v) {
   else return v;
 }
 
+// VEC consecutive elements as they lie in memory: 16 bytes, or one element (VEC = 1).
+template <typename T, int VEC>
+struct Raw {
+  uint32_t w[VEC == 1 ? 1 : 4];
+  static_assert(VEC == 1 || VEC * sizeof(T) == 16, "one element or 16 bytes");
+};
+template <typename T, int VEC>
+MOE_DEVICE void zero_raw(Raw<T, VEC>& r) {
+#pragma unroll
+  for (uint32_t& w : r.w) w = 0u;
+}
+// Streamed data is not kept in L1, which the weights of the following rows want.
+template <typename T, int VEC>
+MOE_DEVICE void load_raw(const T* p, Raw<T, VEC>& r) {
+  if constexpr (VEC > 1) {
+    asm volatile("ld.global.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r.w[0]), "=r"(r.w[1]), "=r"(r.w[2]), "=r"(r.w[3])
+                 : "l"(p));
+  } else if constexpr (sizeof(T) == 2) {
+    r.w[0] = *reinterpret_cast<const uint16_t*>(p);
+  } else {
+    r.w[0] = __float_as_uint(*p);
+  }
+}
+template <typename T, int VEC>
+MOE_DEVICE float raw_at(const Raw<T, VEC>& r, int j) {  // j is a constant after unrolling
+  if constexpr (sizeof(T) == 4) return __uint_as_float(r.w[j]);
+  else return (j & 1) ? bf16_hi(r.w[j >> 1]) : bf16_lo(r.w[j >> 1]);
+}
+
 // VEC consecutive elements (VEC * sizeof(T) a multiple of 16 bytes, or VEC = 1) as fp32.
 template <typename T, int VEC>
 MOE_DEVICE void load_vec(const T* p, float (&v)[VEC]) {
   if constexpr (VEC == 1) {
-    v[0] = to_f(*p);
+    v[0] = to_f(__ldg(p));
   } else {
     constexpr int W = VEC * sizeof(T) / 16;
 #pragma unroll
     for (int w = 0; w < W; ++w) {
-      const uint4 q = reinterpret_cast<const uint4*>(p)[w];
+      const uint4 q = __ldg(reinterpret_cast<const uint4*>(p) + w);
       const uint32_t u[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -53,98 +87,115 @@ template <typename T, int VEC>
 MOE_DEVICE void store_vec(T* p, const float (&v)[VEC]) {
   if constexpr (VEC == 1) {
     *p = from_f<T>(v[0]);
+  } else if constexpr (sizeof(T) == 2) {
+    *reinterpret_cast<uint4*>(p) =
+        make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                   pack_bf16x2(v[6], v[7]));
   } else {
-    constexpr int W = VEC * sizeof(T) / 16;
-#pragma unroll
-    for (int w = 0; w < W; ++w) {
-      uint4 q;
-      if constexpr (sizeof(T) == 2)
-        q = make_uint4(pack_bf16x2(v[8 * w], v[8 * w + 1]), pack_bf16x2(v[8 * w + 2], v[8 * w + 3]),
-                       pack_bf16x2(v[8 * w + 4], v[8 * w + 5]),
-                       pack_bf16x2(v[8 * w + 6], v[8 * w + 7]));
-      else
-        q = make_uint4(__float_as_uint(v[4 * w]), __float_as_uint(v[4 * w + 1]),
-                       __float_as_uint(v[4 * w + 2]), __float_as_uint(v[4 * w + 3]));
-      reinterpret_cast<uint4*>(p)[w] = q;
-    }
+    *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
   }
 }
 
-// Sums of a and b over the G threads of a row's group (G = 32, or a whole block of G threads;
-// `sm` then holds 2 * 32 floats and may be reused after the next call's first barrier).
-template <int G>
-MOE_DEVICE void row_sum2(float& a, float& b, float* sm) {
+MOE_DEVICE float warp_sum(float a) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    a += __shfl_xor_sync(0xFFFFFFFFu, a, o);
-    b += __shfl_xor_sync(0xFFFFFFFFu, b, o);
+  for (int o = 16; o > 0; o >>= 1) a += __shfl_xor_sync(0xFFFFFFFFu, a, o);
+  return a;
+}
+// Sum over the G threads of a row's group: a warp, or a whole block, whose warps all add the
+// warps' sums in the same order. `sm` must not be in use by a call less than one barrier ago.
+template <int G>
+MOE_DEVICE float row_sum(float a, float (&sm)[32]) {
+  a = warp_sum(a);
+  if constexpr (G > 32) {
+    const int lane = threadIdx.x & 31;
+    if (lane == 0) sm[threadIdx.x >> 5] = a;
+    __syncthreads();
+    if constexpr (G <= 256) {
+      a = sm[0];
+#pragma unroll
+      for (int w = 1; w < G / 32; ++w) a += sm[w];
+    } else {
+      a = warp_sum(lane < G / 32 ? sm[lane] : 0.f);
+    }
   }
+  return a;
+}
+// Two sums at once; a block's calls take turns (0, 1, 0, ..) with the halves of `sm`.
+template <int G>
+MOE_DEVICE void row_sum2(float& a, float& b, float (&sm)[2][2][32], int turn) {
+  a = warp_sum(a);
+  b = warp_sum(b);
   if constexpr (G > 32) {
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-    __syncthreads();
     if (lane == 0) {
-      sm[w] = a;
-      sm[32 + w] = b;
+      sm[turn][0][w] = a;
+      sm[turn][1][w] = b;
     }
     __syncthreads();
-    a = 0.f;
-    b = 0.f;
+    if constexpr (G <= 256) {
+      a = sm[turn][0][0];
+      b = sm[turn][1][0];
 #pragma unroll
-    for (int i = 0; i < G / 32; ++i) {
-      a += sm[i];
-      b += sm[32 + i];
+      for (int i = 1; i < G / 32; ++i) {
+        a += sm[turn][0][i];
+        b += sm[turn][1][i];
+      }
+    } else {
+      a = warp_sum(lane < G / 32 ? sm[turn][0][lane] : 0.f);
+      b = warp_sum(lane < G / 32 ? sm[turn][1][lane] : 0.f);
     }
   }
 }
 
-// G threads a row, PER vectors of VEC elements a thread: N <= G * PER * VEC.
-template <typename XT, typename WT, int VEC, int G, int PER>
+// G threads (a warp of four in a block, or a whole block) take RP rows, PER vectors of VEC elements
+// a thread and row: N <= G * PER * VEC. Two rows share each load of the weights.
+template <typename XT, typename WT, int VEC, int G, int PER, int RP>
 __global__ void __launch_bounds__(G < 128 ? 128 : G) ln_fwd_kernel(
-    const XT* __restrict__ x, int64_t ldx, const WT* __restrict__ gamma,
-    const WT* __restrict__ beta, XT* __restrict__ y, int64_t ldy, float* __restrict__ mean_out,
-    float* __restrict__ rstd_out, int64_t M, int N, float eps) {
+    const XT* x, int64_t ldx, const WT* __restrict__ gamma, const WT* __restrict__ beta, XT* y,
+    int64_t ldy, float* __restrict__ mean_out, float* __restrict__ rstd_out, int64_t M, int N,
+    float eps) {
   MOE_GRIDDEP_ENTRY();
-  __shared__ float sm[64];
-  constexpr int R = (G < 128 ? 128 : G) / G;  // rows a block
+  __shared__ float sm[2][RP][32];
+  constexpr int R = (G < 128 ? 128 : G) / G;  // groups a block
   const int t = threadIdx.x % G;
-  const int64_t row = (int64_t)blockIdx.x * R + threadIdx.x / G;
-  if (G == 32 && row >= M) return;  // a block's rows are its warps; otherwise R = 1
-  const XT* xr = x + row * ldx;
-  float v[PER][VEC];
-  float s = 0.f, unused = 0.f;
+  const int64_t row0 = ((int64_t)blockIdx.x * R + threadIdx.x / G) * RP;
+  if (G == 32 && row0 >= M) return;  // a block's groups are its warps; otherwise R = 1
+  Raw<XT, VEC> raw[RP][PER];
 #pragma unroll
-  for (int i = 0; i < PER; ++i) {
-    const int c = (i * G + t) * VEC;
-    if (c < N) {
-      load_vec<XT, VEC>(xr + c, v[i]);
-    } else {
+  for (int k = 0; k < RP; ++k)
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) v[i][j] = 0.f;
+    for (int i = 0; i < PER; ++i) {
+      const int c = (i * G + t) * VEC;
+      zero_raw(raw[k][i]);
+      if (c < N && (RP == 1 || row0 + k < M)) load_raw(x + (row0 + k) * ldx + c, raw[k][i]);
     }
-  }
+  float v[RP][PER][VEC], rstd[RP];
 #pragma unroll
-  for (int i = 0; i < PER; ++i)
+  for (int k = 0; k < RP; ++k) {
+    float s = 0.f, q = 0.f;
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) s += v[i][j];
-  row_sum2<G>(s, unused, sm);
-  const float mean = s / (float)N;
-  float q = 0.f;
-#pragma unroll
-  for (int i = 0; i < PER; ++i)
-    if ((i * G + t) * VEC < N) {
+    for (int i = 0; i < PER; ++i)
 #pragma unroll
       for (int j = 0; j < VEC; ++j) {
-        const float d = v[i][j] - mean;
-        q += d * d;
+        v[k][i][j] = raw_at(raw[k][i], j);
+        s += v[k][i][j];
       }
+    const float mean = row_sum<G>(s, sm[0][k]) / (float)N;
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+      if ((i * G + t) * VEC < N) {
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) {
+          v[k][i][j] -= mean;
+          q += v[k][i][j] * v[k][i][j];
+        }
+      }
+    rstd[k] = 1.0f / sqrtf(row_sum<G>(q, sm[1][k]) / (float)N + eps);
+    if (t == 0 && (RP == 1 || row0 + k < M)) {
+      if (mean_out) mean_out[row0 + k] = mean;
+      if (rstd_out) rstd_out[row0 + k] = rstd[k];
     }
-  row_sum2<G>(q, unused, sm);
-  const float rstd = 1.0f / sqrtf(q / (float)N + eps);
-  if (t == 0) {
-    if (mean_out) mean_out[row] = mean;
-    if (rstd_out) rstd_out[row] = rstd;
   }
-  XT* yr = y + row * ldy;
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
     const int c = (i * G + t) * VEC;
@@ -153,11 +204,14 @@ __global__ void __launch_bounds__(G < 128 ? 128 : G) ln_fwd_kernel(
       if (gamma) load_vec<WT, VEC>(gamma + c, gm);
       if (beta) load_vec<WT, VEC>(beta + c, bt);
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) {
-        const float h = (v[i][j] - mean) * rstd;
-        o[j] = (gamma ? h * gm[j] : h) + (beta ? bt[j] : 0.f);
+      for (int k = 0; k < RP; ++k) {
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) {
+          const float h = v[k][i][j] * rstd[k];
+          o[j] = (gamma ? h * gm[j] : h) + (beta ? bt[j] : 0.f);
+        }
+        if (RP == 1 || row0 + k < M) store_vec<XT, VEC>(y + (row0 + k) * ldy + c, o);
       }
-      store_vec<XT, VEC>(yr + c, o);
     }
   }
 }
@@ -169,19 +223,17 @@ __global__ void __launch_bounds__(1024) ln_fwd_long_kernel(
     int64_t ldy, float* __restrict__ mean_out, float* __restrict__ rstd_out, int64_t M, int64_t N,
     float eps) {
   MOE_GRIDDEP_ENTRY();
-  __shared__ float sm[64];
+  __shared__ float sm[2][32];
   for (int64_t row = blockIdx.x; row < M; row += gridDim.x) {
     const XT* xr = x + row * ldx;
-    float s = 0.f, unused = 0.f, q = 0.f;
+    float s = 0.f, q = 0.f;
     for (int64_t c = threadIdx.x; c < N; c += 1024) s += to_f(xr[c]);
-    row_sum2<1024>(s, unused, sm);
-    const float mean = s / (float)N;
+    const float mean = row_sum<1024>(s, sm[0]) / (float)N;
     for (int64_t c = threadIdx.x; c < N; c += 1024) {
       const float d = to_f(xr[c]) - mean;
       q += d * d;
     }
-    row_sum2<1024>(q, unused, sm);
-    const float rstd = 1.0f / sqrtf(q / (float)N + eps);
+    const float rstd = 1.0f / sqrtf(row_sum<1024>(q, sm[1]) / (float)N + eps);
     if (threadIdx.x == 0) {
       if (mean_out) mean_out[row] = mean;
       if (rstd_out) rstd_out[row] = rstd;
@@ -193,70 +245,217 @@ __global__ void __launch_bounds__(1024) ln_fwd_long_kernel(
   }
 }
 
-// One block walks rows blockIdx, blockIdx + grid, ...; a thread owns the same PER * VEC columns
-// of every row and keeps their dgamma and dbeta sums in registers until the end.
-template <typename XT, typename WT, int VEC, int G, int PER>
-__global__ void __launch_bounds__(G) ln_bwd_kernel(
+// Backward. A group of G threads (a warp of eight in a block, or a whole block) walks rows; a
+// thread owns the same PER * VEC columns of every row and keeps their dgamma and dbeta sums in
+// registers until the end. Each thread copies its own columns of the next S - 1 rows into a ring
+// in shared memory (cp.async), so that 64 to 190 KB are on their way on an SM and no barrier is
+// spent on the copies; VEC = 1 (rows off 16-byte boundaries) loads directly.
+template <typename XT, int VEC, int B, int PER, int S>
+constexpr int ring_bytes() {
+  return VEC > 1 ? S * PER * 2 * B * 16 : 0;
+}
+MOE_DEVICE void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
+template <typename XT, typename WT, int VEC, int G, int PER, int S>
+__global__ void __launch_bounds__(G < 256 ? 256 : G) ln_bwd_kernel(
     const XT* dy, int64_t lddy, const XT* x, int64_t ldx, const WT* __restrict__ gamma,
     const float* __restrict__ mean, const float* __restrict__ rstd, XT* dx, int64_t lddx,
-    float* __restrict__ part, int64_t M, int N) {
+    float* __restrict__ part, WT* __restrict__ dgamma, WT* __restrict__ dbeta, int64_t M,
+    int N) {
   MOE_GRIDDEP_ENTRY();
-  __shared__ float sm[64];
-  const int t = threadIdx.x;
+  constexpr int B = G < 256 ? 256 : G, GROUPS = B / G;
+  constexpr bool kRing = VEC > 1;
+  // few enough columns a thread to hold gamma and one row's widened values beside the sums
+  constexpr bool kKeep = PER * VEC <= 16 && G <= 512;
+  __shared__ float sm[2][2][32];
+  extern __shared__ uint4 ring[];  // [S][2 PER][B]
+  const int t = threadIdx.x % G;
+  const int64_t row0 = (int64_t)blockIdx.x * GROUPS + threadIdx.x / G;
+  const int64_t step = (int64_t)gridDim.x * GROUPS;
+  const uint32_t ring0 = smem_u32(ring) + threadIdx.x * 16;
+  auto fetch = [&](int64_t row, int slot) {
+    if (row < M) {
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        const int c = (i * G + t) * VEC;
+        if (c < N) {
+          cp_async16(ring0 + ((slot * 2 * PER + 2 * i) * B) * 16, x + row * ldx + c);
+          cp_async16(ring0 + ((slot * 2 * PER + 2 * i + 1) * B) * 16, dy + row * lddy + c);
+        }
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  auto ring_at = [&](int slot, int i) {
+    const uint4 q = ring[(slot * 2 * PER + i) * B + threadIdx.x];
+    Raw<XT, VEC> r;
+    r.w[0] = q.x;
+    if constexpr (VEC > 1) {
+      r.w[1] = q.y;
+      r.w[2] = q.z;
+      r.w[3] = q.w;
+    }
+    return r;
+  };
   float dg[PER][VEC], db[PER][VEC];
 #pragma unroll
   for (int i = 0; i < PER; ++i)
 #pragma unroll
     for (int j = 0; j < VEC; ++j) dg[i][j] = db[i][j] = 0.f;
-  for (int64_t row = blockIdx.x; row < M; row += gridDim.x) {
-    const float mu = mean[row], rs = rstd[row];
-    float h[PER][VEC], u[PER][VEC];
+  if constexpr (kRing) {
+#pragma unroll
+    for (int k = 0; k < S - 1; ++k) fetch(row0 + k * step, k);
+  }
+  float gm[kKeep ? PER : 1][VEC];
+  if constexpr (kKeep) {
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int c = (i * G + t) * VEC;
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) gm[i][j] = 1.0f;
+      if (gamma && c < N) load_vec<WT, VEC>(gamma + c, gm[i]);
+    }
+  }
+  int slot = 0, turn = 0;
+  float mu = row0 < M ? mean[row0] : 0.f, rs = row0 < M ? rstd[row0] : 0.f;
+  for (int64_t row = row0; row < M; row += step) {
+    Raw<XT, VEC> h[PER], u[PER];
+    if constexpr (kRing) {
+      const int ahead = slot == 0 ? S - 1 : slot - 1;
+      fetch(row + (S - 1) * step, ahead);
+      asm volatile("cp.async.wait_group %0;" ::"n"(S - 1) : "memory");
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        h[i] = ring_at(slot, 2 * i);
+        u[i] = ring_at(slot, 2 * i + 1);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        const int c = (i * G + t) * VEC;
+        if (c < N) {
+          load_raw(x + row * ldx + c, h[i]);
+          load_raw(dy + row * lddy + c, u[i]);
+        }
+      }
+    }
+    const float m0 = mu, r0 = rs;
+    if (row + step < M) {  // the next row's statistics
+      mu = mean[row + step];
+      rs = rstd[row + step];
+    }
+    // c = x - mean; the sums over the row are of u and u c, rstd goes into their factors
+    float c_[kKeep ? PER : 1][VEC], u_[kKeep ? PER : 1][VEC];
     float s1 = 0.f, s2 = 0.f;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
       const int c = (i * G + t) * VEC;
       if (c < N) {
-        float gm[VEC];
-        load_vec<XT, VEC>(x + row * ldx + c, h[i]);
-        load_vec<XT, VEC>(dy + row * lddy + c, u[i]);
-        if (gamma) load_vec<WT, VEC>(gamma + c, gm);
+        float gv[VEC];
+        if (!kKeep && gamma) load_vec<WT, VEC>(gamma + c, gv);
 #pragma unroll
         for (int j = 0; j < VEC; ++j) {
-          h[i][j] = (h[i][j] - mu) * rs;
-          dg[i][j] += u[i][j] * h[i][j];
-          db[i][j] += u[i][j];
-          if (gamma) u[i][j] *= gm[j];
-          s1 += u[i][j];
-          s2 += u[i][j] * h[i][j];
+          const float cj = raw_at(h[i], j) - m0, d = raw_at(u[i], j);
+          dg[i][j] += (d * r0) * cj;
+          db[i][j] += d;
+          const float uj = kKeep ? d * gm[kKeep ? i : 0][j] : gamma ? d * gv[j] : d;
+          s1 += uj;
+          s2 += uj * cj;
+          if (kKeep) {
+            c_[kKeep ? i : 0][j] = cj;
+            u_[kKeep ? i : 0][j] = uj;
+          }
         }
       }
     }
-    row_sum2<G>(s1, s2, sm);
-    s1 /= (float)N;
-    s2 /= (float)N;
+    row_sum2<G>(s1, s2, sm, turn);
+    turn ^= 1;
+    const float k1 = r0 * (s1 / (float)N), k2 = (r0 * r0) * r0 * (s2 / (float)N);
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
       const int c = (i * G + t) * VEC;
       if (c < N) {
-        float o[VEC];
+        if constexpr (!kKeep && kRing) {  // once more from the ring: registers are short here
+          h[i] = ring_at(slot, 2 * i);
+          u[i] = ring_at(slot, 2 * i + 1);
+        }
+        float gv[VEC], o[VEC];
+        if (!kKeep && gamma) load_vec<WT, VEC>(gamma + c, gv);
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) o[j] = rs * (u[i][j] - s1 - h[i][j] * s2);
+        for (int j = 0; j < VEC; ++j) {
+          float cj, uj;
+          if constexpr (kKeep) {
+            cj = c_[i][j];
+            uj = u_[i][j];
+          } else {
+            const float d = raw_at(u[i], j);
+            cj = raw_at(h[i], j) - m0;
+            uj = gamma ? d * gv[j] : d;
+          }
+          o[j] = (r0 * uj - k1) - cj * k2;
+        }
         store_vec<XT, VEC>(dx + row * lddx + c, o);
       }
     }
+    if (kRing && ++slot == S) slot = 0;
   }
   if (!part) return;
-  float* pg = part + (int64_t)blockIdx.x * 2 * N;
+  float* pg = part + (int64_t)blockIdx.x * 2 * N;  // a single block writes the results
+  if constexpr (kRing) asm volatile("cp.async.wait_all;" ::: "memory");
+  if constexpr (GROUPS > 1) {
+    // the block's groups, in order, through the columns of one shared row at a time
+    __shared__ float cols[2][G * PER * VEC];
+    for (int g = 0; g < GROUPS; ++g) {
+      __syncthreads();
+      if ((int)threadIdx.x / G == g) {
 #pragma unroll
-  for (int i = 0; i < PER; ++i)
+        for (int i = 0; i < PER; ++i)
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) {
-      const int c = (i * G + t) * VEC + j;
-      if (c < N) {
-        pg[c] = dg[i][j];
-        pg[N + c] = db[i][j];
+          for (int j = 0; j < VEC; ++j) {
+            const int c = (i * G + t) * VEC + j;
+            cols[0][c] = g == 0 ? dg[i][j] : cols[0][c] + dg[i][j];
+            cols[1][c] = g == 0 ? db[i][j] : cols[1][c] + db[i][j];
+          }
       }
     }
+    __syncthreads();
+    for (int c = threadIdx.x; c < N; c += B) {
+      if (gridDim.x == 1) {
+        if (dgamma) dgamma[c] = from_f<WT>(cols[0][c]);
+        if (dbeta) dbeta[c] = from_f<WT>(cols[1][c]);
+      } else {
+        pg[c] = cols[0][c];
+        pg[N + c] = cols[1][c];
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int c = (i * G + t) * VEC;
+      if (c < N) {
+        if (gridDim.x == 1) {
+#pragma unroll
+          for (int j = 0; j < VEC; ++j) {
+            if (dgamma) dgamma[c + j] = from_f<WT>(dg[i][j]);
+            if (dbeta) dbeta[c + j] = from_f<WT>(db[i][j]);
+          }
+        } else if constexpr (VEC > 1) {  // N is a multiple of VEC, the partials 16-byte aligned
+#pragma unroll
+          for (int j = 0; j < VEC; j += 4) {
+            *reinterpret_cast<float4*>(pg + c + j) =
+                make_float4(dg[i][j], dg[i][j + 1], dg[i][j + 2], dg[i][j + 3]);
+            *reinterpret_cast<float4*>(pg + N + c + j) =
+                make_float4(db[i][j], db[i][j + 1], db[i][j + 2], db[i][j + 3]);
+          }
+        } else {
+          pg[c] = dg[i][0];
+          pg[N + c] = db[i][0];
+        }
+      }
+    }
+  }
 }
 
 // Longer rows: the weight gradients' partials first (dx may be dy or x), then dx.
@@ -283,7 +482,8 @@ __global__ void __launch_bounds__(1024) ln_bwd_rows_long_kernel(
     const float* __restrict__ mean, const float* __restrict__ rstd, XT* dx, int64_t lddx,
     int64_t M, int64_t N) {
   MOE_GRIDDEP_ENTRY();
-  __shared__ float sm[64];
+  __shared__ float sm[2][2][32];
+  int turn = 0;
   for (int64_t row = blockIdx.x; row < M; row += gridDim.x) {
     const float mu = mean[row], rs = rstd[row];
     float s1 = 0.f, s2 = 0.f;
@@ -293,7 +493,8 @@ __global__ void __launch_bounds__(1024) ln_bwd_rows_long_kernel(
       s1 += u;
       s2 += u * ((to_f(x[row * ldx + c]) - mu) * rs);
     }
-    row_sum2<1024>(s1, s2, sm);
+    row_sum2<1024>(s1, s2, sm, turn);
+    turn ^= 1;
     s1 /= (float)N;
     s2 /= (float)N;
     for (int64_t c = threadIdx.x; c < N; c += 1024) {
@@ -305,29 +506,34 @@ __global__ void __launch_bounds__(1024) ln_bwd_rows_long_kernel(
   }
 }
 
-// dgamma[c] (columns [0, N)) and dbeta (columns [N, 2N)) = sum of the blocks' partials. A warp
-// sums every eighth partial of 32 columns; the eight sums are added in order.
+// dgamma[c] (columns [0, N)) and dbeta (columns [N, 2N)) = sum of the blocks' partials. Each of a
+// block's 32 warps sums every 32nd partial of 32 columns; the warps' sums are added in order.
 template <typename WT>
-__global__ void __launch_bounds__(256) ln_colsum_kernel(const float* __restrict__ part, int nparts,
-                                                        int64_t N, WT* __restrict__ dgamma,
-                                                        WT* __restrict__ dbeta) {
+__global__ void __launch_bounds__(1024) ln_colsum_kernel(const float* __restrict__ part,
+                                                         int nparts, int64_t N,
+                                                         WT* __restrict__ dgamma,
+                                                         WT* __restrict__ dbeta) {
   MOE_GRIDDEP_ENTRY();
-  __shared__ float sm[8][32];
+  __shared__ float sm[32][33];
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int64_t c = (int64_t)blockIdx.x * 32 + lane;
   float s = 0.f;
-  if (c < 2 * N)
-    for (int b = w; b < nparts; b += 8) s += part[(int64_t)b * 2 * N + c];
+  if (c < 2 * N) {
+#pragma unroll 5
+    for (int b = w; b < nparts; b += 32) s += part[(int64_t)b * 2 * N + c];
+  }
   sm[w][lane] = s;
   __syncthreads();
-  if (w == 0 && c < 2 * N) {
-    s = 0.f;
+  // warp w holds column w's 32 sums: lane l that of warp l
+  s = sm[lane][w];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) s += sm[i][lane];
-    if (c < N) {
-      if (dgamma) dgamma[c] = from_f<WT>(s);
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+  const int64_t col = (int64_t)blockIdx.x * 32 + w;
+  if (lane == 0 && col < 2 * N) {
+    if (col < N) {
+      if (dgamma) dgamma[col] = from_f<WT>(s);
     } else if (dbeta) {
-      dbeta[c - N] = from_f<WT>(s);
+      dbeta[col - N] = from_f<WT>(s);
     }
   }
 }
@@ -343,16 +549,18 @@ struct LnArgs {
   float *mean, *rstd;
   int64_t M, N;
   float eps;
+  void *dgamma, *dbeta;
   float* part;
   int nparts;
+  bool done;  // the weight gradients are final
   cudaStream_t s;
 };
 
-template <typename XT, typename WT, int VEC, int G, int PER>
+template <typename XT, typename WT, int VEC, int G, int PER, int RP = 1>
 void fwd_launch(const LnArgs& a) {
-  constexpr int B = G < 128 ? 128 : G;
-  const int64_t blocks = (a.M + B / G - 1) / (B / G);
-  ln_fwd_kernel<XT, WT, VEC, G, PER><<<(unsigned)blocks, B, 0, a.s>>>(
+  constexpr int B = G < 128 ? 128 : G, rows = B / G * RP;
+  const int64_t blocks = (a.M + rows - 1) / rows;
+  ln_fwd_kernel<XT, WT, VEC, G, PER, RP><<<(unsigned)blocks, B, 0, a.s>>>(
       static_cast<const XT*>(a.x), a.ldx, static_cast<const WT*>(a.gamma),
       static_cast<const WT*>(a.beta), static_cast<XT*>(a.y), a.ldy, a.mean, a.rstd, a.M, (int)a.N,
       a.eps);
@@ -361,18 +569,42 @@ void fwd_launch(const LnArgs& a) {
 template <typename XT, typename WT>
 void fwd_typed(const LnArgs& a) {
   constexpr int V = 16 / sizeof(XT);
+  // Weights wider than the rows cost more L1 reads than the rows: two rows share them (16384 x
+  // 2880 bf16 rows, fp32 weights: 35.4 us against 42.7). With equal types the registers of a
+  // second row cost more than it saves (8192 x 4096 bf16: 29.8 us against 23.2).
+  constexpr int RP = sizeof(WT) > sizeof(XT) ? 2 : 1;
   const bool vec = a.N % V == 0 && a.ldx % V == 0 && a.ldy % V == 0 && aligned_to(a.x, 16) &&
                    aligned_to(a.y, 16) && aligned_to(a.gamma, 16) && aligned_to(a.beta, 16);
   const int64_t N = a.N;
+  // Up to 32 elements a thread: as few warps a row as hold it, for many rows in flight; with too
+  // few rows to fill the GPU that way, as many threads as the row feeds, which is there sooner.
+  const bool many = a.M >= (int64_t)std::max(device_sms(), 1) * 2;
   if (vec) {
+    constexpr int P = 32 / V;  // vectors of 32 elements
     if (N <= 32 * V) return fwd_launch<XT, WT, V, 32, 1>(a);
-    if (N <= 32 * 4 * V) return fwd_launch<XT, WT, V, 32, 4>(a);
-    if (N <= 256 * 2 * V) return fwd_launch<XT, WT, V, 256, 2>(a);
-    if (N <= 512 * 4 * V) return fwd_launch<XT, WT, V, 512, 4>(a);
+    if (many) {
+      if (N <= 32 * 2 * V) return fwd_launch<XT, WT, V, 32, 2>(a);
+      if (N <= 32 * 32) return fwd_launch<XT, WT, V, 32, P>(a);
+      if (N <= 128 * 16) return fwd_launch<XT, WT, V, 128, P / 2, RP>(a);
+      if (N <= 128 * 24) return fwd_launch<XT, WT, V, 128, P / 4 * 3, RP>(a);
+      if (N <= 128 * 32) return fwd_launch<XT, WT, V, 128, P, RP>(a);
+      if (N <= 256 * 32) return fwd_launch<XT, WT, V, 256, P, RP>(a);
+      if (N <= 512 * 32) return fwd_launch<XT, WT, V, 512, P, RP>(a);
+    }
+    if (N <= 256 * V) return fwd_launch<XT, WT, V, 256, 1>(a);
+    if (N <= 512 * V) return fwd_launch<XT, WT, V, 512, 1>(a);
+    if (N <= 1024 * V) return fwd_launch<XT, WT, V, 1024, 1>(a);
+    if (N <= 1024 * 16) return fwd_launch<XT, WT, V, 1024, 16 / V>(a);
+    if (N <= 1024 * 32) return fwd_launch<XT, WT, V, 1024, P>(a);
   } else {
     if (N <= 32 * 8) return fwd_launch<XT, WT, 1, 32, 8>(a);
-    if (N <= 256 * 8) return fwd_launch<XT, WT, 1, 256, 8>(a);
-    if (N <= 512 * 32) return fwd_launch<XT, WT, 1, 512, 32>(a);
+    if (many) {
+      if (N <= 32 * 16) return fwd_launch<XT, WT, 1, 32, 16>(a);
+      if (N <= 32 * 32) return fwd_launch<XT, WT, 1, 32, 32>(a);
+      if (N <= 128 * 24) return fwd_launch<XT, WT, 1, 128, 24>(a);
+    }
+    if (N <= 1024 * 4) return fwd_launch<XT, WT, 1, 1024, 4>(a);
+    if (N <= 1024 * 16) return fwd_launch<XT, WT, 1, 1024, 16>(a);
   }
   const int grid = (int)std::min<int64_t>(a.M, (int64_t)std::max(device_sms(), 1) * 2);
   ln_fwd_long_kernel<XT, WT><<<grid, 1024, 0, a.s>>>(
@@ -381,36 +613,62 @@ void fwd_typed(const LnArgs& a) {
       a.eps);
 }
 
-int bwd_parts(int64_t M) {
-  const int most = std::min(std::max(device_sms(), 1), kMaxParts);
-  return (int)std::max<int64_t>(1, std::min<int64_t>(M, most));
-}
-
-template <typename XT, typename WT, int VEC, int G, int PER>
-void bwd_launch(const LnArgs& a) {
-  ln_bwd_kernel<XT, WT, VEC, G, PER><<<a.nparts, G, 0, a.s>>>(
-      static_cast<const XT*>(a.dy), a.lddy, static_cast<const XT*>(a.x), a.ldx,
-      static_cast<const WT*>(a.gamma), a.mean, a.rstd, static_cast<XT*>(a.dx), a.lddx, a.part, a.M,
-      (int)a.N);
+template <typename XT, typename WT, int VEC, int G, int PER, int S>
+cudaError_t bwd_launch(LnArgs& a) {
+  constexpr int B = G < 256 ? 256 : G, GROUPS = B / G;
+  constexpr int smem = ring_bytes<XT, VEC, B, PER, S>();
+  auto kern = ln_bwd_kernel<XT, WT, VEC, G, PER, S>;
+  if (smem > 0) {
+    cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kern), smem);
+    if (e != cudaSuccess) return e;
+  }
+  // as many blocks as fit at once (at least two where registers allow), each a row of partials
+  static const int per_sm = [&] {
+    int n = 0;
+    return cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, B, smem) == cudaSuccess && n > 0
+               ? n : 1;
+  }();
+  const int64_t fit = (int64_t)std::max(device_sms(), 1) * per_sm;
+  a.nparts = (int)std::max<int64_t>(
+      1, std::min<int64_t>((a.M + GROUPS - 1) / GROUPS, std::min<int64_t>(fit, max_parts(a.N))));
+  kern<<<a.nparts, B, smem, a.s>>>(static_cast<const XT*>(a.dy), a.lddy,
+                                   static_cast<const XT*>(a.x), a.ldx,
+                                   static_cast<const WT*>(a.gamma), a.mean, a.rstd,
+                                   static_cast<XT*>(a.dx), a.lddx, a.part,
+                                   static_cast<WT*>(a.dgamma), static_cast<WT*>(a.dbeta), a.M,
+                                   (int)a.N);
+  a.done = a.nparts == 1;
+  return cudaGetLastError();
 }
 
 template <typename XT, typename WT>
-void bwd_typed(const LnArgs& a) {
+cudaError_t bwd_typed(LnArgs& a) {
   constexpr int V = 16 / sizeof(XT);
   const bool vec = a.N % V == 0 && a.ldx % V == 0 && a.lddy % V == 0 && a.lddx % V == 0 &&
                    aligned_to(a.x, 16) && aligned_to(a.dy, 16) && aligned_to(a.dx, 16) &&
                    aligned_to(a.gamma, 16);
   const int64_t N = a.N;
   if (vec) {
-    if (N <= 32 * V) return bwd_launch<XT, WT, V, 32, 1>(a);
-    if (N <= 256 * V) return bwd_launch<XT, WT, V, 256, 1>(a);
-    if (N <= 512 * 2 * V) return bwd_launch<XT, WT, V, 512, 2>(a);
-    if (N <= 512 * 4 * V) return bwd_launch<XT, WT, V, 512, 4>(a);
+    if (N <= 32 * V) return bwd_launch<XT, WT, V, 32, 1, 4>(a);
+    if (N <= 32 * 2 * V) return bwd_launch<XT, WT, V, 32, 2, 3>(a);
+    if (N <= 32 * 4 * V) return bwd_launch<XT, WT, V, 32, 4, 3>(a);
+    if (N <= 256 * V) return bwd_launch<XT, WT, V, 256, 1, 4>(a);
+    if (N <= 256 * 2 * V) return bwd_launch<XT, WT, V, 256, 2, 4>(a);
+    if constexpr (sizeof(XT) == 4) {
+      if (N <= 256 * 4 * V) return bwd_launch<XT, WT, V, 256, 4, 3>(a);
+    } else {
+      if (N <= 512 * 2 * V) return bwd_launch<XT, WT, V, 512, 2, 3>(a);
+    }
+    if (N <= 512 * 4 * V) return bwd_launch<XT, WT, V, 512, 4, 3>(a);
+    if constexpr (sizeof(XT) == 4)
+      if (N <= 512 * 8 * V) return bwd_launch<XT, WT, V, 512, 8, 1>(a);
   } else {
-    if (N <= 32 * 8) return bwd_launch<XT, WT, 1, 32, 8>(a);
-    if (N <= 512 * 8) return bwd_launch<XT, WT, 1, 512, 8>(a);
-    if (N <= 512 * 32) return bwd_launch<XT, WT, 1, 512, 32>(a);
+    if (N <= 32 * 8) return bwd_launch<XT, WT, 1, 32, 8, 1>(a);
+    if (N <= 256 * 4) return bwd_launch<XT, WT, 1, 256, 4, 1>(a);
+    if (N <= 512 * 8) return bwd_launch<XT, WT, 1, 512, 8, 1>(a);
+    if (N <= 512 * 32) return bwd_launch<XT, WT, 1, 512, 32, 1>(a);
   }
+  a.nparts = (int)std::min<int64_t>(a.M, std::min<int64_t>(std::max(device_sms(), 1), max_parts(N)));
   if (a.part) {
     ln_bwd_cols_long_kernel<XT><<<a.nparts, 256, 0, a.s>>>(
         static_cast<const XT*>(a.dy), a.lddy, static_cast<const XT*>(a.x), a.ldx, a.mean, a.rstd,
@@ -421,6 +679,7 @@ void bwd_typed(const LnArgs& a) {
   ln_bwd_rows_long_kernel<XT, WT><<<grid, 1024, 0, a.s>>>(
       static_cast<const XT*>(a.dy), a.lddy, static_cast<const XT*>(a.x), a.ldx,
       static_cast<const WT*>(a.gamma), a.mean, a.rstd, static_cast<XT*>(a.dx), a.lddx, a.M, a.N);
+  return cudaGetLastError();
 }
 
 moe_status_t check_types(int64_t M, int64_t N, int32_t xd, int32_t wd) {
@@ -472,7 +731,7 @@ size_t moe_layernorm_workspace(int64_t M, int64_t N) {
     fail(MOE_ERR_INVALID_ARG, "M must be in [0, 2^31) and N in [1, 2^31)");
     return 0;
   }
-  return (size_t)std::max<int64_t>(1, std::min<int64_t>(M, kMaxParts)) * 2 * N * sizeof(float);
+  return (size_t)std::max<int64_t>(1, std::min<int64_t>(M, max_parts(N))) * 2 * N * sizeof(float);
 }
 
 moe_status_t moe_layernorm_bwd(const void* dy, int64_t lddy, const void* x, int64_t ldx,
@@ -505,26 +764,24 @@ moe_status_t moe_layernorm_bwd(const void* dy, int64_t lddy, const void* x, int6
   a.mean = const_cast<float*>(mean); a.rstd = const_cast<float*>(rstd);
   a.M = M; a.N = N;
   a.part = weights ? static_cast<float*>(ws) : nullptr;
-  a.nparts = bwd_parts(M);
+  a.dgamma = dgamma;
+  a.dbeta = dbeta;
   a.s = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e = cudaSuccess;
   if (M > 0) {
-    if (x_dtype == MOE_DT_FP32) bwd_typed<float, float>(a);
-    else if (w_dtype == MOE_DT_FP32) bwd_typed<__nv_bfloat16, float>(a);
-    else bwd_typed<__nv_bfloat16, __nv_bfloat16>(a);
+    e = x_dtype == MOE_DT_FP32   ? bwd_typed<float, float>(a)
+        : w_dtype == MOE_DT_FP32 ? bwd_typed<__nv_bfloat16, float>(a)
+                                 : bwd_typed<__nv_bfloat16, __nv_bfloat16>(a);
     count_launch(a.s, MOE_K_LAYERNORM_BWD);
-    e = cudaGetLastError();
     if (e != cudaSuccess) return cuda_fail(e, "layernorm backward launch");
-  } else {
-    a.nparts = 0;  // no rows: the sums are zero
-  }
-  if (weights) {
+  }  // no rows: no partials, the sums are zero
+  if (weights && !a.done) {
     const unsigned grid = (unsigned)((2 * N + 31) / 32);
     if (w_dtype == MOE_DT_FP32)
-      e = launch_chained(ln_colsum_kernel<float>, grid, 256, 0, a.s, (const float*)a.part,
+      e = launch_chained(ln_colsum_kernel<float>, grid, 1024, 0, a.s, (const float*)a.part,
                          a.nparts, N, static_cast<float*>(dgamma), static_cast<float*>(dbeta));
     else
-      e = launch_chained(ln_colsum_kernel<__nv_bfloat16>, grid, 256, 0, a.s,
+      e = launch_chained(ln_colsum_kernel<__nv_bfloat16>, grid, 1024, 0, a.s,
                          (const float*)a.part, a.nparts, N, static_cast<__nv_bfloat16*>(dgamma),
                          static_cast<__nv_bfloat16*>(dbeta));
     count_launch(a.s, MOE_K_LAYERNORM_REDUCE);
