@@ -14,9 +14,12 @@
 namespace moe {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 256;       // gradient
 constexpr int kWarps = kThreads / 32;
-constexpr int kMaxBlocks = 256;  // partial rows the workspace holds
+constexpr int kLossThreads = 1024;  // loss: one block an SM, so that few partials are left
+constexpr int kLossWarps = kLossThreads / 32;
+constexpr int kMaxBlocks = 256;     // partial rows the workspace holds
+constexpr int kFinishCtas = 8;      // cluster that adds them up, 32 experts a CTA
 
 // One block's share: sum of p over its valid tokens and the pairs routed to the expert. Entry E
 // holds the number of valid tokens in c.
@@ -44,7 +47,7 @@ MOE_DEVICE void load_row(const float* row, int E, int L, int sub, float (&v)[V *
     }
   }
 #pragma unroll
-  for (int i = 0; i < V * VEC; ++i) v[i] = v[i] == v[i] ? v[i] : -INFINITY;
+  for (int i = 0; i < V * VEC; ++i) v[i] = fmaxf(v[i], -INFINITY);  // a NaN loses to -inf
 }
 
 MOE_DEVICE float group_max(float x, int L) {
@@ -56,69 +59,71 @@ MOE_DEVICE float group_sum(float x, int L) {
   return x;
 }
 
-// v <- softmax over the group; a value equal to the maximum weighs 1 (also an infinite one).
+// v <- exp(v - max) over the group; returns the reciprocal of their sum. Under an infinite maximum
+// the values equal to it weigh 1 and the others 0.
 template <int VEC, int V>
-MOE_DEVICE void softmax_row(float (&v)[V * VEC], int E, int L, int sub) {
-  float m = -INFINITY;
+MOE_DEVICE float softmax_row(float (&v)[V * VEC], int E, int L, int sub) {
+  float m = v[0];
 #pragma unroll
-  for (int i = 0; i < V * VEC; ++i) m = fmaxf(m, v[i]);
+  for (int i = 1; i < V * VEC; ++i) m = fmaxf(m, v[i]);
   m = group_max(m, L);
   float s = 0.f;
+  if (fabsf(m) < INFINITY) {
 #pragma unroll
-  for (int i = 0; i < V; ++i)
-#pragma unroll
-    for (int j = 0; j < VEC; ++j) {
-      float& x = v[i * VEC + j];
-      const bool in = (i * L + sub) * VEC + j < E;
-      x = !in ? 0.f : x == m ? 1.0f : expf(x - m);
-      s += x;
+    for (int i = 0; i < V * VEC; ++i) {
+      v[i] = expf(v[i] - m);
+      s += v[i];
     }
-  s = group_sum(s, L);
-  const float inv = 1.0f / s;
+  } else {
 #pragma unroll
-  for (int i = 0; i < V * VEC; ++i) v[i] *= inv;
-}
-
-// The block's partials, or (one block) straight to the results.
-MOE_DEVICE void finish_expert(int e, double p, int c, int n, int E, int k, float* mean_prob,
-                              int32_t* counts, double& term) {
-  const double mp = n > 0 ? p / n : 0.0;
-  mean_prob[e] = (float)mp;
-  counts[e] = c;
-  if (n > 0) term += mp * ((double)E * c / ((double)k * n));
+    for (int i = 0; i < V; ++i)
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) {
+        float& x = v[i * VEC + j];
+        x = (i * L + sub) * VEC + j < E && x == m ? 1.0f : 0.f;
+        s += x;
+      }
+  }
+  __syncwarp();
+  return 1.0f / group_sum(s, L);
 }
 
 template <int VEC, int V>
-__global__ void __launch_bounds__(kThreads) router_loss_kernel(
+__global__ void __launch_bounds__(kLossThreads) router_loss_kernel(
     const float* __restrict__ logits, int64_t ld, const int32_t* __restrict__ ids,
     const uint8_t* __restrict__ mask, int T, int E, int k, int L, Partial* __restrict__ part) {
   MOE_GRIDDEP_ENTRY();
   __shared__ int hist[257];
-  __shared__ float psum[kWarps][256];
-  for (int i = threadIdx.x; i <= E; i += kThreads) hist[i] = 0;
+  __shared__ float psum[kLossWarps][256];
+  for (int i = threadIdx.x; i <= E; i += kLossThreads) hist[i] = 0;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int sub = lane & (L - 1), grp = lane / L, G = 32 / L;
-  const int64_t stride = (int64_t)gridDim.x * kWarps * G;
+  const int64_t stride = (int64_t)gridDim.x * kLossWarps * G;
   float acc[V * VEC];
 #pragma unroll
   for (int i = 0; i < V * VEC; ++i) acc[i] = 0.f;
   int valid = 0;
   __syncthreads();
-  for (int64_t t0 = ((int64_t)blockIdx.x * kWarps + warp) * G; t0 < T; t0 += stride) {
+  for (int64_t t0 = ((int64_t)blockIdx.x * kLossWarps + warp) * G; t0 < T; t0 += stride) {
     const int64_t t = t0 + grp;
     const bool live = t < T && (!mask || mask[t]);
+    const int32_t* id = ids + t * k;
+    int e0 = -1;  // this lane's first id, loaded ahead
+    if (live && sub < k) e0 = id[sub];
     float v[V * VEC];
     load_row<VEC, V>(logits + (t < T ? t : t0) * ld, E, L, sub, v);
-    softmax_row<VEC, V>(v, E, L, sub);
+    const float inv = softmax_row<VEC, V>(v, E, L, sub);
     if (live) {
 #pragma unroll
-      for (int i = 0; i < V * VEC; ++i) acc[i] += v[i];
+      for (int i = 0; i < V * VEC; ++i) acc[i] += v[i] * inv;
       valid += sub == 0;
-      for (int j = sub; j < k; j += L) {
-        const int e = ids[t * k + j];
+      if (e0 >= 0 && e0 < E) atomicAdd(&hist[e0], 1);
+      for (int j = sub + L; j < k; j += L) {
+        const int e = id[j];
         if (e >= 0 && e < E) atomicAdd(&hist[e], 1);
       }
     }
+    __syncwarp();
   }
   // the warp's token groups, then the block's warps, in a fixed order
 #pragma unroll
@@ -135,61 +140,84 @@ __global__ void __launch_bounds__(kThreads) router_loss_kernel(
   }
   if (valid) atomicAdd(&hist[E], valid);
   __syncthreads();
-  for (int e = threadIdx.x; e <= E; e += kThreads) {
+  for (int e = threadIdx.x; e <= E; e += kLossThreads) {
     Partial o;
     o.c = hist[e];
     o.p = 0.f;
-    if (e < E)
-      for (int w = 0; w < kWarps; ++w) o.p += psum[w][e];
+    if (e < E) {
+      float s[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int w = 0; w < kLossWarps; ++w) s[w & 3] += psum[w][e];
+      o.p = (s[0] + s[1]) + (s[2] + s[3]);
+    }
     part[(int64_t)blockIdx.x * (E + 1) + e] = o;
   }
 }
 
-// Sums the blocks' partials in block order and forms the loss (one block).
-__global__ void __launch_bounds__(1024) router_loss_finish_kernel(
-    const Partial* __restrict__ part, int nblk, int E, int k, float coef, float* loss,
-    int32_t* counts, float* mean_prob, int32_t* n_valid) {
+// Sums the blocks' partials in a fixed order and forms the loss: one cluster, CTA c for experts
+// 32 c .., its warp w for every eighth partial.
+__global__ void __launch_bounds__(256) __cluster_dims__(kFinishCtas, 1, 1)
+    router_loss_finish_kernel(const Partial* __restrict__ part, int nblk, int E, int k, float coef,
+                              float* loss, int32_t* counts, float* mean_prob, int32_t* n_valid) {
   MOE_GRIDDEP_ENTRY();
-  __shared__ double sp[1024];
-  __shared__ int sc[1024];
-  __shared__ int s_n;
-  __shared__ double s_term[32];
-  // thread (g, e): every fourth block's entry of expert e (E <= 256); valid tokens separately
-  const int g = threadIdx.x >> 8, e = threadIdx.x & 255;
-  double p = 0.0;
-  int c = 0;
-  if (e < E)
-    for (int b = g; b < nblk; b += 4) {
+  __shared__ float sp[8][32];
+  __shared__ int sc[8][32];
+  __shared__ int sn[8];
+  __shared__ float term;
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const uint32_t rank = cluster_ctarank();
+  const int e = (int)rank * 32 + lane;
+  float p = 0.f;
+  int c = 0, n = 0;
+  if (e < E) {
+#pragma unroll 4
+    for (int b = w; b < nblk; b += 8) {
       const Partial q = part[(int64_t)b * (E + 1) + e];
       p += q.p;
       c += q.c;
     }
-  sp[threadIdx.x] = p;
-  sc[threadIdx.x] = c;
-  if (threadIdx.x < 32) {
-    int n = 0;
-    for (int b = threadIdx.x; b < nblk; b += 32) n += part[(int64_t)b * (E + 1) + E].c;
-    for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xFFFFFFFFu, n, o);
-    if (threadIdx.x == 0) s_n = n;
+  }
+  for (int b = threadIdx.x; b < nblk; b += 256) n += part[(int64_t)b * (E + 1) + E].c;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xFFFFFFFFu, n, o);
+  sp[w][lane] = p;
+  sc[w][lane] = c;
+  if (lane == 0) sn[w] = n;
+  __syncthreads();
+  n = 0;
+  for (int i = 0; i < 8; ++i) n += sn[i];
+  if (w == 0) {
+    float x = 0.f;
+    if (e < E) {
+      p = 0.f;
+      c = 0;
+      for (int i = 0; i < 8; ++i) {
+        p += sp[i][lane];
+        c += sc[i][lane];
+      }
+      const float mp = n > 0 ? p / (float)n : 0.f;
+      mean_prob[e] = mp;
+      counts[e] = c;
+      if (n > 0) x = mp * ((float)E * (float)c / ((float)k * (float)n));
+    }
+    x = group_sum(x, 32);
+    if (lane == 0) term = x;
   }
   __syncthreads();
-  const int n = s_n;
-  double term = 0.0;
-  if (threadIdx.x < E) {
-    const int x = threadIdx.x;
-    finish_expert(x, (sp[x] + sp[x + 256]) + (sp[x + 512] + sp[x + 768]),
-                  sc[x] + sc[x + 256] + sc[x + 512] + sc[x + 768], n, E, k, mean_prob, counts,
-                  term);
-  }
-  for (int o = 16; o > 0; o >>= 1) term += __shfl_xor_sync(0xFFFFFFFFu, term, o);
-  if ((threadIdx.x & 31) == 0) s_term[threadIdx.x >> 5] = term;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    double s = 0.0;
-    for (int w = 0; w < 8; ++w) s += s_term[w];
-    *loss = (float)((double)coef * s);
+  cluster_sync_all();
+  if (rank == 0 && threadIdx.x == 0) {
+    float s = 0.f;
+    for (uint32_t r = 0; r < kFinishCtas; ++r) {
+      float v;
+      asm volatile("ld.shared::cluster.f32 %0, [%1];"
+                   : "=f"(v) : "r"(mapa_shared(smem_u32(&term), r)) : "memory");
+      s += v;
+    }
+    *loss = coef * s;
     *n_valid = n;
   }
+  __syncthreads();
+  cluster_sync_all();  // no CTA leaves while its term may be read
 }
 
 template <int VEC, int V>
@@ -200,18 +228,15 @@ __global__ void __launch_bounds__(kThreads) router_grad_kernel(
     const int32_t* __restrict__ counts, const int32_t* __restrict__ n_valid,
     float* __restrict__ d, int64_t ldd) {
   MOE_GRIDDEP_ENTRY();
-  __shared__ float f[256];
   // the chosen probabilities' part of a warp's rows, added by slot and read back by expert
-  __shared__ float chosen[kWarps][32 * 8];
-  const int n = *n_valid;
-  const float g = n > 0 ? (d_loss ? *d_loss : 1.0f) * coef / (float)n : 0.f;
-  for (int e = threadIdx.x; e < 256; e += kThreads)
-    f[e] = e < E && n > 0 ? (float)((double)E * counts[e] / ((double)k * n)) : 0.f;
-  for (int i = threadIdx.x; i < kWarps * 32 * 8; i += kThreads) (&chosen[0][0])[i] = 0.f;
-  __syncthreads();
+  __shared__ __align__(16) float chosen[kWarps][32 * 8];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int sub = lane & (L - 1), grp = lane / L, G = 32 / L;
   const int64_t stride = (int64_t)gridDim.x * kWarps * G;
+  const int n = *n_valid;
+  const float g = n > 0 ? (d_loss ? *d_loss : 1.0f) * coef / (float)n : 0.f;
+  const float fs = n > 0 ? (float)E / ((float)k * (float)n) : 0.f;
+  for (int i = lane; i < 32 * 8; i += 32) chosen[warp][i] = 0.f;
   float* row_c = &chosen[warp][grp * L * V * VEC];  // G * L * V * VEC <= 256
   float fe[V * VEC];
 #pragma unroll
@@ -219,35 +244,46 @@ __global__ void __launch_bounds__(kThreads) router_grad_kernel(
 #pragma unroll
     for (int j = 0; j < VEC; ++j) {
       const int e = (i * L + sub) * VEC + j;
-      fe[i * VEC + j] = e < E ? f[e] : 0.f;
+      fe[i * VEC + j] = e < E ? fs * (float)counts[e] : 0.f;
     }
+  __syncwarp();
   for (int64_t t0 = ((int64_t)blockIdx.x * kWarps + warp) * G; t0 < T; t0 += stride) {
     const int64_t t = t0 + grp;
     const bool in = t < T;
+    const int64_t at = t * k + sub;
+    int e0 = -1;  // this lane's first slot, loaded ahead
+    float w0 = 0.f, d0 = 0.f;
+    if (w && in && sub < k) {
+      e0 = ids[at];
+      w0 = w[at];
+      d0 = dw[at];
+    }
     float v[V * VEC];
     load_row<VEC, V>(logits + (in ? t : t0) * ld, E, L, sub, v);
-    softmax_row<VEC, V>(v, E, L, sub);
+    const float inv = softmax_row<VEC, V>(v, E, L, sub);
     float s = 0.f;
 #pragma unroll
     for (int i = 0; i < V * VEC; ++i) s += v[i] * fe[i];
-    s = group_sum(s, L);
-    const float c = in && (!mask || mask[t]) ? g : 0.f;
+    s = group_sum(s, L) * inv;
     if (w) {
-      float dot = 0.f;
+      const bool ok0 = e0 >= 0 && e0 < E;
+      float dot = ok0 ? w0 * d0 : 0.f;
       if (in)
-        for (int j = sub; j < k; j += L) {
-          const int e = ids[t * k + j];
-          if (e >= 0 && e < E) dot += w[t * k + j] * dw[t * k + j];
+        for (int j = L; sub + j < k; j += L) {
+          const int e = ids[at + j];
+          if (e >= 0 && e < E) dot += w[at + j] * dw[at + j];
         }
       dot = group_sum(dot, L);
-      __syncwarp();
+      if (ok0) atomicAdd(&row_c[e0], w0 * (d0 - dot));
       if (in)
-        for (int j = sub; j < k; j += L) {
-          const int e = ids[t * k + j];
-          if (e >= 0 && e < E) atomicAdd(&row_c[e], w[t * k + j] * (dw[t * k + j] - dot));
+        for (int j = L; sub + j < k; j += L) {
+          const int e = ids[at + j];
+          if (e >= 0 && e < E) atomicAdd(&row_c[e], w[at + j] * (dw[at + j] - dot));
         }
       __syncwarp();
     }
+    const float c = in && (!mask || mask[t]) ? g : 0.f;
+    const float ci = c * inv;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int e = (i * L + sub) * VEC;
@@ -255,19 +291,29 @@ __global__ void __launch_bounds__(kThreads) router_grad_kernel(
 #pragma unroll
       for (int j = 0; j < VEC; ++j) {
         const int q = i * VEC + j;
-        o[j] = c != 0.f ? c * v[q] * (fe[q] - s) : 0.f;
-        if (w && e + j < E) {
-          o[j] += row_c[e + j];
-          row_c[e + j] = 0.f;
+        o[j] = c != 0.f ? ci * v[q] * (fe[q] - s) : 0.f;
+      }
+      if (e < E) {
+        if constexpr (VEC == 4) {
+          if (w) {
+            float4& r = *reinterpret_cast<float4*>(row_c + e);
+            o[0] += r.x;
+            o[1] += r.y;
+            o[2] += r.z;
+            o[3] += r.w;
+            r = make_float4(0.f, 0.f, 0.f, 0.f);
+          }
+          if (in) *reinterpret_cast<float4*>(d + t * ldd + e) = make_float4(o[0], o[1], o[2], o[3]);
+        } else {
+          if (w) {
+            o[0] += row_c[e];
+            row_c[e] = 0.f;
+          }
+          if (in) d[t * ldd + e] = o[0];
         }
       }
-      if (in && e < E) {
-        if constexpr (VEC == 4)
-          *reinterpret_cast<float4*>(d + t * ldd + e) = make_float4(o[0], o[1], o[2], o[3]);
-        else
-          d[t * ldd + e] = o[0];
-      }
     }
+    __syncwarp();
   }
 }
 
@@ -304,8 +350,8 @@ void with_map(const RowMap& m, F&& fn) {
   }
 }
 
-int router_blocks(int64_t T, const RowMap& m, int per_warp, int most) {
-  const int64_t per_block = (int64_t)kWarps * (32 / m.L) * per_warp;
+int router_blocks(int64_t T, const RowMap& m, int warps, int most) {
+  const int64_t per_block = (int64_t)warps * (32 / m.L);
   return (int)std::max<int64_t>(1, std::min<int64_t>((T + per_block - 1) / per_block, most));
 }
 
@@ -353,16 +399,16 @@ moe_status_t moe_router_loss_fwd(const float* logits, int64_t ld_logits, const i
                 moe_router_loss_workspace(E));
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const RowMap m = row_map(E, E % 4 == 0 && ld_logits % 4 == 0 && a16(logits));
-  const int nblk = router_blocks(T, m, 2, std::min(std::max(device_sms(), 1), kMaxBlocks));
+  const int nblk = router_blocks(T, m, kLossWarps, std::min(std::max(device_sms(), 1), kMaxBlocks));
   Partial* part = static_cast<Partial*>(ws);
   with_map(m, [&](auto vec, auto v) {
-    router_loss_kernel<vec.value, v.value><<<nblk, kThreads, 0, s>>>(
+    router_loss_kernel<vec.value, v.value><<<nblk, kLossThreads, 0, s>>>(
         logits, ld_logits, topk_ids, token_mask, T, E, k, m.L, part);
   });
   count_launch(s, MOE_K_ROUTER_LOSS);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return cuda_fail(e, "router loss launch");
-  e = launch_chained(router_loss_finish_kernel, 1, 1024, 0, s, (const Partial*)part, nblk, E, k,
+  e = launch_chained(router_loss_finish_kernel, kFinishCtas, 256, 0, s, (const Partial*)part, nblk, E, k,
                      coef, loss, counts, mean_prob, n_valid);
   count_launch(s, MOE_K_ROUTER_LOSS);
   if (e != cudaSuccess) return cuda_fail(e, "router loss finish launch");
@@ -389,7 +435,7 @@ moe_status_t moe_router_loss_bwd(const float* logits, int64_t ld_logits, const i
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const RowMap m = row_map(E, E % 4 == 0 && ld_logits % 4 == 0 && ld_d % 4 == 0 && a16(logits) &&
                                   a16(d_logits));
-  const int nblk = router_blocks(T, m, 1, std::max(device_sms(), 1) * 8);
+  const int nblk = router_blocks(T, m, kWarps, std::max(device_sms(), 1) * 8);
   with_map(m, [&](auto vec, auto v) {
     router_grad_kernel<vec.value, v.value><<<nblk, kThreads, 0, s>>>(
         logits, ld_logits, topk_ids, topk_probs, d_probs, token_mask, T, E, k, m.L, coef, d_loss,
