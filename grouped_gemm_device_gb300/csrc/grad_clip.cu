@@ -4,8 +4,11 @@
 //   norm = sqrt(sum g^2),  c = min(1, max_norm / (norm + 1e-6)),  out = c g
 //
 // Bound by HBM: one read of every gradient for the norm, one read and one write for the product.
-// Two kinds of launch: partial sums (one fp64 value a block), then the product, whose blocks each
-// add up the partial sums in the same order, so that no launch, counter or atomic joins them.
+// Two kinds of launch: partial sums (one a block), then the product, whose blocks each add up the
+// partial sums in the same order, so that no launch, counter or atomic joins them.
+// Sums are pairs of fp32 numbers (a running sum and what its roundings lost, by the error-free sum
+// of two numbers, Knuth 1969): about 48 bits at the full fp32 rate, where this GPU adds two fp64
+// numbers an SM and cycle. Squares that fp32 cannot hold go into an fp64 sum of their own.
 // The tensors travel as kernel parameters (up to kCap a launch); their elements are cut into
 // chunks that blocks take in turn.
 #include "kernels.cuh"
@@ -18,7 +21,7 @@ constexpr int kVecs = 4;                          // 16-byte loads a thread and 
 constexpr int kChunkBytes = kThreads * kVecs * 16;
 constexpr int kCap = 96;                          // tensors a launch
 constexpr int kMaxBlocks = 1216;                  // partial sums one launch leaves
-constexpr int kMaxLaunches = (65536 + kCap - 1) / kCap;
+constexpr int kMaxParts = 32768;                  // partial sums all launches leave together
 constexpr float kEps = 1e-6f;
 
 // A tensor is cut at 16-byte boundaries of its address: `src` is rounded down to one, `lead` the
@@ -45,132 +48,186 @@ MOE_DEVICE int find_tensor(const Batch& b, int64_t chunk) {
   return lo;
 }
 
-// The 16 bytes of vector `v` (element index v * PER of the rounded-down tensor) as fp32; elements
-// outside [lead, lead + numel) read as 0.
+// The 16 bytes of vector `v` (element index v * PER of the rounded-down tensor); elements outside
+// [lead, lead + numel) read as 0.
 template <int PER>
-MOE_DEVICE bool load16(const Tensor& t, int64_t v, float (&x)[PER]) {
+MOE_DEVICE uint4 load16(const Tensor& t, int64_t v) {
   const int64_t e = v * PER, end = t.lead + t.numel;
-  if (e >= end) {
-#pragma unroll
-    for (int i = 0; i < PER; ++i) x[i] = 0.f;
-    return false;
-  }
-  if (e >= t.lead && e + PER <= end) {
-    const uint4 q = reinterpret_cast<const uint4*>(t.src)[v];
-    const uint32_t u[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if constexpr (PER == 8) {
-        x[2 * i] = bf16_lo(u[i]);
-        x[2 * i + 1] = bf16_hi(u[i]);
-      } else {
-        x[i] = __uint_as_float(u[i]);
-      }
-    }
-  } else {
+  uint32_t u[4] = {0u, 0u, 0u, 0u};
+  if (e >= t.lead && e + PER <= end) return reinterpret_cast<const uint4*>(t.src)[v];
+  if (e < end) {
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-      const bool in = e + i >= t.lead && e + i < end;
+      if (e + i < t.lead || e + i >= end) continue;
       if constexpr (PER == 8)
-        x[i] = in ? __bfloat162float(static_cast<const __nv_bfloat16*>(t.src)[e + i]) : 0.f;
+        u[i >> 1] |= (uint32_t)static_cast<const uint16_t*>(t.src)[e + i] << (16 * (i & 1));
       else
-        x[i] = in ? static_cast<const float*>(t.src)[e + i] : 0.f;
+        u[i] = static_cast<const uint32_t*>(t.src)[e + i];
     }
   }
-  return true;
+  return make_uint4(u[0], u[1], u[2], u[3]);
+}
+template <int PER>
+MOE_DEVICE void widen(const uint4& q, float (&x)[PER]) {
+  const uint32_t u[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (PER == 8) {
+      x[2 * i] = bf16_lo(u[i]);
+      x[2 * i + 1] = bf16_hi(u[i]);
+    } else {
+      x[i] = __uint_as_float(u[i]);
+    }
+  }
 }
 
-// Sum of squares of one thread's share of a chunk. fp32 where the result is well inside its
-// range; otherwise (an overflow, or squares that may have been lost below it) fp64.
+// hi + lo, and what lies outside fp32's comfortable range.
+struct Sum {
+  float hi, lo;
+  double odd;
+};
+// (hi, lo) += x with no error but the rounding of lo
+MOE_DEVICE void add_to(float& hi, float& lo, float x) {
+  const float s = hi + x, v = s - hi;
+  lo += (hi - (s - v)) + (x - v);
+  hi = s;
+}
+
+// Adds the squares of one thread's share of a chunk: at most 32 of them in fp32 where their sum
+// is well inside its range; otherwise (an overflow, a NaN, or squares that may have been lost
+// below the range) in fp64.
 template <int PER>
-MOE_DEVICE double chunk_squares(const Tensor& t, int64_t v0) {
-  float x[kVecs][PER];
+MOE_DEVICE void add_squares(const Tensor& t, int64_t v0, Sum& sum) {
+  uint4 q[kVecs];
 #pragma unroll
-  for (int i = 0; i < kVecs; ++i) load16<PER>(t, v0 + i * kThreads, x[i]);
+  for (int i = 0; i < kVecs; ++i) q[i] = load16<PER>(t, v0 + i * kThreads);
   float s = 0.f;
 #pragma unroll
   for (int i = 0; i < kVecs; ++i) {
-    float q = 0.f;
+    float x[PER], p = 0.f;
+    widen<PER>(q[i], x);
 #pragma unroll
-    for (int j = 0; j < PER; ++j) q += x[i][j] * x[i][j];
-    s += q;
+    for (int j = 0; j < PER; ++j) p += x[j] * x[j];
+    s += p;
   }
-  if (s > 1e-20f && s < 1e30f) return (double)s;
-  bool zero = s == 0.f;  // an expert without tokens has zero gradients: nothing to add
+  if (s > 1e-20f && s < 1e28f) {
+    add_to(sum.hi, sum.lo, s);
+    return;
+  }
+  uint32_t any = 0;  // an expert without tokens has zero gradients: nothing to add
 #pragma unroll
-  for (int i = 0; i < kVecs; ++i)
+  for (int i = 0; i < kVecs; ++i) any |= q[i].x | q[i].y | q[i].z | q[i].w;
+  if (any == 0) return;
 #pragma unroll
-    for (int j = 0; j < PER; ++j) zero = zero && x[i][j] == 0.f;
-  if (zero) return 0.0;
-  double d = 0.0;
+  for (int i = 0; i < kVecs; ++i) {
+    float x[PER];
+    widen<PER>(q[i], x);
 #pragma unroll 1
-  for (int i = 0; i < kVecs; ++i)
-#pragma unroll
-    for (int j = 0; j < PER; ++j) d += (double)x[i][j] * (double)x[i][j];
-  return d;
+    for (int j = 0; j < PER; ++j) sum.odd += (double)x[j] * (double)x[j];
+  }
 }
 
-MOE_DEVICE double block_sum(double v, double* sm) {
+// The block's sum, the same in every thread.
+MOE_DEVICE Sum block_sum(Sum v) {
+  __shared__ float s_hi[kThreads / 32], s_lo[kThreads / 32];
+  __shared__ double s_odd[kThreads / 32];
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-  if ((threadIdx.x & 31) == 0) sm[threadIdx.x >> 5] = v;
-  __syncthreads();
-  double s = 0.0;
+  for (int o = 16; o > 0; o >>= 1) {
+    const float hi = __shfl_xor_sync(0xFFFFFFFFu, v.hi, o);
+    const float lo = __shfl_xor_sync(0xFFFFFFFFu, v.lo, o);
+    add_to(v.hi, v.lo, hi);
+    v.lo += lo;
+  }
+  if (lane == 0) {
+    s_hi[w] = v.hi;
+    s_lo[w] = v.lo;
+  }
+  const bool odd = __syncthreads_or(v.odd != 0.0);  // also a barrier for the sums above
+  v.hi = v.lo = 0.f;
 #pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w) s += sm[w];
+  for (int i = 0; i < kThreads / 32; ++i) {
+    add_to(v.hi, v.lo, s_hi[i]);
+    v.lo += s_lo[i];
+  }
+  if (odd) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v.odd += __shfl_xor_sync(0xFFFFFFFFu, v.odd, o);
+    if (lane == 0) s_odd[w] = v.odd;
+    __syncthreads();
+    v.odd = 0.0;
+    for (int i = 0; i < kThreads / 32; ++i) v.odd += s_odd[i];
+  }
+  return v;
+}
+
+// One thread's share of the partial sums.
+MOE_DEVICE Sum sum_parts(const Sum* part, int nparts) {
+  Sum s = {0.f, 0.f, 0.0};
+  for (int i = threadIdx.x; i < nparts; i += kThreads) {
+    const Sum p = part[i];
+    add_to(s.hi, s.lo, p.hi);
+    s.lo += p.lo;
+    if (p.odd != 0.0) s.odd += p.odd;
+  }
   return s;
 }
 
 __global__ void __launch_bounds__(kThreads) grad_norm_kernel(const __grid_constant__ Batch b,
-                                                             double* __restrict__ part) {
+                                                             Sum* __restrict__ part) {
   MOE_GRIDDEP_ENTRY();
-  __shared__ double sm[kThreads / 32];
-  double s = 0.0;
+  Sum s = {0.f, 0.f, 0.0};
   for (int64_t c = blockIdx.x; c < b.chunks; c += gridDim.x) {
     const Tensor& t = b.t[find_tensor(b, c)];
     const int64_t v0 = (c - t.first_chunk) * (kThreads * kVecs) + threadIdx.x;
-    s += t.fp32 ? chunk_squares<4>(t, v0) : chunk_squares<8>(t, v0);
+    if (t.fp32) add_squares<4>(t, v0, s);
+    else add_squares<8>(t, v0, s);
   }
-  s = block_sum(s, sm);
+  s = block_sum(s);
   if (threadIdx.x == 0) part[blockIdx.x] = s;
 }
 
 template <int PER>
 MOE_DEVICE void scale_chunk(const Tensor& t, int64_t v0, float c) {
-  float x[kVecs][PER];
-  bool in[kVecs];
+  uint4 q[kVecs];
 #pragma unroll
-  for (int i = 0; i < kVecs; ++i) in[i] = load16<PER>(t, v0 + i * kThreads, x[i]);
+  for (int i = 0; i < kVecs; ++i) q[i] = load16<PER>(t, v0 + i * kThreads);
 #pragma unroll
   for (int i = 0; i < kVecs; ++i) {
-    if (!in[i]) continue;
     const int64_t e = (v0 + i * kThreads) * PER, end = t.lead + t.numel;
+    if (e >= end) continue;
+    float x[PER];
+    widen<PER>(q[i], x);
 #pragma unroll
-    for (int j = 0; j < PER; ++j) x[i][j] *= c;
+    for (int j = 0; j < PER; ++j) x[j] *= c;
     // dst counts elements from the tensor's own first one
     if (t.dst_vec && e >= t.lead && e + PER <= end) {
-      uint4 q;
       if constexpr (PER == 8)
-        q = make_uint4(pack_bf16x2(x[i][0], x[i][1]), pack_bf16x2(x[i][2], x[i][3]),
-                       pack_bf16x2(x[i][4], x[i][5]), pack_bf16x2(x[i][6], x[i][7]));
+        *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(t.dst) + (e - t.lead)) =
+            make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
+                       pack_bf16x2(x[6], x[7]));
       else
-        q = make_uint4(__float_as_uint(x[i][0]), __float_as_uint(x[i][1]),
-                       __float_as_uint(x[i][2]), __float_as_uint(x[i][3]));
-      if constexpr (PER == 8)
-        *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(t.dst) + (e - t.lead)) = q;
-      else
-        *reinterpret_cast<uint4*>(static_cast<float*>(t.dst) + (e - t.lead)) = q;
+        *reinterpret_cast<float4*>(static_cast<float*>(t.dst) + (e - t.lead)) =
+            make_float4(x[0], x[1], x[2], x[3]);
     } else {
 #pragma unroll
       for (int j = 0; j < PER; ++j) {
         if (e + j < t.lead || e + j >= end) continue;
         if constexpr (PER == 8)
-          static_cast<__nv_bfloat16*>(t.dst)[e + j - t.lead] = __float2bfloat16_rn(x[i][j]);
+          static_cast<__nv_bfloat16*>(t.dst)[e + j - t.lead] = __float2bfloat16_rn(x[j]);
         else
-          static_cast<float*>(t.dst)[e + j - t.lead] = x[i][j];
+          static_cast<float*>(t.dst)[e + j - t.lead] = x[j];
       }
     }
   }
+}
+
+// Several launches' partial sums into one (one block).
+__global__ void __launch_bounds__(kThreads) grad_total_kernel(const Sum* __restrict__ part,
+                                                              int nparts, Sum* __restrict__ total) {
+  MOE_GRIDDEP_ENTRY();
+  const Sum s = block_sum(sum_parts(part, nparts));
+  if (threadIdx.x == 0) *total = s;
 }
 
 // c = min(1, max_norm / (norm + eps)) in fp32; a NaN norm gives NaN.
@@ -181,16 +238,14 @@ MOE_DEVICE float clip_factor(float norm, float max_norm) {
 
 // in_place: nothing to do when the factor is 1. apply = 0: only the norm.
 __global__ void __launch_bounds__(kThreads) grad_scale_kernel(const __grid_constant__ Batch b,
-                                                              const double* __restrict__ part,
+                                                              const Sum* __restrict__ part,
                                                               int nparts, float max_norm,
                                                               int apply, int in_place,
                                                               float* __restrict__ norm_out) {
   MOE_GRIDDEP_ENTRY();
-  __shared__ double sm[kThreads / 32];
-  double s = 0.0;
-  for (int i = threadIdx.x; i < nparts; i += kThreads) s += part[i];
-  s = block_sum(s, sm);
-  const float norm = (float)sqrt(s);
+  const Sum s = block_sum(sum_parts(part, nparts));
+  const float norm = s.odd != 0.0 ? (float)sqrt(((double)s.hi + (double)s.lo) + s.odd)
+                                  : sqrtf(s.hi + s.lo);
   if (norm_out && blockIdx.x == 0 && threadIdx.x == 0) *norm_out = norm;
   if (!apply) return;
   const float c = clip_factor(norm, max_norm);
@@ -228,8 +283,18 @@ int fill_batch(Batch& b, int i, int n, const void* const* grads, void* const* ou
   return i;
 }
 
-int clip_blocks(int64_t chunks) {
-  const int64_t most = std::min<int64_t>(kMaxBlocks, (int64_t)std::max(device_sms(), 1) * 8);
+// As many blocks as fit at once, or one a chunk. Very long lists get twice as many, which evens
+// out the blocks' ends (1.4 G bf16 elements: 1247 us against 1301; at 20 M the second half only
+// costs its start, 21.5 us against 18.2).
+template <class K>
+int clip_blocks(K kernel, int64_t chunks) {
+  static const int per_sm = [&] {
+    int n = 0;
+    return cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, kThreads, 0) == cudaSuccess &&
+                   n > 0 ? n : 1;
+  }();
+  const int64_t fit = (int64_t)std::max(device_sms(), 1) * per_sm;
+  const int64_t most = std::min<int64_t>(kMaxBlocks, chunks > 64 * fit ? 2 * fit : fit);
   return (int)std::max<int64_t>(1, std::min(chunks, most));
 }
 
@@ -241,7 +306,7 @@ using namespace moe;
 extern "C" {
 
 size_t moe_grad_clip_workspace(void) {
-  return (size_t)kMaxBlocks * kMaxLaunches * sizeof(double);
+  return (size_t)(kMaxParts + 1) * sizeof(Sum);
 }
 
 moe_status_t moe_grad_clip(int32_t n, const void* const* grads, void* const* outs,
@@ -272,8 +337,12 @@ moe_status_t moe_grad_clip(int32_t n, const void* const* grads, void* const* out
       return fail(MOE_ERR_INVALID_ARG, "tensor %d: not aligned to its elements", i);
   }
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  double* part = static_cast<double*>(ws);
-  int nparts = 0;
+  Sum* part = static_cast<Sum*>(ws);
+  int nparts = 0, held = 0, batches = 0;
+  for (int i = 0; i < n; ++i) held += numel[i] != 0;
+  // few launches take as many blocks as fit; many share the room for their partial sums
+  const int launches = (held + kCap - 1) / kCap;
+  const int most = launches > 0 ? std::max(kMaxParts / launches, 1) : 1;
   bool in_place = true;
   for (int i = 0; outs && i < n; ++i) in_place = in_place && (outs[i] == grads[i] || !numel[i]);
   Batch b;
@@ -281,7 +350,7 @@ moe_status_t moe_grad_clip(int32_t n, const void* const* grads, void* const* out
   for (int i = 0; i < n;) {
     i = fill_batch(b, i, n, grads, outs, numel, dtypes);
     if (b.n == 0) break;
-    const int grid = clip_blocks(b.chunks);
+    const int grid = std::min(clip_blocks(grad_norm_kernel, b.chunks), most);
     if (nparts == 0) {
       grad_norm_kernel<<<grid, kThreads, 0, s>>>(b, part);
       e = cudaGetLastError();
@@ -291,14 +360,23 @@ moe_status_t moe_grad_clip(int32_t n, const void* const* grads, void* const* out
     count_launch(s, MOE_K_GRAD_NORM);
     if (e != cudaSuccess) return cuda_fail(e, "gradient norm launch");
     nparts += grid;
+    ++batches;
+  }
+  if (batches > 1) {
+    e = launch_chained(grad_total_kernel, 1, kThreads, 0, s, (const Sum*)part, nparts,
+                       part + kMaxParts);
+    count_launch(s, MOE_K_GRAD_NORM);
+    if (e != cudaSuccess) return cuda_fail(e, "gradient norm total launch");
+    part += kMaxParts;
+    nparts = 1;
   }
   // the batches once more; every launch forms the same norm and factor
   int written = 0;
   for (int i = 0; i < n || written == 0;) {
     i = fill_batch(b, i, n, grads, outs, numel, dtypes);
     if (b.n == 0 && written > 0) break;
-    const int grid = apply ? clip_blocks(b.chunks) : 1;
-    e = launch_chained(grad_scale_kernel, grid, kThreads, 0, s, b, (const double*)part, nparts,
+    const int grid = apply ? clip_blocks(grad_scale_kernel, b.chunks) : 1;
+    e = launch_chained(grad_scale_kernel, grid, kThreads, 0, s, b, (const Sum*)part, nparts,
                        max_norm, apply ? 1 : 0, in_place ? 1 : 0, written == 0 ? norm : nullptr);
     count_launch(s, MOE_K_GRAD_SCALE);
     if (e != cudaSuccess) return cuda_fail(e, "gradient scale launch");
