@@ -160,6 +160,8 @@ def _ptr(t) -> int | None:
 def _stream(stream) -> int | None:
     if stream is None:
         import torch
+        if torch.cuda.is_initialized():  # the same handle without building a Stream object
+            return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
@@ -550,6 +552,11 @@ def _ld(t) -> int:
     return t.stride(0) if t.shape[0] > 1 else t.shape[1]
 
 
+def _first(buf, n):
+    """The first n rows of a buffer (the buffer itself when that is all of them)."""
+    return buf if buf.shape[0] == n else buf[:n]
+
+
 class RouterLoss:
     """Load-balance loss of a top-k router over up to T_max tokens, and the gradient of the
     router's logits (moe_router_loss_fwd / _bwd). Owns the results' buffers: they hold the last
@@ -605,7 +612,7 @@ class RouterLoss:
         moe_router_loss_bwd(logits, _ld(logits), topk_ids, topk_probs, d_probs, token_mask, T,
                             self.E, self.k, self.coef, d_loss, self.counts, self.n_valid,
                             self.d_logits, self.E, stream)
-        return self.d_logits[:T]
+        return _first(self.d_logits, T)
 
 
 class LayerNorm:
@@ -639,7 +646,7 @@ class LayerNorm:
         moe_layernorm_fwd(x, _ld(x), self._weight(gamma, "gamma"), self._weight(beta, "beta"),
                           self.y, self.N, self.mean, self.rstd, M, self.N, self.eps,
                           *self._codes, stream)
-        return self.y[:M], self.mean[:M], self.rstd[:M]
+        return _first(self.y, M), _first(self.mean, M), _first(self.rstd, M)
 
     def backward(self, dy, x, gamma=None, mean=None, rstd=None, stream=None):
         """mean, rstd: the forward's (None: those of the last forward). Returns
@@ -659,7 +666,7 @@ class LayerNorm:
         moe_layernorm_bwd(dy, _ld(dy), x, _ld(x), self._weight(gamma, "gamma"), mean, rstd,
                           self.dx, self.N, self.dgamma, self.dbeta, M, self.N, *self._codes,
                           self.ws, self.ws_bytes, stream)
-        return self.dx[:M], self.dgamma, self.dbeta
+        return _first(self.dx, M), self.dgamma, self.dbeta
 
 
 class GradClip:
@@ -718,8 +725,8 @@ class Fp8Linear:
             return torch.empty(max(blocks, 1), n, dtype=torch.float32, device=dev)
 
         mb = -(-M_max // 128)
-        self.wq, self.ws = codes(N, self._kp), scales(self.nb, self.kb)
-        self.xq, self.xs = codes(M_max, self._kp), scales(self.kb, self._mp)
+        self.wq, self.w_scale = codes(N, self._kp), scales(self.nb, self.kb)
+        self.xq, self.x_scale = codes(M_max, self._kp), scales(self.kb, self._mp)
         self.y = torch.empty(M_max, N, dtype=torch.bfloat16, device=dev)
         self.err = torch.zeros(1, dtype=torch.int32, device=dev)
         self.M = None
@@ -736,10 +743,10 @@ class Fp8Linear:
         import torch
         _expect(w, "w", torch.bfloat16, (self.N, self.K), rows=True)
         if self.train:
-            fp8_block_quantize_weight(w, _ld(w), self.N, self.K, self.wq, self._kp, self.ws,
+            fp8_block_quantize_weight(w, _ld(w), self.N, self.K, self.wq, self._kp, self.w_scale,
                                       self.wqt, self._np, self.wst, stream)
         else:
-            fp8_block_quantize_weight(w, _ld(w), self.N, self.K, self.wq, self._kp, self.ws,
+            fp8_block_quantize_weight(w, _ld(w), self.N, self.K, self.wq, self._kp, self.w_scale,
                                       stream=stream)
 
     def forward(self, x, stream=None):
@@ -750,15 +757,15 @@ class Fp8Linear:
             raise ValueError(f"{M} rows, but M_max is {self.M_max}")
         _expect(x, "x", torch.bfloat16, (M, self.K), rows=True)
         if self.train:
-            fp8_block_quantize_rows(x, _ld(x), M, self.K, self.xq, self._kp, self.xs, self._mp,
+            fp8_block_quantize_rows(x, _ld(x), M, self.K, self.xq, self._kp, self.x_scale, self._mp,
                                     self.xqt, self._mp, self.xst, _up(self.K, 4), stream)
         else:
-            fp8_block_quantize_rows(x, _ld(x), M, self.K, self.xq, self._kp, self.xs, self._mp,
+            fp8_block_quantize_rows(x, _ld(x), M, self.K, self.xq, self._kp, self.x_scale, self._mp,
                                     stream=stream)
-        fp8_block_gemm(self.xq, self._kp, self.xs, self._mp, self.wq, self._kp, self.ws, self.kb,
+        fp8_block_gemm(self.xq, self._kp, self.x_scale, self._mp, self.wq, self._kp, self.w_scale, self.kb,
                        1, self.y, self.N, 0, M, self.N, self.K, self.err, stream)
         self.M = M
-        return self.y[:M]
+        return _first(self.y, M)
 
     def backward(self, dy, stream=None):
         """dy bf16 [M, N] of the last forward's rows -> (dx bf16 [M, K], dw bf16 [N, K])."""
@@ -776,4 +783,4 @@ class Fp8Linear:
         fp8_block_gemm(self.dyqt, self._mp, self.dyst, _up(self.N, 4), self.xqt, self._mp,
                        self.xst, _up(self.K, 4), 0, self.dw, self.K, 0, self.N, self.K, M,
                        self.err, stream)
-        return self.dx[:M], self.dw
+        return _first(self.dx, M), self.dw

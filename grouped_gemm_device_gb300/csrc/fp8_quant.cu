@@ -63,8 +63,12 @@ MOE_DEVICE uint4 load8(const uint16_t* row, int64_t c, int64_t N, bool vec) {
 
 // Rows alone: a warp takes 512 columns (16 a lane, eight lanes a block) of kRows rows.
 constexpr int kRows = 4;
+constexpr unsigned kFewBlocks = 64;
 __global__ void __launch_bounds__(kThreads) fp8_quantize_rows_kernel(const QuantArgs a) {
   MOE_GRIDDEP_ENTRY();
+  // a few rows: the product that follows may set itself up meanwhile (with many, its CTAs would
+  // take shared memory from blocks still to come)
+  if (gridDim.x <= kFewBlocks) griddep_launch_dependents();
   const int lane = threadIdx.x & 31;
   const int64_t segs = (a.N + 511) / 512, groups = (a.M + kRows - 1) / kRows;
   const int64_t step = (int64_t)gridDim.x * (kThreads / 32);
@@ -284,9 +288,10 @@ __global__ void __launch_bounds__(kThreads, 3) fp8_quantize_kernel(const QuantAr
 template <bool ROW, bool COL, bool SQUARE>
 cudaError_t launch_quant(const QuantArgs& a, cudaStream_t s) {
   const int64_t most = (int64_t)std::max(device_sms(), 1) * 16;
-  fp8_quantize_kernel<ROW, COL, SQUARE><<<(unsigned)std::min(a.tiles, most), kThreads, 0, s>>>(a);
+  cudaError_t e = launch_pdl(fp8_quantize_kernel<ROW, COL, SQUARE>,
+                             (unsigned)std::min(a.tiles, most), kThreads, 0, s, 1, a);
   count_launch(s, MOE_K_FP8_QUANTIZE);
-  return cudaGetLastError();
+  return e;
 }
 
 bool aligned_to(const void* p, int64_t ld, int bytes) {
@@ -338,9 +343,9 @@ moe_status_t fp8_block_quantize_rows(const void* x, int64_t ldx, int64_t M, int6
     const int64_t warps = (N + 511) / 512 * ((M + kRows - 1) / kRows);
     const int64_t most = (int64_t)std::max(device_sms(), 1) * 32;
     const int64_t blocks = std::min((warps + kThreads / 32 - 1) / (kThreads / 32), most);
-    fp8_quantize_rows_kernel<<<(unsigned)blocks, kThreads, 0, s>>>(a);
+    cudaError_t e =
+        launch_pdl(fp8_quantize_rows_kernel, (unsigned)blocks, kThreads, 0, s, 1, a);
     count_launch(s, MOE_K_FP8_QUANTIZE);
-    cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return cuda_fail(e, "fp8 quantiser launch");
     return MOE_OK;
   }

@@ -205,7 +205,6 @@ MOE_DEVICE void tile_at(const Fp8Args& p, int tile, int& p0, int& q0) {
 template <int BN, bool QV>
 __global__ void __launch_bounds__(Smem<BN>::THREADS, 1)
     fp8_gemm_kernel(const __grid_constant__ Fp8Args p) {
-  MOE_GRIDDEP_ENTRY();
   using L = Smem<BN>;
   constexpr int STAGES = L::STAGES, BUFS = L::BUFS, SLOTS = L::SLOTS;
   constexpr int CW = L::CW, CH = CW < 32 ? CW : 32;  // columns a warp holds, a TMEM load takes
@@ -247,6 +246,7 @@ __global__ void __launch_bounds__(Smem<BN>::THREADS, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = c.tmem_base;
+  MOE_GRIDDEP_ENTRY();  // the setup above touches no global memory
 
   if (warp < kLeadWarps) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(L::LEAD_REGS));
@@ -568,14 +568,9 @@ cudaError_t launch_gemm(Fp8Args& a, const Operand& P, const Operand& Q, cudaStre
   if (e != cudaSuccess) return e;
   const int tiles = a.tiles_p * a.tiles_q;
   const int sms = std::max(device_sms(), 1);
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = (unsigned)a.split;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
   const int grid = a.split > 1 ? tiles * a.split : std::min(tiles, sms);
-  e = launch_kernel(kern, dim3((unsigned)grid), dim3(Smem<BN>::THREADS), Smem<BN>::TOTAL, s, attr,
-                    a.split > 1 ? 1 : 0, a);
+  e = launch_pdl(kern, dim3((unsigned)grid), dim3(Smem<BN>::THREADS), Smem<BN>::TOTAL, s, a.split,
+                 a);
   count_launch(s, MOE_K_FP8_GEMM);
   return e;
 }

@@ -351,19 +351,14 @@ moe_status_t moe_grad_clip(int32_t n, const void* const* grads, void* const* out
     i = fill_batch(b, i, n, grads, outs, numel, dtypes);
     if (b.n == 0) break;
     const int grid = std::min(clip_blocks(grad_norm_kernel, b.chunks), most);
-    if (nparts == 0) {
-      grad_norm_kernel<<<grid, kThreads, 0, s>>>(b, part);
-      e = cudaGetLastError();
-    } else {
-      e = launch_chained(grad_norm_kernel, grid, kThreads, 0, s, b, part + nparts);
-    }
+    e = launch_pdl(grad_norm_kernel, grid, kThreads, 0, s, 1, b, part + nparts);
     count_launch(s, MOE_K_GRAD_NORM);
     if (e != cudaSuccess) return cuda_fail(e, "gradient norm launch");
     nparts += grid;
     ++batches;
   }
   if (batches > 1) {
-    e = launch_chained(grad_total_kernel, 1, kThreads, 0, s, (const Sum*)part, nparts,
+    e = launch_pdl(grad_total_kernel, 1, kThreads, 0, s, 1, (const Sum*)part, nparts,
                        part + kMaxParts);
     count_launch(s, MOE_K_GRAD_NORM);
     if (e != cudaSuccess) return cuda_fail(e, "gradient norm total launch");
@@ -376,7 +371,7 @@ moe_status_t moe_grad_clip(int32_t n, const void* const* grads, void* const* out
     i = fill_batch(b, i, n, grads, outs, numel, dtypes);
     if (b.n == 0 && written > 0) break;
     const int grid = apply ? clip_blocks(grad_scale_kernel, b.chunks) : 1;
-    e = launch_chained(grad_scale_kernel, grid, kThreads, 0, s, b, (const Sum*)part, nparts,
+    e = launch_pdl(grad_scale_kernel, grid, kThreads, 0, s, 1, b, (const Sum*)part, nparts,
                        max_norm, apply ? 1 : 0, in_place ? 1 : 0, written == 0 ? norm : nullptr);
     count_launch(s, MOE_K_GRAD_SCALE);
     if (e != cudaSuccess) return cuda_fail(e, "gradient scale launch");

@@ -36,22 +36,28 @@ cudaError_t launch_kernel(void (*k)(KArgs...), dim3 grid, dim3 block, size_t sme
   cfg.numAttrs = n;
   return cudaLaunchKernelEx(&cfg, k, std::forward<Args>(args)...);
 }
-// Launch `k` as a later kernel of the same call: with programmatic stream serialization, so that
-// its CTAs are scheduled while the call's previous kernel finishes. `k` starts with
-// MOE_GRIDDEP_ENTRY, so it touches memory only after that kernel has completed.
+// Launch `k` with programmatic stream serialization always on (the operators without a layer
+// description): its CTAs are scheduled while the stream's previous kernel finishes. Every thread
+// of `k` passes MOE_GRIDDEP_ENTRY before it touches global memory, so it sees that kernel's
+// results, and through that kernel's own wait those of all earlier ones. cluster > 1: CTAs a
+// cluster.
 template <typename... KArgs, typename... Args>
-cudaError_t launch_chained(void (*k)(KArgs...), dim3 grid, dim3 block, size_t smem,
-                           cudaStream_t s, Args&&... args) {
+cudaError_t launch_pdl(void (*k)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t s,
+                       int cluster, Args&&... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = block;
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, k, std::forward<Args>(args)...);
 }
 // host-side helpers of the C entry points (api.cu): record this thread's error message and return

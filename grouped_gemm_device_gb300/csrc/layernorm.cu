@@ -557,17 +557,17 @@ struct LnArgs {
 };
 
 template <typename XT, typename WT, int VEC, int G, int PER, int RP = 1>
-void fwd_launch(const LnArgs& a) {
+cudaError_t fwd_launch(const LnArgs& a) {
   constexpr int B = G < 128 ? 128 : G, rows = B / G * RP;
   const int64_t blocks = (a.M + rows - 1) / rows;
-  ln_fwd_kernel<XT, WT, VEC, G, PER, RP><<<(unsigned)blocks, B, 0, a.s>>>(
-      static_cast<const XT*>(a.x), a.ldx, static_cast<const WT*>(a.gamma),
-      static_cast<const WT*>(a.beta), static_cast<XT*>(a.y), a.ldy, a.mean, a.rstd, a.M, (int)a.N,
-      a.eps);
+  return launch_pdl(ln_fwd_kernel<XT, WT, VEC, G, PER, RP>, (unsigned)blocks, B, 0, a.s, 1,
+                    static_cast<const XT*>(a.x), a.ldx, static_cast<const WT*>(a.gamma),
+                    static_cast<const WT*>(a.beta), static_cast<XT*>(a.y), a.ldy, a.mean, a.rstd,
+                    a.M, (int)a.N, a.eps);
 }
 
 template <typename XT, typename WT>
-void fwd_typed(const LnArgs& a) {
+cudaError_t fwd_typed(const LnArgs& a) {
   constexpr int V = 16 / sizeof(XT);
   // Weights wider than the rows cost more L1 reads than the rows: two rows share them (16384 x
   // 2880 bf16 rows, fp32 weights: 35.4 us against 42.7). With equal types the registers of a
@@ -607,10 +607,10 @@ void fwd_typed(const LnArgs& a) {
     if (N <= 1024 * 16) return fwd_launch<XT, WT, 1, 1024, 16>(a);
   }
   const int grid = (int)std::min<int64_t>(a.M, (int64_t)std::max(device_sms(), 1) * 2);
-  ln_fwd_long_kernel<XT, WT><<<grid, 1024, 0, a.s>>>(
-      static_cast<const XT*>(a.x), a.ldx, static_cast<const WT*>(a.gamma),
-      static_cast<const WT*>(a.beta), static_cast<XT*>(a.y), a.ldy, a.mean, a.rstd, a.M, a.N,
-      a.eps);
+  return launch_pdl(ln_fwd_long_kernel<XT, WT>, grid, 1024, 0, a.s, 1,
+                    static_cast<const XT*>(a.x), a.ldx, static_cast<const WT*>(a.gamma),
+                    static_cast<const WT*>(a.beta), static_cast<XT*>(a.y), a.ldy, a.mean, a.rstd,
+                    a.M, a.N, a.eps);
 }
 
 template <typename XT, typename WT, int VEC, int G, int PER, int S>
@@ -631,14 +631,11 @@ cudaError_t bwd_launch(LnArgs& a) {
   const int64_t fit = (int64_t)std::max(device_sms(), 1) * per_sm;
   a.nparts = (int)std::max<int64_t>(
       1, std::min<int64_t>((a.M + GROUPS - 1) / GROUPS, std::min<int64_t>(fit, max_parts(a.N))));
-  kern<<<a.nparts, B, smem, a.s>>>(static_cast<const XT*>(a.dy), a.lddy,
-                                   static_cast<const XT*>(a.x), a.ldx,
-                                   static_cast<const WT*>(a.gamma), a.mean, a.rstd,
-                                   static_cast<XT*>(a.dx), a.lddx, a.part,
-                                   static_cast<WT*>(a.dgamma), static_cast<WT*>(a.dbeta), a.M,
-                                   (int)a.N);
   a.done = a.nparts == 1;
-  return cudaGetLastError();
+  return launch_pdl(kern, a.nparts, B, smem, a.s, 1, static_cast<const XT*>(a.dy), a.lddy,
+                    static_cast<const XT*>(a.x), a.ldx, static_cast<const WT*>(a.gamma), a.mean,
+                    a.rstd, static_cast<XT*>(a.dx), a.lddx, a.part, static_cast<WT*>(a.dgamma),
+                    static_cast<WT*>(a.dbeta), a.M, (int)a.N);
 }
 
 template <typename XT, typename WT>
@@ -670,16 +667,17 @@ cudaError_t bwd_typed(LnArgs& a) {
   }
   a.nparts = (int)std::min<int64_t>(a.M, std::min<int64_t>(std::max(device_sms(), 1), max_parts(N)));
   if (a.part) {
-    ln_bwd_cols_long_kernel<XT><<<a.nparts, 256, 0, a.s>>>(
-        static_cast<const XT*>(a.dy), a.lddy, static_cast<const XT*>(a.x), a.ldx, a.mean, a.rstd,
-        a.part, a.M, a.N);
+    cudaError_t e = launch_pdl(ln_bwd_cols_long_kernel<XT>, a.nparts, 256, 0, a.s, 1,
+                               static_cast<const XT*>(a.dy), a.lddy, static_cast<const XT*>(a.x),
+                               a.ldx, a.mean, a.rstd, a.part, a.M, a.N);
     count_launch(a.s, MOE_K_LAYERNORM_BWD);
+    if (e != cudaSuccess) return e;
   }
   const int grid = (int)std::min<int64_t>(a.M, (int64_t)std::max(device_sms(), 1) * 2);
-  ln_bwd_rows_long_kernel<XT, WT><<<grid, 1024, 0, a.s>>>(
-      static_cast<const XT*>(a.dy), a.lddy, static_cast<const XT*>(a.x), a.ldx,
-      static_cast<const WT*>(a.gamma), a.mean, a.rstd, static_cast<XT*>(a.dx), a.lddx, a.M, a.N);
-  return cudaGetLastError();
+  return launch_pdl(ln_bwd_rows_long_kernel<XT, WT>, grid, 1024, 0, a.s, 1,
+                    static_cast<const XT*>(a.dy), a.lddy, static_cast<const XT*>(a.x), a.ldx,
+                    static_cast<const WT*>(a.gamma), a.mean, a.rstd, static_cast<XT*>(a.dx),
+                    a.lddx, a.M, a.N);
 }
 
 moe_status_t check_types(int64_t M, int64_t N, int32_t xd, int32_t wd) {
@@ -717,11 +715,10 @@ moe_status_t moe_layernorm_fwd(const void* x, int64_t ldx, const void* gamma, co
   a.x = x; a.ldx = ldx; a.gamma = gamma; a.beta = beta; a.y = y; a.ldy = ldy;
   a.mean = mean; a.rstd = rstd; a.M = M; a.N = N; a.eps = eps;
   a.s = reinterpret_cast<cudaStream_t>(stream);
-  if (x_dtype == MOE_DT_FP32) fwd_typed<float, float>(a);
-  else if (w_dtype == MOE_DT_FP32) fwd_typed<__nv_bfloat16, float>(a);
-  else fwd_typed<__nv_bfloat16, __nv_bfloat16>(a);
+  cudaError_t e = x_dtype == MOE_DT_FP32   ? fwd_typed<float, float>(a)
+                  : w_dtype == MOE_DT_FP32 ? fwd_typed<__nv_bfloat16, float>(a)
+                                           : fwd_typed<__nv_bfloat16, __nv_bfloat16>(a);
   count_launch(a.s, MOE_K_LAYERNORM_FWD);
-  cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return cuda_fail(e, "layernorm forward launch");
   return MOE_OK;
 }
@@ -778,10 +775,10 @@ moe_status_t moe_layernorm_bwd(const void* dy, int64_t lddy, const void* x, int6
   if (weights && !a.done) {
     const unsigned grid = (unsigned)((2 * N + 31) / 32);
     if (w_dtype == MOE_DT_FP32)
-      e = launch_chained(ln_colsum_kernel<float>, grid, 1024, 0, a.s, (const float*)a.part,
+      e = launch_pdl(ln_colsum_kernel<float>, grid, 1024, 0, a.s, 1, (const float*)a.part,
                          a.nparts, N, static_cast<float*>(dgamma), static_cast<float*>(dbeta));
     else
-      e = launch_chained(ln_colsum_kernel<__nv_bfloat16>, grid, 1024, 0, a.s,
+      e = launch_pdl(ln_colsum_kernel<__nv_bfloat16>, grid, 1024, 0, a.s, 1,
                          (const float*)a.part, a.nparts, N, static_cast<__nv_bfloat16*>(dgamma),
                          static_cast<__nv_bfloat16*>(dbeta));
     count_launch(a.s, MOE_K_LAYERNORM_REDUCE);

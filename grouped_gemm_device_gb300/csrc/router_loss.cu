@@ -156,7 +156,7 @@ __global__ void __launch_bounds__(kLossThreads) router_loss_kernel(
 
 // Sums the blocks' partials in a fixed order and forms the loss: one cluster, CTA c for experts
 // 32 c .., its warp w for every eighth partial.
-__global__ void __launch_bounds__(256) __cluster_dims__(kFinishCtas, 1, 1)
+__global__ void __launch_bounds__(256)
     router_loss_finish_kernel(const Partial* __restrict__ part, int nblk, int E, int k, float coef,
                               float* loss, int32_t* counts, float* mean_prob, int32_t* n_valid) {
   MOE_GRIDDEP_ENTRY();
@@ -401,15 +401,15 @@ moe_status_t moe_router_loss_fwd(const float* logits, int64_t ld_logits, const i
   const RowMap m = row_map(E, E % 4 == 0 && ld_logits % 4 == 0 && a16(logits));
   const int nblk = router_blocks(T, m, kLossWarps, std::min(std::max(device_sms(), 1), kMaxBlocks));
   Partial* part = static_cast<Partial*>(ws);
+  cudaError_t e = cudaSuccess;
   with_map(m, [&](auto vec, auto v) {
-    router_loss_kernel<vec.value, v.value><<<nblk, kLossThreads, 0, s>>>(
-        logits, ld_logits, topk_ids, token_mask, T, E, k, m.L, part);
+    e = launch_pdl(router_loss_kernel<vec.value, v.value>, nblk, kLossThreads, 0, s, 1, logits,
+                   ld_logits, topk_ids, token_mask, T, E, k, m.L, part);
   });
   count_launch(s, MOE_K_ROUTER_LOSS);
-  cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return cuda_fail(e, "router loss launch");
-  e = launch_chained(router_loss_finish_kernel, kFinishCtas, 256, 0, s, (const Partial*)part, nblk, E, k,
-                     coef, loss, counts, mean_prob, n_valid);
+  e = launch_pdl(router_loss_finish_kernel, kFinishCtas, 256, 0, s, kFinishCtas,
+                 (const Partial*)part, nblk, E, k, coef, loss, counts, mean_prob, n_valid);
   count_launch(s, MOE_K_ROUTER_LOSS);
   if (e != cudaSuccess) return cuda_fail(e, "router loss finish launch");
   return MOE_OK;
@@ -436,13 +436,13 @@ moe_status_t moe_router_loss_bwd(const float* logits, int64_t ld_logits, const i
   const RowMap m = row_map(E, E % 4 == 0 && ld_logits % 4 == 0 && ld_d % 4 == 0 && a16(logits) &&
                                   a16(d_logits));
   const int nblk = router_blocks(T, m, kWarps, std::max(device_sms(), 1) * 8);
+  cudaError_t e = cudaSuccess;
   with_map(m, [&](auto vec, auto v) {
-    router_grad_kernel<vec.value, v.value><<<nblk, kThreads, 0, s>>>(
-        logits, ld_logits, topk_ids, topk_probs, d_probs, token_mask, T, E, k, m.L, coef, d_loss,
-        counts, n_valid, d_logits, ld_d);
+    e = launch_pdl(router_grad_kernel<vec.value, v.value>, nblk, kThreads, 0, s, 1, logits,
+                   ld_logits, topk_ids, topk_probs, d_probs, token_mask, T, E, k, m.L, coef,
+                   d_loss, counts, n_valid, d_logits, ld_d);
   });
   count_launch(s, MOE_K_ROUTER_GRAD);
-  cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return cuda_fail(e, "router gradient launch");
   return MOE_OK;
 }
