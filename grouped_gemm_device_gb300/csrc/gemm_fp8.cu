@@ -16,8 +16,11 @@
 //   Few rows (M <= 128): P = b, Q = a (BN = M rounded up), so that the whole 128-row side is
 //   filled with features and the small operand costs what it holds; the result is written
 //   transposed, one feature a lane.
-//   Few tiles: the k-blocks are split over a cluster of 2-8 CTAs, whose sums are added through
-//   distributed shared memory in the order of their ranks.
+//   Tiles that do not fill the GPU (all of them, or those of the last round): the k-blocks are
+//   split over a cluster of 2-8 CTAs, whose sums are added through distributed shared memory in
+//   the order of their ranks.
+#include <mutex>
+
 #include "gemm_common.cuh"
 
 namespace moe {
@@ -32,19 +35,20 @@ constexpr int kMaxSplit = 8;
 
 struct Fp8Args {
   CUtensorMap tmP, tmQ;    // codes [rows, K]
-  CUtensorMap tmSP, tmSQ;  // 1 x 128 scales [k-blocks, rows] (those that are vectors)
-  const float* sp;         // 128 x 128 scales of P, [ceil(rows/128), k-blocks] (sp_vec = 0)
-  const float* sq;         // 128 x 128 scales of Q (QV = 0)
+  CUtensorMap tmSP, tmSQ;  // 1 x 128 scales [k-blocks, rows] (PV, QV)
+  const float* sp;         // 128 x 128 scales of P, [ceil(rows/128), k-blocks] (not PV)
+  const float* sq;         // the same of Q (not QV)
   int64_t ld_sp, ld_sq;
-  int sp_vec;
   int swapped;             // P = b, Q = a: C[q][p]
   void* c;
   int64_t ldc;
   int c_fp32;
-  int align;               // bytes every row of C is aligned to (16 or 32), or 0
+  int align;               // bytes every row of C is aligned to (8, 16 or 32), or less
   int rows_p, rows_q, K;
   int tiles_p, tiles_q;
-  int split;               // CTAs of a cluster that share one tile's k-blocks
+  // Every CTA takes `rounds` whole tiles; the `rem` tiles left go to one CTA each or, with
+  // split > 1, to one cluster of that many CTAs each, which share the tile's k-blocks.
+  int rounds, rem, split;
   int* err;
 };
 
@@ -133,10 +137,8 @@ MOE_DEVICE void tmem_ld(uint32_t taddr, uint32_t (&r)[W]) {
   else tmem_ld_32x32b_x8(taddr, r);
 }
 
-MOE_DEVICE float ld_shared_cluster(uint32_t addr) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
-  return v;
+MOE_DEVICE void st_shared_cluster(uint32_t addr, float v) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
 
 // W consecutive results of one row.
@@ -144,7 +146,7 @@ template <int W>
 MOE_DEVICE void store_row(const Fp8Args& p, int64_t row, int col, const float (&v)[W]) {
   if (p.c_fp32) {
     float* o = static_cast<float*>(p.c) + row * p.ldc + col;
-    if (p.align && col + W <= p.rows_q) {
+    if (p.align >= 16 && col + W <= p.rows_q) {
 #pragma unroll
       for (int i = 0; i < W; i += 8) {
         uint32_t w[8];
@@ -164,7 +166,7 @@ MOE_DEVICE void store_row(const Fp8Args& p, int64_t row, int col, const float (&
     }
   } else {
     __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.c) + row * p.ldc + col;
-    if (p.align && col + W <= p.rows_q) {
+    if (p.align >= 16 && col + W <= p.rows_q) {
 #pragma unroll
       for (int i = 0; i < W; i += 16) {
         uint32_t w[8];
@@ -202,24 +204,53 @@ MOE_DEVICE void tile_at(const Fp8Args& p, int tile, int& p0, int& q0) {
   q0 = (in / rows) * BN;
 }
 
-template <int BN, bool QV>
+// Four consecutive rows of P of the swapped form.
+MOE_DEVICE void store_swapped4(const Fp8Args& p, int prow, int64_t qrow, float4 v) {
+  const float x[4] = {v.x, v.y, v.z, v.w};
+  if (p.align >= (p.c_fp32 ? 16 : 8) && prow + 4 <= p.rows_p) {
+    if (p.c_fp32)
+      *reinterpret_cast<float4*>(static_cast<float*>(p.c) + qrow * p.ldc + prow) = v;
+    else
+      *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.c) + qrow * p.ldc + prow) =
+          make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (prow + i < p.rows_p) store_swapped(p, prow + i, qrow, x[i]);
+  }
+}
+
+// PV, QV: P and Q have 1 x 128 scales; otherwise 128 x 128.
+template <int BN, bool PV, bool QV>
 __global__ void __launch_bounds__(Smem<BN>::THREADS, 1)
     fp8_gemm_kernel(const __grid_constant__ Fp8Args p) {
   using L = Smem<BN>;
   constexpr int STAGES = L::STAGES, BUFS = L::BUFS, SLOTS = L::SLOTS;
-  constexpr int CW = L::CW, CH = CW < 32 ? CW : 32;  // columns a warp holds, a TMEM load takes
+  // columns a warp holds, and a TMEM load takes (with Q's scales beside them, half as many)
+  constexpr int CW = L::CW, CH = CW < (QV ? 16 : 32) ? CW : (QV ? 16 : 32);
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_addr = smem_u32(smem_raw);
   uint8_t* smem = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
   Ctrl& c = *reinterpret_cast<Ctrl*>(smem + L::CTRL_OFF);
   volatile int* abort = &c.abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rank = p.split > 1 ? (int)cluster_ctarank() : 0;
-  const int total = p.tiles_p * p.tiles_q;
-  const int tile0 = (int)blockIdx.x / p.split, tstep = (int)gridDim.x / p.split;
-  const int nkb_all = (p.K + BK - 1) / BK;
-  const int kb0 = (int)((int64_t)nkb_all * rank / p.split);
-  const int kb1 = (int)((int64_t)nkb_all * (rank + 1) / p.split);
+  const int nkb = (p.K + BK - 1) / BK;
+  const int cluster = (int)blockIdx.x / p.split;
+  const bool tail_split = p.split > 1 && cluster < p.rem;  // the same in a whole cluster
+  // The it-th piece of work of this CTA: a tile and its k-blocks [k0, k1).
+  auto unit = [&](int it, int& tile, int& k0, int& k1) {
+    k0 = 0;
+    k1 = nkb;
+    tile = it * (int)gridDim.x + (int)blockIdx.x;
+    if (it < p.rounds) return true;
+    if (it > p.rounds) return false;
+    if (p.split == 1) return (int)blockIdx.x < p.rem;
+    const int rank = (int)blockIdx.x - cluster * p.split;
+    tile = it * (int)gridDim.x + cluster;
+    k0 = (int)((int64_t)nkb * rank / p.split);
+    k1 = (int)((int64_t)nkb * (rank + 1) / p.split);
+    return tail_split;
+  };
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
@@ -253,12 +284,13 @@ __global__ void __launch_bounds__(Smem<BN>::THREADS, 1)
     if (warp == 0) {
       // ------------------------------------------------------------ TMA producer
       if (lane == 0) {
-        const uint32_t tx = L::STAGE + (p.sp_vec ? L::SP_BYTES : 0) + (QV ? BN * 4 : 0);
+        constexpr uint32_t tx = L::STAGE + (PV ? L::SP_BYTES : 0) + (QV ? BN * 4 : 0);
         int stage = 0, slot = 0;
         uint32_t phase = 0;
         int64_t loaded = 0;  // k-blocks
         bool ok = true;
-        for (int tile = tile0; ok && tile < total; tile += tstep) {
+        int tile, kb0, kb1;
+        for (int it = 0; ok && unit(it, tile, kb0, kb1); ++it) {
           int p0, q0;
           tile_at<BN>(p, tile, p0, q0);
           for (int kb = kb0; kb < kb1; ++kb) {
@@ -273,7 +305,7 @@ __global__ void __launch_bounds__(Smem<BN>::THREADS, 1)
             ++loaded;
             tma_load_2d(sP, &p.tmP, bar, kb * BK, p0);
             tma_load_2d(sP + L::P_BYTES, &p.tmQ, bar, kb * BK, q0);
-            if (p.sp_vec) tma_load_2d(sl, &p.tmSP, bar, p0, kb);
+            if (PV) tma_load_2d(sl, &p.tmSP, bar, p0, kb);
             if (QV) tma_load_2d(sl + L::SP_BYTES, &p.tmSQ, bar, q0, kb);
             if (++stage == STAGES) {
               stage = 0;
@@ -297,11 +329,12 @@ __global__ void __launch_bounds__(Smem<BN>::THREADS, 1)
       // the same in every lane, which the MMAs' uniform operands need.
       const uint32_t tmem_u = __shfl_sync(0xFFFFFFFFu, tmem_base, 0);
       const uint64_t desc_p = smem_desc_sw128(smem_u32(smem), 16, 1024);
-      const int kb_short = p.K % BK ? nkb_all - 1 : -1;
+      const int kb_short = p.K % BK ? nkb - 1 : -1;
       int stage = 0, buf = 0;
       uint32_t phase = 0, tphase = 0;
       bool ok = true, issued = false;
-      for (int tile = tile0; ok && tile < total; tile += tstep) {
+      int tile, kb0, kb1;
+      for (int it = 0; ok && unit(it, tile, kb0, kb1); ++it) {
         for (int kb = kb0; kb < kb1; ++kb) {
           const bool got = mbar_wait(&c.tempty[buf], tphase ^ 1, abort, p.err) &&
                            mbar_wait(&c.full[stage], phase, abort, p.err);
@@ -351,7 +384,7 @@ __global__ void __launch_bounds__(Smem<BN>::THREADS, 1)
       }
       __syncwarp();
     }
-    if (p.split > 1) {  // the epilogue warps' two cluster barriers
+    if (tail_split) {  // the epilogue warps' two cluster barriers
       cluster_sync_all();
       cluster_sync_all();
     }
@@ -362,7 +395,10 @@ __global__ void __launch_bounds__(Smem<BN>::THREADS, 1)
     const int row = q * 32 + lane;  // of the tile's P side
     constexpr int NC = CW / CH;     // TMEM loads a k-block
     const uint32_t tacc = tmem_base + c0 + ((uint32_t)(q * 32) << 16);
-    int buf = 0, slot = 0;
+    constexpr bool kBlocks = !PV || !QV;  // one side has a number a k-block
+    const float* const slots = reinterpret_cast<const float*>(smem + L::SLOT_OFF);
+    const float* sl = slots;  // the next k-block's slot
+    int buf = 0;
     uint32_t tphase = 0;
     uint32_t r[2][CH];
     auto free_buffer = [&]() {  // its sums and scales have been read
@@ -374,60 +410,80 @@ __global__ void __launch_bounds__(Smem<BN>::THREADS, 1)
         tphase ^= 1;
       }
     };
-    // Waits for the next k-block and starts its first load. A wait that gives up has raised the
+    // Starts on the next k-block of this warp's order: waits until its product is in `buf`,
+    // starts the first load and fetches this row's scale. A wait that gives up has raised the
     // abort flag and the error word; the warps go on through their loops with undefined sums
     // (every later wait then returns at once), so no branch depends on it.
-    auto next_block = [&]() {
+    auto start_block = [&](float& f, const float*& sqv) {
       mbar_wait(&c.tfull[buf], tphase, abort, p.err);
       __syncwarp();
       tc_fence_after();
       tmem_ld(tacc + buf * BN, r[0]);
+      f = PV ? sl[row] : 1.0f;
+      sqv = sl + L::SP_BYTES / 4 + c0;
+      sl += L::SLOT / 4;
+      if (sl == slots + SLOTS * (L::SLOT / 4)) sl = slots;
     };
-    for (int tile = tile0; tile < total; tile += tstep) {
+    int tile, kb0, kb1;
+    for (int it = 0; unit(it, tile, kb0, kb1); ++it) {
       __syncwarp();  // rows past the end left the last tile early
       int p0, q0;
       tile_at<BN>(p, tile, p0, q0);
       // Scales that are one number a k-block for these rows and columns (P's blocks when it has
       // no vector, times Q's): lane l holds that of k-block base + l. A column group past the
       // last column reads the last block's and stores nothing.
-      const float* sp_at = p.sp_vec ? nullptr : p.sp + (int64_t)(p0 >> 7) * p.ld_sp;
+      const float* sp_at = PV ? nullptr : p.sp + (int64_t)(p0 >> 7) * p.ld_sp;
       const float* sq_at =
           QV ? nullptr : p.sq + (int64_t)(min(q0 + c0, p.rows_q - 1) >> 7) * p.ld_sq;
       auto block_scales = [&](int base) {
         const int kb = min(base + lane, kb1 - 1);
-        return (sp_at ? __ldg(sp_at + kb) : 1.0f) * (sq_at ? __ldg(sq_at + kb) : 1.0f);
+        return (PV ? 1.0f : __ldg(sp_at + kb)) * (QV ? 1.0f : __ldg(sq_at + kb));
       };
-      float bs = block_scales(kb0);
+      float bs = kBlocks ? block_scales(kb0) : 1.0f, bs_next = 1.0f, f_next;
+      const float* sq_next;
       float acc[CW];
 #pragma unroll
       for (int i = 0; i < CW; ++i) acc[i] = 0.f;
-      next_block();
+      start_block(f_next, sq_next);
       for (int kb = kb0; kb < kb1; ++kb) {
+        float f = f_next;
+        const float* sqv = sq_next;
+        const bool more = kb + 1 < kb1;
         const int at = (kb - kb0) & 31;
-        if (at == 0 && kb > kb0) bs = block_scales(kb);
-        float f = __shfl_sync(0xFFFFFFFFu, bs, at);
-        const float* sl = reinterpret_cast<const float*>(smem + L::SLOT_OFF + slot * L::SLOT);
-        if (p.sp_vec) f *= sl[row];
-        const float* sqv = sl + L::SP_BYTES / 4 + c0;
-        if (++slot == SLOTS) slot = 0;
+        float fb = 1.0f;
+        if constexpr (kBlocks) {
+          if (at == 0 && kb + 32 < kb1) bs_next = block_scales(kb + 32);  // one batch ahead
+          fb = __shfl_sync(0xFFFFFFFFu, bs, at);
+          if (at == 31) bs = bs_next;
+        }
 #pragma unroll
         for (int j = 0; j < NC; ++j) {
+          float4 s4[QV ? CH / 4 : 1];
+          if constexpr (QV) {
+#pragma unroll
+            for (int i = 0; i < CH / 4; ++i)
+              s4[i] = reinterpret_cast<const float4*>(sqv + j * CH)[i];
+          }
           tmem_wait(r[j & 1]);
+          if (j == 0) {
+            // the scale's load is waited for here, not where it was issued
+            asm volatile("" : "+f"(f));
+            f *= fb;
+          }
           if (j + 1 < NC) {
             tmem_ld(tacc + buf * BN + (j + 1) * CH, r[(j + 1) & 1]);
           } else {
             free_buffer();
             // the next k-block's first load, before this one's last columns are added (an odd
             // number of loads a k-block would put it into the registers being added)
-            if (NC % 2 == 0 && kb + 1 < kb1) next_block();
+            if (NC % 2 == 0 && more) start_block(f_next, sq_next);
           }
 #pragma unroll
           for (int i = 0; i < CH; i += 4) {
             float2 g0 = make_float2(f, f), g1 = g0;
-            if (QV) {
-              const float4 s4 = *reinterpret_cast<const float4*>(sqv + j * CH + i);
-              g0 = __fmul2_rn(g0, make_float2(s4.x, s4.y));
-              g1 = __fmul2_rn(g1, make_float2(s4.z, s4.w));
+            if constexpr (QV) {
+              g0 = __fmul2_rn(g0, make_float2(s4[i / 4].x, s4[i / 4].y));
+              g1 = __fmul2_rn(g1, make_float2(s4[i / 4].z, s4[i / 4].w));
             }
             float* o = &acc[j * CH + i];
             const uint32_t* x = &r[j & 1][i];
@@ -440,15 +496,27 @@ __global__ void __launch_bounds__(Smem<BN>::THREADS, 1)
             o[2] = a1.x;
             o[3] = a1.y;
           }
-          if (NC % 2 == 1 && j + 1 == NC && kb + 1 < kb1) next_block();
+          if (NC % 2 == 1 && j + 1 == NC && more) start_block(f_next, sq_next);
         }
       }
-      if (p.split > 1) {
-        // this CTA's sums, column by column, where the stages were (every load has been used)
-        float* st = reinterpret_cast<float*>(smem) + c0 * BM + row;
+      if (tail_split && it == p.rounds) {
+        // Rank o adds up columns [o BN / split, (o + 1) BN / split): every CTA sends it its sums of
+        // them (pushed: reading them from the other side measured 10 bytes a cycle), to
+        // [rank][column][row] where the stages were, once every CTA is done with its stages.
+        const int per = BN / p.split, lg = 31 - __clz(per);  // a power of two
+        const uint32_t mine = smem_u32(smem) + (cluster_ctarank() * per * BM + row) * 4;
+        constexpr int RUN = BN >= 64 ? 8 : 2;  // columns that surely have one owner
+        __syncwarp();
+        cluster_sync_all();
 #pragma unroll
-        for (int i = 0; i < CW; ++i) st[i * BM] = acc[i];
-        break;  // one tile a cluster
+        for (int i = 0; i < CW; i += RUN) {
+          const int owner = (c0 + i) >> lg;
+          const uint32_t to =
+              mapa_shared(mine + (uint32_t)(c0 + i - (owner << lg)) * (BM * 4), (uint32_t)owner);
+#pragma unroll
+          for (int j = 0; j < RUN; ++j) st_shared_cluster(to + j * (BM * 4), acc[i + j]);
+        }
+        break;  // the last of its work
       }
       if (p0 + row >= p.rows_p) continue;
       if (p.swapped) {
@@ -470,50 +538,48 @@ __global__ void __launch_bounds__(Smem<BN>::THREADS, 1)
         }
       }
     }
-    if (p.split > 1) {
-      // rank r adds columns [r BN / split, (r + 1) BN / split) of every CTA of the cluster, in the
-      // order of the ranks, and stores them
+    if (tail_split) {
+      // the sums of this CTA's columns, in the order of the ranks
       __syncwarp();
       cluster_sync_all();
       if (!*abort) {
-        const int tid = threadIdx.x - 32 * kLeadWarps;
-        const int row = tid & 127, cg = tid >> 7;  // this thread's row, half of the columns
+        const int w = warp - kLeadWarps, per = BN / p.split;
+        const int col0 = (int)cluster_ctarank() * per;
+        const float* sums = reinterpret_cast<const float*>(smem);
         int p0, q0;
-        tile_at<BN>(p, tile0, p0, q0);
-        const int per = BN / p.split;
-        const uint32_t base = smem_u32(smem) + (uint32_t)row * 4;
-        uint32_t peer[kMaxSplit];
-#pragma unroll
-        for (int s = 0; s < kMaxSplit; ++s)
-          if (s < p.split) peer[s] = mapa_shared(base, (uint32_t)s);
-        auto sum = [&](int col) {
-          float v = 0.f;
-#pragma unroll
-          for (int s = 0; s < kMaxSplit; ++s)
-            if (s < p.split) v += ld_shared_cluster(peer[s] + (uint32_t)col * (BM * 4));
-          return v;
-        };
-        if (p0 + row < p.rows_p) {
-          if (p.swapped) {
-            const int half = per / 2;
-            for (int i = rank * per + cg * half; i < rank * per + (cg + 1) * half; ++i)
-              if (q0 + i < p.rows_q) store_swapped(p, p0 + row, q0 + i, sum(i));
-          } else {  // 16 columns of a row at a time (per >= 16)
-            for (int i = rank * per + cg * 16; i < (rank + 1) * per && q0 + i < p.rows_q; i += 32) {
-              float v[16];
-#pragma unroll
-              for (int j = 0; j < 16; ++j) v[j] = sum(i + j);
-              store_row<16>(p, p0 + row, q0 + i, v);
+        tile_at<BN>(p, tile, p0, q0);
+        if (p.swapped) {  // four rows of P a lane
+          const int prow = p0 + lane * 4;
+          for (int i = w; i < per && q0 + col0 + i < p.rows_q; i += L::EW) {
+            const float4* at = reinterpret_cast<const float4*>(sums + i * BM + lane * 4);
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+            for (int s = 0; s < p.split; ++s, at += per * (BM / 4)) {
+              const float4 x = *at;
+              v.x += x.x;
+              v.y += x.y;
+              v.z += x.z;
+              v.w += x.w;
             }
+            if (prow < p.rows_p) store_swapped4(p, prow, q0 + col0 + i, v);
+          }
+        } else {  // eight columns of a row a lane (per is a multiple of 8)
+          for (int u = w; u < 4 * (per / 8); u += L::EW) {
+            const int r = (u & 3) * 32 + lane, i = (u >> 2) * 8;
+            const float* x = sums + i * BM + r;
+            float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll 2
+            for (int s = 0; s < p.split; ++s, x += per * BM)
+#pragma unroll
+              for (int j = 0; j < 8; ++j) v[j] += x[j * BM];
+            if (p0 + r < p.rows_p && q0 + col0 + i < p.rows_q)
+              store_row<8>(p, p0 + r, q0 + col0 + i, v);
           }
         }
         __syncwarp();
       }
-      // no CTA leaves while another may read its sums
-      cluster_sync_all();
     }
   }
-
   griddep_launch_dependents();
   tc_fence_before();
   __syncthreads();
@@ -549,15 +615,76 @@ struct Operand {
   bool vec;
 };
 
-template <int BN, bool QV>
-cudaError_t launch_gemm(Fp8Args& a, const Operand& P, const Operand& Q, cudaStream_t s) {
+// Clusters of `split` CTAs of a kernel that fit the GPU at once (1: CTAs), asked once each.
+template <int BN, bool PV, bool QV>
+int resident(int split) {
+  static int cache[kMaxSplit + 1] = {0};
+  static std::mutex mu;
+  std::lock_guard<std::mutex> lock(mu);
+  if (cache[split]) return cache[split];
+  int n = std::max(device_sms(), 1);
+  if (split > 1) {
+    auto kern = fp8_gemm_kernel<BN, PV, QV>;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)split;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)split, 1, 1);
+    cfg.blockDim = dim3(Smem<BN>::THREADS, 1, 1);
+    cfg.dynamicSmemBytes = Smem<BN>::TOTAL;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (ensure_smem_attr(reinterpret_cast<const void*>(kern), Smem<BN>::TOTAL) != cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n < 1) {
+      cudaGetLastError();  // clear the sticky-free error of a failed query
+      n = 1;
+    }
+  }
+  return cache[split] = n;
+}
+
+struct Plan {
+  int rounds = 0, rem = 0, split = 1, grid = 1;
+  double ns = 1e30;
+};
+
+// How the tiles of one width are dealt out, by the time of the CTA that runs longest. A k-block of
+// a 128 x BN tile was measured at `kb_ns`; a round's first loads and last stores at about 800 ns;
+// adding up a cluster's sums at about 1200 ns and 11 ns a column of the tile.
+template <int BN, bool PV, bool QV>
+Plan plan_tiles(int64_t rows_p, int64_t rows_q, int64_t nkb) {
+  constexpr double kb_ns = QV ? (BN >= 256 ? 620 : BN >= 128 ? 354 : BN >= 64 ? 300 : 265)
+                              : (BN >= 256 ? 403 : BN >= 128 ? 286 : 262);
+  const int64_t tiles = ((rows_p + BM - 1) / BM) * ((rows_q + BN - 1) / BN);
+  Plan best;
+  for (int split = 1; split <= kMaxSplit && split <= nkb; split *= 2) {
+    const int64_t fit = resident<BN, PV, QV>(split), n = fit * split;
+    Plan p;
+    p.split = split;
+    p.rounds = (int)(tiles / n);
+    p.rem = (int)(tiles - p.rounds * n);
+    if (split > 1 && (p.rem == 0 || p.rem > fit)) continue;
+    p.grid = (int)(p.rounds ? n : (int64_t)p.rem * split);
+    p.ns = p.rounds * (nkb * kb_ns + 800);
+    if (p.rem) p.ns += (nkb + split - 1) / split * kb_ns + 800;
+    if (split > 1) p.ns += 1200 + 11 * BN;
+    if (p.ns < best.ns) best = p;
+  }
+  return best;
+}
+
+template <int BN, bool PV, bool QV>
+cudaError_t launch_gemm(Fp8Args& a, const Plan& plan, const Operand& P, const Operand& Q,
+                        cudaStream_t s) {
   const int64_t kb = (a.K + BK - 1) / BK;
   if (!tmap_codes(&a.tmP, P.q, P.rows, a.K, P.ld, BM) ||
       !tmap_codes(&a.tmQ, Q.q, Q.rows, a.K, Q.ld, BN) ||
-      (P.vec && !tmap_scales(&a.tmSP, P.s, P.rows, kb, P.ld_s, BM)) ||
+      (PV && !tmap_scales(&a.tmSP, P.s, P.rows, kb, P.ld_s, BM)) ||
       (QV && !tmap_scales(&a.tmSQ, Q.s, Q.rows, kb, Q.ld_s, BN)))
     return cudaErrorInvalidValue;
-  auto kern = fp8_gemm_kernel<BN, QV>;
+  auto kern = fp8_gemm_kernel<BN, PV, QV>;
   // the register split waits for registers that the launch must have: checked once
   static const int regs = [&] {
     cudaFuncAttributes at;
@@ -566,54 +693,42 @@ cudaError_t launch_gemm(Fp8Args& a, const Operand& P, const Operand& Q, cudaStre
   if (regs < Smem<BN>::LAUNCH_REGS) return cudaErrorInvalidConfiguration;
   cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kern), Smem<BN>::TOTAL);
   if (e != cudaSuccess) return e;
-  const int tiles = a.tiles_p * a.tiles_q;
-  const int sms = std::max(device_sms(), 1);
-  const int grid = a.split > 1 ? tiles * a.split : std::min(tiles, sms);
-  e = launch_pdl(kern, dim3((unsigned)grid), dim3(Smem<BN>::THREADS), Smem<BN>::TOTAL, s, a.split,
-                 a);
+  a.tiles_p = (int)((P.rows + BM - 1) / BM);
+  a.tiles_q = (int)((Q.rows + BN - 1) / BN);
+  a.rounds = plan.rounds;
+  a.rem = plan.rem;
+  a.split = plan.split;
+  e = launch_pdl(kern, dim3((unsigned)plan.grid), dim3(Smem<BN>::THREADS), Smem<BN>::TOTAL, s,
+                 a.split, a);
   count_launch(s, MOE_K_FP8_GEMM);
   return e;
 }
 
-struct Plan {
-  int bn, split;
-};
-
-// Tile width and split of the k-blocks for P x Q rows, by the time of the longest-running SM in
-// SM cycles: a k-block of a 128 x BN tile takes `kb_cycles` (its loads or its MMAs), a tile's
-// results and first loads about 2000 on top, adding up a cluster's sums 1500.
-Plan choose(int64_t rows_p, int64_t rows_q, int64_t nkb, bool swapped, int sms) {
-  static const int widths[5] = {16, 32, 64, 128, 256};
-  static const int kb_cycles[5] = {300, 310, 330, 380, 580};
-  Plan best = {0, 1};
-  int64_t best_t = INT64_MAX;
-  const int64_t tp = (rows_p + BM - 1) / BM;
-  for (int i = swapped ? 0 : 2; i < 5; ++i) {
-    const int64_t tiles = tp * ((rows_q + widths[i] - 1) / widths[i]);
-    for (int split = 1; split <= kMaxSplit; split *= 2) {
-      if (split > 1 && (tiles * split > sms || split > nkb || (!swapped && widths[i] / split < 16)))
-        break;
-      const int64_t waves = split > 1 ? 1 : (tiles + sms - 1) / sms;
-      const int64_t t =
-          waves * ((nkb + split - 1) / split * kb_cycles[i] + 2000) + (split > 1 ? 1500 : 0);
-      if (t < best_t) {
-        best_t = t;
-        best = {widths[i], split};
-      }
+// The widths in turn: the one whose plan ends first. Few rows take the narrowest tile that holds
+// them (swapped form); otherwise tiles of 64, 128 or 256 columns.
+template <bool PV, bool QV>
+cudaError_t launch_any(Fp8Args& a, const Operand& P, const Operand& Q, cudaStream_t s) {
+  const int64_t nkb = (a.K + BK - 1) / BK;
+  if (a.swapped) {
+    if constexpr (QV) {
+      if (Q.rows <= 16)
+        return launch_gemm<16, PV, QV>(a, plan_tiles<16, PV, QV>(P.rows, Q.rows, nkb), P, Q, s);
+      if (Q.rows <= 32)
+        return launch_gemm<32, PV, QV>(a, plan_tiles<32, PV, QV>(P.rows, Q.rows, nkb), P, Q, s);
+      if (Q.rows <= 64)
+        return launch_gemm<64, PV, QV>(a, plan_tiles<64, PV, QV>(P.rows, Q.rows, nkb), P, Q, s);
+      return launch_gemm<128, PV, QV>(a, plan_tiles<128, PV, QV>(P.rows, Q.rows, nkb), P, Q, s);
     }
+  } else if constexpr (PV) {
+    const Plan p64 = plan_tiles<64, PV, QV>(P.rows, Q.rows, nkb);
+    const Plan p128 = plan_tiles<128, PV, QV>(P.rows, Q.rows, nkb);
+    const Plan p256 = plan_tiles<256, PV, QV>(P.rows, Q.rows, nkb);
+    if (p256.ns <= p128.ns && p256.ns <= p64.ns)
+      return launch_gemm<256, PV, QV>(a, p256, P, Q, s);
+    if (p128.ns <= p64.ns) return launch_gemm<128, PV, QV>(a, p128, P, Q, s);
+    return launch_gemm<64, PV, QV>(a, p64, P, Q, s);
   }
-  return best;
-}
-
-template <bool QV>
-cudaError_t launch_width(int bn, Fp8Args& a, const Operand& P, const Operand& Q, cudaStream_t s) {
-  if constexpr (QV) {
-    if (bn == 16) return launch_gemm<16, QV>(a, P, Q, s);
-    if (bn == 32) return launch_gemm<32, QV>(a, P, Q, s);
-  }
-  if (bn == 64) return launch_gemm<64, QV>(a, P, Q, s);
-  if (bn == 128) return launch_gemm<128, QV>(a, P, Q, s);
-  return launch_gemm<256, QV>(a, P, Q, s);
+  return cudaErrorInvalidValue;  // a (Q when swapped, else P) always has 1 x 128 scales
 }
 
 }  // namespace
@@ -649,30 +764,27 @@ extern "C" moe_status_t fp8_block_gemm(const uint8_t* a, int64_t lda, const floa
   const Operand A = {a, M, lda, sa, ld_sa, true}, B = {b, N, ldb, sb, ld_sb, b_scale == 0};
   const bool swapped = M <= BM;
   const Operand &P = swapped ? B : A, &Q = swapped ? A : B;
+  if ((P.rows + BM - 1) / BM * ((Q.rows + 15) / 16) > most)
+    return fail(MOE_ERR_UNSUPPORTED, "too many tiles");
   Fp8Args p = {};
   p.sp = P.s;
   p.sq = Q.s;
   p.ld_sp = P.ld_s;
   p.ld_sq = Q.ld_s;
-  p.sp_vec = P.vec ? 1 : 0;
   p.swapped = swapped ? 1 : 0;
   p.c = c;
   p.ldc = ldc;
   p.c_fp32 = es == 4;
-  p.align = at(c, 32) && ldc * es % 32 == 0 ? 32 : at(c, 16) && ldc * es % 16 == 0 ? 16 : 0;
+  p.align = 32;
+  while (p.align > es && (!at(c, p.align) || ldc * es % p.align)) p.align /= 2;
   p.rows_p = (int)P.rows;
   p.rows_q = (int)Q.rows;
   p.K = (int)K;
   p.err = err;
-  const Plan plan = choose(P.rows, Q.rows, kb, swapped && Q.vec, std::max(device_sms(), 1));
-  p.tiles_p = (int)((P.rows + BM - 1) / BM);
-  const int64_t tiles_q = (Q.rows + plan.bn - 1) / plan.bn;
-  if (tiles_q * p.tiles_p > most) return fail(MOE_ERR_UNSUPPORTED, "too many tiles");
-  p.tiles_q = (int)tiles_q;
-  p.split = plan.split;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  cudaError_t e = Q.vec ? launch_width<true>(plan.bn, p, P, Q, s)
-                        : launch_width<false>(plan.bn, p, P, Q, s);
+  cudaError_t e = !Q.vec  ? launch_any<true, false>(p, P, Q, s)
+                  : P.vec ? launch_any<true, true>(p, P, Q, s)
+                          : launch_any<false, true>(p, P, Q, s);
   if (e != cudaSuccess) return cuda_fail(e, "fp8 gemm launch");
   return MOE_OK;
 }
