@@ -536,7 +536,9 @@ def _dtype_code(dtype) -> int:
 
 
 def _expect(t, name, dtype, shape, rows=False):
-    """A tensor argument's type, shape and strides: contiguous, or (rows) any row stride."""
+    """A tensor argument's place, type, shape and strides: contiguous, or (rows) any row stride."""
+    if not t.is_cuda:
+        raise ValueError(f"{name}: must be on the GPU")
     if t.dtype != dtype or t.shape != shape:
         raise ValueError(f"{name}: expected {dtype} {tuple(shape)}, "
                          f"got {t.dtype} {tuple(t.shape)}")
@@ -573,6 +575,10 @@ class RouterLoss:
         self.mean_prob = torch.zeros(E, dtype=torch.float32, device=dev)
         self.n_valid = torch.zeros(1, dtype=torch.int32, device=dev)
         self.d_logits = torch.empty(T_max, E, dtype=torch.float32, device=dev)
+        # the buffers' addresses, taken once: a small call's time is the host's
+        self._lib = load()
+        self._p = {n: getattr(self, n).data_ptr() for n in
+                   ("ws", "loss", "counts", "mean_prob", "n_valid", "d_logits")}
 
     def _tokens(self, logits, topk_ids, token_mask):
         import torch
@@ -591,9 +597,11 @@ class RouterLoss:
         """logits fp32 [T, E], topk_ids int32 [T, k], token_mask bool [T] (False: left out).
         Returns (loss [1], counts int32 [E], mean_prob [E])."""
         T = self._tokens(logits, topk_ids, token_mask)
-        moe_router_loss_fwd(logits, _ld(logits), topk_ids, token_mask, T, self.E, self.k,
-                            self.coef, self.loss, self.counts, self.mean_prob, self.n_valid,
-                            self.ws, self.ws_bytes, stream)
+        p = self._p
+        _check(self._lib.moe_router_loss_fwd(
+            logits.data_ptr(), _ld(logits), topk_ids.data_ptr(), _ptr(token_mask), T, self.E,
+            self.k, self.coef, p["loss"], p["counts"], p["mean_prob"], p["n_valid"], p["ws"],
+            self.ws_bytes, _stream(stream)))
         return self.loss, self.counts, self.mean_prob
 
     def backward(self, logits, topk_ids, topk_probs=None, d_probs=None, token_mask=None,
@@ -609,9 +617,11 @@ class RouterLoss:
             _expect(d_loss, "d_loss", torch.float32, d_loss.shape)
             if d_loss.numel() != 1:
                 raise ValueError("d_loss must hold one value")
-        moe_router_loss_bwd(logits, _ld(logits), topk_ids, topk_probs, d_probs, token_mask, T,
-                            self.E, self.k, self.coef, d_loss, self.counts, self.n_valid,
-                            self.d_logits, self.E, stream)
+        p = self._p
+        _check(self._lib.moe_router_loss_bwd(
+            logits.data_ptr(), _ld(logits), topk_ids.data_ptr(), _ptr(topk_probs), _ptr(d_probs),
+            _ptr(token_mask), T, self.E, self.k, self.coef, _ptr(d_loss), p["counts"],
+            p["n_valid"], p["d_logits"], self.E, _stream(stream)))
         return _first(self.d_logits, T)
 
 
@@ -631,6 +641,8 @@ class LayerNorm:
         self.mean = torch.empty(M_max, dtype=torch.float32, device=dev)
         self.rstd = torch.empty(M_max, dtype=torch.float32, device=dev)
         self.dx = None
+        self._lib = load()
+        self._out = self.y.data_ptr(), N, self.mean.data_ptr(), self.rstd.data_ptr()
 
     def _rows(self, x, name):
         if x.dim() != 2 or x.shape[0] > self.M_max:
@@ -643,9 +655,10 @@ class LayerNorm:
     def forward(self, x, gamma=None, beta=None, stream=None):
         """Returns (y [M, N], mean [M], rstd [M])."""
         M = self._rows(x, "x")
-        moe_layernorm_fwd(x, _ld(x), self._weight(gamma, "gamma"), self._weight(beta, "beta"),
-                          self.y, self.N, self.mean, self.rstd, M, self.N, self.eps,
-                          *self._codes, stream)
+        _check(self._lib.moe_layernorm_fwd(
+            x.data_ptr(), _ld(x), _ptr(self._weight(gamma, "gamma")),
+            _ptr(self._weight(beta, "beta")), *self._out, M, self.N, self.eps, *self._codes,
+            _stream(stream)))
         return _first(self.y, M), _first(self.mean, M), _first(self.rstd, M)
 
     def backward(self, dy, x, gamma=None, mean=None, rstd=None, stream=None):
@@ -680,8 +693,8 @@ class GradClip:
         if len(self.outs) != len(self.grads):
             raise ValueError("outs must have one tensor for each gradient")
         for g, o in zip(self.grads, self.outs):
-            if not g.is_contiguous() or not o.is_contiguous():
-                raise ValueError("gradients and outs must be contiguous")
+            if not (g.is_cuda and o.is_cuda and g.is_contiguous() and o.is_contiguous()):
+                raise ValueError("gradients and outs must be on the GPU and contiguous")
             if g.dtype != o.dtype or g.shape != o.shape:
                 raise ValueError("an out differs from its gradient in type or shape")
         n = self.n = len(self.grads)
@@ -693,12 +706,14 @@ class GradClip:
         self.norm = torch.zeros(1, dtype=torch.float32, device=dev)
         self.ws_bytes = moe_grad_clip_workspace()
         self.ws = torch.empty(self.ws_bytes, dtype=torch.uint8, device=dev)
+        self._lib = load()
+        self._work = self.norm.data_ptr(), self.ws.data_ptr(), self.ws_bytes
 
     def clip(self, max_norm, stream=None):
         """Returns the norm [1] (on the device). max_norm = inf only takes the norm."""
         outs = None if max_norm == math.inf else self._out
-        moe_grad_clip(self.n, self._in, outs, self._numel, self._types, max_norm, self.norm,
-                      self.ws, self.ws_bytes, stream)
+        _check(self._lib.moe_grad_clip(self.n, self._in, outs, self._numel, self._types, max_norm,
+                                       *self._work, _stream(stream)))
         return self.norm
 
 
@@ -730,40 +745,57 @@ class Fp8Linear:
         self.y = torch.empty(M_max, N, dtype=torch.bfloat16, device=dev)
         self.err = torch.zeros(1, dtype=torch.int32, device=dev)
         self.M = None
+        self.has_weight = False
         if train:
-            self.wqt, self.wst = codes(K, self._np), scales(self.kb, self.nb)
-            self.xqt, self.xst = codes(K, self._mp), scales(mb, _up(K, 4))
-            self.dyq, self.dys = codes(M_max, self._np), scales(self.nb, self._mp)
-            self.dyqt, self.dyst = codes(N, self._mp), scales(mb, _up(N, 4))
+            self.wqt, self.wt_scale = codes(K, self._np), scales(self.kb, self.nb)
+            self.xqt, self.xt_scale = codes(K, self._mp), scales(mb, _up(K, 4))
+            self.dyq, self.dy_scale = codes(M_max, self._np), scales(self.nb, self._mp)
+            self.dyqt, self.dyt_scale = codes(N, self._mp), scales(mb, _up(N, 4))
             self.dx = torch.empty(M_max, K, dtype=torch.bfloat16, device=dev)
             self.dw = torch.empty(N, K, dtype=torch.bfloat16, device=dev)
+
+        # operands as (address of the codes, row stride, address of the scales, row stride)
+        def operand(q, s):
+            return q.data_ptr(), q.shape[1], s.data_ptr(), s.shape[1]
+
+        self._lib = load()
+        self._w, self._x = operand(self.wq, self.w_scale), operand(self.xq, self.x_scale)
+        self._none = None, 0, None, 0
+        self._xt = self._none
+        if train:
+            self._wt = operand(self.wqt, self.wt_scale)
+            self._xt = operand(self.xqt, self.xt_scale)
+            self._dy = operand(self.dyq, self.dy_scale)
+            self._dyt = operand(self.dyqt, self.dyt_scale)
 
     def set_weight(self, w, stream=None):
         """Quantise w bf16 [N, K] (both orders for training); again whenever w has changed."""
         import torch
         _expect(w, "w", torch.bfloat16, (self.N, self.K), rows=True)
-        if self.train:
-            fp8_block_quantize_weight(w, _ld(w), self.N, self.K, self.wq, self._kp, self.w_scale,
-                                      self.wqt, self._np, self.wst, stream)
-        else:
-            fp8_block_quantize_weight(w, _ld(w), self.N, self.K, self.wq, self._kp, self.w_scale,
-                                      stream=stream)
+        qt, ldqt, st, _ = self._wt if self.train else self._none
+        _check(self._lib.fp8_block_quantize_weight(w.data_ptr(), _ld(w), self.N, self.K,
+                                                   *self._w[:3], qt, ldqt, st, _stream(stream)))
+        self.has_weight = True
+
+    def _quantize(self, x, M, N, row, col, stream):
+        _check(self._lib.fp8_block_quantize_rows(x.data_ptr(), _ld(x), M, N, *row, *col, stream))
+
+    def _product(self, a, b, blocks, c, M, N, K, stream):
+        _check(self._lib.fp8_block_gemm(*a, *b, blocks, c.data_ptr(), N, 0, M, N, K,
+                                        self.err.data_ptr(), stream))
 
     def forward(self, x, stream=None):
         """x bf16 [M, K] -> y bf16 [M, N]."""
         import torch
+        if not self.has_weight:
+            raise ValueError("set_weight comes before forward")
         M = x.shape[0]
         if M > self.M_max:
             raise ValueError(f"{M} rows, but M_max is {self.M_max}")
         _expect(x, "x", torch.bfloat16, (M, self.K), rows=True)
-        if self.train:
-            fp8_block_quantize_rows(x, _ld(x), M, self.K, self.xq, self._kp, self.x_scale, self._mp,
-                                    self.xqt, self._mp, self.xst, _up(self.K, 4), stream)
-        else:
-            fp8_block_quantize_rows(x, _ld(x), M, self.K, self.xq, self._kp, self.x_scale, self._mp,
-                                    stream=stream)
-        fp8_block_gemm(self.xq, self._kp, self.x_scale, self._mp, self.wq, self._kp, self.w_scale, self.kb,
-                       1, self.y, self.N, 0, M, self.N, self.K, self.err, stream)
+        stream = _stream(stream)
+        self._quantize(x, M, self.K, self._x, self._xt, stream)
+        self._product(self._x, self._w, 1, self.y, M, self.N, self.K, stream)
         self.M = M
         return _first(self.y, M)
 
@@ -776,11 +808,8 @@ class Fp8Linear:
         _expect(dy, "dy", torch.bfloat16, (M, self.N), rows=True)
         if M == 0:
             return self.dx[:0], self.dw.zero_()
-        fp8_block_quantize_rows(dy, _ld(dy), M, self.N, self.dyq, self._np, self.dys, self._mp,
-                                self.dyqt, self._mp, self.dyst, _up(self.N, 4), stream)
-        fp8_block_gemm(self.dyq, self._np, self.dys, self._mp, self.wqt, self._np, self.wst,
-                       self.nb, 1, self.dx, self.K, 0, M, self.K, self.N, self.err, stream)
-        fp8_block_gemm(self.dyqt, self._mp, self.dyst, _up(self.N, 4), self.xqt, self._mp,
-                       self.xst, _up(self.K, 4), 0, self.dw, self.K, 0, self.N, self.K, M,
-                       self.err, stream)
+        stream = _stream(stream)
+        self._quantize(dy, M, self.N, self._dy, self._dyt, stream)
+        self._product(self._dy, self._wt, 1, self.dx, M, self.K, self.N, stream)
+        self._product(self._dyt, self._xt, 0, self.dw, self.N, self.K, M, stream)
         return _first(self.dx, M), self.dw

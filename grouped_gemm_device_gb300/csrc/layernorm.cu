@@ -240,7 +240,8 @@ __global__ void __launch_bounds__(1024) ln_fwd_long_kernel(
     }
     for (int64_t c = threadIdx.x; c < N; c += 1024) {
       const float h = (to_f(xr[c]) - mean) * rstd;
-      y[row * ldy + c] = from_f<XT>((gamma ? h * to_f(gamma[c]) : h) + (beta ? to_f(beta[c]) : 0.f));
+      const float o = (gamma ? h * to_f(gamma[c]) : h) + (beta ? to_f(beta[c]) : 0.f);
+      y[row * ldy + c] = from_f<XT>(o);
     }
   }
 }
@@ -665,7 +666,8 @@ cudaError_t bwd_typed(LnArgs& a) {
     if (N <= 512 * 8) return bwd_launch<XT, WT, 1, 512, 8, 1>(a);
     if (N <= 512 * 32) return bwd_launch<XT, WT, 1, 512, 32, 1>(a);
   }
-  a.nparts = (int)std::min<int64_t>(a.M, std::min<int64_t>(std::max(device_sms(), 1), max_parts(N)));
+  const int64_t most = std::min<int64_t>(std::max(device_sms(), 1), max_parts(N));
+  a.nparts = (int)std::min<int64_t>(a.M, most);
   if (a.part) {
     cudaError_t e = launch_pdl(ln_bwd_cols_long_kernel<XT>, a.nparts, 256, 0, a.s, 1,
                                static_cast<const XT*>(a.dy), a.lddy, static_cast<const XT*>(a.x),

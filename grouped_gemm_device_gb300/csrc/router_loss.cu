@@ -88,10 +88,26 @@ MOE_DEVICE float softmax_row(float (&v)[V * VEC], int E, int L, int sub) {
   return 1.0f / group_sum(s, L);
 }
 
+struct Results {
+  float* loss;
+  int32_t* counts;
+  float* mean_prob;
+  int32_t* n_valid;
+  float coef;
+};
+// Writes an expert's count and mean probability; returns its term of the loss.
+MOE_DEVICE float finish_expert(int e, float p, int c, int n, int E, int k, const Results& out) {
+  const float mp = n > 0 ? p / (float)n : 0.f;
+  out.mean_prob[e] = mp;
+  out.counts[e] = c;
+  return n > 0 ? mp * ((float)E * (float)c / ((float)k * (float)n)) : 0.f;
+}
+
 template <int VEC, int V>
 __global__ void __launch_bounds__(kLossThreads) router_loss_kernel(
     const float* __restrict__ logits, int64_t ld, const int32_t* __restrict__ ids,
-    const uint8_t* __restrict__ mask, int T, int E, int k, int L, Partial* __restrict__ part) {
+    const uint8_t* __restrict__ mask, int T, int E, int k, int L, Partial* __restrict__ part,
+    const Results out) {
   MOE_GRIDDEP_ENTRY();
   __shared__ int hist[257];
   __shared__ float psum[kLossWarps][256];
@@ -140,25 +156,41 @@ __global__ void __launch_bounds__(kLossThreads) router_loss_kernel(
   }
   if (valid) atomicAdd(&hist[E], valid);
   __syncthreads();
-  for (int e = threadIdx.x; e <= E; e += kLossThreads) {
-    Partial o;
-    o.c = hist[e];
-    o.p = 0.f;
-    if (e < E) {
-      float s[4] = {0.f, 0.f, 0.f, 0.f};
+  Partial o = {0.f, 0};
+  const int e = threadIdx.x;  // E < kLossThreads
+  if (e <= E) o.c = hist[e];
+  if (e < E) {
+    float s[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int w = 0; w < kLossWarps; ++w) s[w & 3] += psum[w][e];
-      o.p = (s[0] + s[1]) + (s[2] + s[3]);
-    }
-    part[(int64_t)blockIdx.x * (E + 1) + e] = o;
+    for (int w = 0; w < kLossWarps; ++w) s[w & 3] += psum[w][e];
+    o.p = (s[0] + s[1]) + (s[2] + s[3]);
+  }
+  if (gridDim.x > 1) {
+    if (e <= E) part[(int64_t)blockIdx.x * (E + 1) + e] = o;
+    return;
+  }
+  // a single block: the results themselves
+  __shared__ float terms[8];
+  const int n = hist[E];
+  float x = e < E ? finish_expert(e, o.p, o.c, n, E, k, out) : 0.f;
+  if (e < 256) {  // whole warps; E <= 256
+    x = group_sum(x, 32);
+    if (lane == 0) terms[warp] = x;
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    x = 0.f;
+    for (int w = 0; w < 8; ++w) x += terms[w];
+    *out.loss = out.coef * x;
+    *out.n_valid = n;
   }
 }
 
 // Sums the blocks' partials in a fixed order and forms the loss: one cluster, CTA c for experts
 // 32 c .., its warp w for every eighth partial.
 __global__ void __launch_bounds__(256)
-    router_loss_finish_kernel(const Partial* __restrict__ part, int nblk, int E, int k, float coef,
-                              float* loss, int32_t* counts, float* mean_prob, int32_t* n_valid) {
+    router_loss_finish_kernel(const Partial* __restrict__ part, int nblk, int E, int k,
+                              const Results out) {
   MOE_GRIDDEP_ENTRY();
   __shared__ float sp[8][32];
   __shared__ int sc[8][32];
@@ -195,10 +227,7 @@ __global__ void __launch_bounds__(256)
         p += sp[i][lane];
         c += sc[i][lane];
       }
-      const float mp = n > 0 ? p / (float)n : 0.f;
-      mean_prob[e] = mp;
-      counts[e] = c;
-      if (n > 0) x = mp * ((float)E * (float)c / ((float)k * (float)n));
+      x = finish_expert(e, p, c, n, E, k, out);
     }
     x = group_sum(x, 32);
     if (lane == 0) term = x;
@@ -213,8 +242,8 @@ __global__ void __launch_bounds__(256)
                    : "=f"(v) : "r"(mapa_shared(smem_u32(&term), r)) : "memory");
       s += v;
     }
-    *loss = coef * s;
-    *n_valid = n;
+    *out.loss = out.coef * s;
+    *out.n_valid = n;
   }
   __syncthreads();
   cluster_sync_all();  // no CTA leaves while its term may be read
@@ -399,17 +428,21 @@ moe_status_t moe_router_loss_fwd(const float* logits, int64_t ld_logits, const i
                 moe_router_loss_workspace(E));
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const RowMap m = row_map(E, E % 4 == 0 && ld_logits % 4 == 0 && a16(logits));
-  const int nblk = router_blocks(T, m, kLossWarps, std::min(std::max(device_sms(), 1), kMaxBlocks));
+  // up to four turns of one block are sooner done than two launches (512 x 4: 5.6 us with two)
+  int nblk = router_blocks(T, m, kLossWarps, std::min(std::max(device_sms(), 1), kMaxBlocks));
+  if (nblk <= 4) nblk = 1;
+  const Results out = {loss, counts, mean_prob, n_valid, coef};
   Partial* part = static_cast<Partial*>(ws);
   cudaError_t e = cudaSuccess;
   with_map(m, [&](auto vec, auto v) {
     e = launch_pdl(router_loss_kernel<vec.value, v.value>, nblk, kLossThreads, 0, s, 1, logits,
-                   ld_logits, topk_ids, token_mask, T, E, k, m.L, part);
+                   ld_logits, topk_ids, token_mask, T, E, k, m.L, part, out);
   });
   count_launch(s, MOE_K_ROUTER_LOSS);
   if (e != cudaSuccess) return cuda_fail(e, "router loss launch");
+  if (nblk == 1) return MOE_OK;
   e = launch_pdl(router_loss_finish_kernel, kFinishCtas, 256, 0, s, kFinishCtas,
-                 (const Partial*)part, nblk, E, k, coef, loss, counts, mean_prob, n_valid);
+                 (const Partial*)part, nblk, E, k, out);
   count_launch(s, MOE_K_ROUTER_LOSS);
   if (e != cudaSuccess) return cuda_fail(e, "router loss finish launch");
   return MOE_OK;
