@@ -10,11 +10,14 @@ There is no fallback: if the shared library is missing, `load()` raises.
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import math
 import os
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "_lib", "libmoegmm.so")
+CALLS_PATH = os.path.join(_PKG, "_lib", "_moecalls.so")
 
 PREC = {"bf16": 0, "mxfp8": 1, "nvfp4": 2}
 ACT = {"swiglu": 0, "clamped_swiglu": 1, "geglu": 2, "srelu": 3}
@@ -138,6 +141,31 @@ def load():
     return lib
 
 
+# Functions of the library that the operator classes call through csrc/calls.c, in the order of its
+# bind(): the same arguments as above, without ctypes' time.
+_CALLS = ("moe_router_loss_fwd", "moe_router_loss_bwd", "moe_layernorm_fwd", "moe_layernorm_bwd",
+          "moe_grad_clip", "fp8_block_quantize_rows", "fp8_block_quantize_weight",
+          "fp8_block_gemm")
+_calls = None
+
+
+def _load_calls():
+    """The module of csrc/calls.c, bound to the library. Raises if it is missing."""
+    global _calls
+    if _calls is None:
+        lib = load()
+        if not os.path.exists(CALLS_PATH):
+            raise RuntimeError(f"{CALLS_PATH} not built; run the build step first")
+        spec = importlib.util.spec_from_file_location(
+            "_moecalls", CALLS_PATH,
+            loader=importlib.machinery.ExtensionFileLoader("_moecalls", CALLS_PATH))
+        mod = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(mod)
+        mod.bind(*[ctypes.cast(getattr(lib, name), _P).value for name in _CALLS])
+        _calls = mod
+    return _calls
+
+
 class MoeError(RuntimeError):
     def __init__(self, status: int, msg: str):
         super().__init__(f"status {status}: {msg}")
@@ -157,12 +185,19 @@ def _ptr(t) -> int | None:
     return t.data_ptr()
 
 
+_cuda = None  # torch._C once CUDA is initialised
+
+
 def _stream(stream) -> int | None:
+    global _cuda
     if stream is None:
-        import torch
-        if torch.cuda.is_initialized():  # the same handle without building a Stream object
-            return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
-        return torch.cuda.current_stream().cuda_stream
+        if _cuda is None:
+            import torch
+            if not torch.cuda.is_initialized():
+                return torch.cuda.current_stream().cuda_stream
+            _cuda = torch._C
+        # the current stream's handle without building a Stream object
+        return _cuda._cuda_getCurrentRawStream(_cuda._cuda_getDevice())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -576,18 +611,18 @@ class RouterLoss:
         self.n_valid = torch.zeros(1, dtype=torch.int32, device=dev)
         self.d_logits = torch.empty(T_max, E, dtype=torch.float32, device=dev)
         # the buffers' addresses, taken once: a small call's time is the host's
-        self._lib = load()
+        self._lib = _load_calls()
         self._p = {n: getattr(self, n).data_ptr() for n in
                    ("ws", "loss", "counts", "mean_prob", "n_valid", "d_logits")}
 
     def _tokens(self, logits, topk_ids, token_mask):
-        import torch
         T = logits.shape[0]
         if T > self.T_max:
             raise ValueError(f"{T} tokens, but T_max is {self.T_max}")
-        _expect(logits, "logits", torch.float32, (T, self.E), rows=True)
-        _expect(topk_ids, "topk_ids", torch.int32, (T, self.k))
+        _expect(logits, "logits", self.loss.dtype, (T, self.E), rows=True)
+        _expect(topk_ids, "topk_ids", self.counts.dtype, (T, self.k))
         if token_mask is not None:
+            import torch
             if token_mask.dtype not in (torch.bool, torch.uint8):
                 raise ValueError("token_mask must be bool or uint8")
             _expect(token_mask, "token_mask", token_mask.dtype, (T,))
@@ -608,13 +643,12 @@ class RouterLoss:
                  d_loss=None, stream=None):
         """topk_probs and d_probs fp32 [T, k] (the layer's routing probabilities and the
         gradient its backward gives them), d_loss fp32 [1] (None: 1). Returns d_logits [T, E]."""
-        import torch
         T = self._tokens(logits, topk_ids, token_mask)
         for t, name in ((topk_probs, "topk_probs"), (d_probs, "d_probs")):
             if t is not None:
-                _expect(t, name, torch.float32, (T, self.k))
+                _expect(t, name, self.loss.dtype, (T, self.k))
         if d_loss is not None:
-            _expect(d_loss, "d_loss", torch.float32, d_loss.shape)
+            _expect(d_loss, "d_loss", self.loss.dtype, d_loss.shape)
             if d_loss.numel() != 1:
                 raise ValueError("d_loss must hold one value")
         p = self._p
@@ -641,7 +675,7 @@ class LayerNorm:
         self.mean = torch.empty(M_max, dtype=torch.float32, device=dev)
         self.rstd = torch.empty(M_max, dtype=torch.float32, device=dev)
         self.dx = None
-        self._lib = load()
+        self._lib = _load_calls()
         self._out = self.y.data_ptr(), N, self.mean.data_ptr(), self.rstd.data_ptr()
 
     def _rows(self, x, name):
@@ -676,9 +710,11 @@ class LayerNorm:
             self.dbeta = torch.empty(self.N, dtype=self.weight_dtype, device=self.device)
             self.ws_bytes = moe_layernorm_workspace(self.M_max, self.N)
             self.ws = torch.empty(self.ws_bytes, dtype=torch.uint8, device=self.device)
-        moe_layernorm_bwd(dy, _ld(dy), x, _ld(x), self._weight(gamma, "gamma"), mean, rstd,
-                          self.dx, self.N, self.dgamma, self.dbeta, M, self.N, *self._codes,
-                          self.ws, self.ws_bytes, stream)
+        _check(self._lib.moe_layernorm_bwd(
+            dy.data_ptr(), _ld(dy), x.data_ptr(), _ld(x), _ptr(self._weight(gamma, "gamma")),
+            mean.data_ptr(), rstd.data_ptr(), self.dx.data_ptr(), self.N, self.dgamma.data_ptr(),
+            self.dbeta.data_ptr(), M, self.N, *self._codes, self.ws.data_ptr(), self.ws_bytes,
+            _stream(stream)))
         return _first(self.dx, M), self.dgamma, self.dbeta
 
 
@@ -703,17 +739,18 @@ class GradClip:
         self._out = (_P * n)(*[o.data_ptr() for o in self.outs])
         self._numel = (_I64 * n)(*[g.numel() for g in self.grads])
         self._types = (_I32 * n)(*[_dtype_code(g.dtype) for g in self.grads])
+        self._at = [ctypes.addressof(a) for a in (self._in, self._out, self._numel, self._types)]
         self.norm = torch.zeros(1, dtype=torch.float32, device=dev)
         self.ws_bytes = moe_grad_clip_workspace()
         self.ws = torch.empty(self.ws_bytes, dtype=torch.uint8, device=dev)
-        self._lib = load()
+        self._lib = _load_calls()
         self._work = self.norm.data_ptr(), self.ws.data_ptr(), self.ws_bytes
 
     def clip(self, max_norm, stream=None):
         """Returns the norm [1] (on the device). max_norm = inf only takes the norm."""
-        outs = None if max_norm == math.inf else self._out
-        _check(self._lib.moe_grad_clip(self.n, self._in, outs, self._numel, self._types, max_norm,
-                                       *self._work, _stream(stream)))
+        at = self._at
+        _check(self._lib.moe_grad_clip(self.n, at[0], None if max_norm == math.inf else at[1],
+                                       at[2], at[3], max_norm, *self._work, _stream(stream)))
         return self.norm
 
 
@@ -758,7 +795,7 @@ class Fp8Linear:
         def operand(q, s):
             return q.data_ptr(), q.shape[1], s.data_ptr(), s.shape[1]
 
-        self._lib = load()
+        self._lib = _load_calls()
         self._w, self._x = operand(self.wq, self.w_scale), operand(self.xq, self.x_scale)
         self._none = None, 0, None, 0
         self._xt = self._none
@@ -786,13 +823,12 @@ class Fp8Linear:
 
     def forward(self, x, stream=None):
         """x bf16 [M, K] -> y bf16 [M, N]."""
-        import torch
         if not self.has_weight:
             raise ValueError("set_weight comes before forward")
         M = x.shape[0]
         if M > self.M_max:
             raise ValueError(f"{M} rows, but M_max is {self.M_max}")
-        _expect(x, "x", torch.bfloat16, (M, self.K), rows=True)
+        _expect(x, "x", self.y.dtype, (M, self.K), rows=True)
         stream = _stream(stream)
         self._quantize(x, M, self.K, self._x, self._xt, stream)
         self._product(self._x, self._w, 1, self.y, M, self.N, self.K, stream)
@@ -801,11 +837,10 @@ class Fp8Linear:
 
     def backward(self, dy, stream=None):
         """dy bf16 [M, N] of the last forward's rows -> (dx bf16 [M, K], dw bf16 [N, K])."""
-        import torch
         if not self.train or self.M is None:
             raise ValueError("backward needs a layer made with train=True and a forward")
         M = self.M
-        _expect(dy, "dy", torch.bfloat16, (M, self.N), rows=True)
+        _expect(dy, "dy", self.y.dtype, (M, self.N), rows=True)
         if M == 0:
             return self.dx[:0], self.dw.zero_()
         stream = _stream(stream)

@@ -7,12 +7,14 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 OUT_DIR = os.path.join(PKG, "_lib")
 LIB = os.path.join(OUT_DIR, "libmoegmm.so")
+CALLS = os.path.join(OUT_DIR, "_moecalls.so")  # Python's way into the operators
 SOURCES = ["api.cu", "route.cu", "mxfp8.cu", "gemm.cu", "gemm_mx.cu", "gemm_rc.cu", "noalloc.cu",
            "nvfp4.cu", "gemm_fp4.cu", "router_loss.cu", "layernorm.cu", "grad_clip.cu",
            "fp8_quant.cu", "gemm_fp8.cu"]
@@ -41,10 +43,22 @@ def _compile(src: str, obj: str, verbose_ptxas: bool) -> str:
     return r.stderr
 
 
+def _compile_calls() -> None:
+    cc = sysconfig.get_config_var("CC") or "gcc"
+    cc = cc.split()[0] if shutil.which(cc.split()[0]) else "gcc"
+    cmd = [cc, "-O2", "-shared", "-fPIC", "-Wall", "-I" + sysconfig.get_paths()["include"],
+           "-I" + os.path.join(ROOT, "include"), os.path.join(CSRC, "calls.c"),
+           "-o", CALLS + ".tmp"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{cc} failed for calls.c:\n{r.stdout}\n{r.stderr}")
+    os.replace(CALLS + ".tmp", CALLS)
+
+
 def _stale(objs) -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(CALLS):
         return True
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(CALLS))
     deps = [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
     deps.append(os.path.join(ROOT, "include", "moegmm.h"))
     deps.append(os.path.abspath(__file__))
@@ -61,6 +75,7 @@ def build(force: bool = False, verbose_ptxas: bool = False) -> str:
     if verbose_ptxas:
         for s, l in zip(SOURCES, logs):
             sys.stderr.write(f"== {s}\n{l}")
+    _compile_calls()
     tmp = LIB + ".tmp"
     cmd = [nvcc(), *ARCH, "-shared", "-Xcompiler", "-fPIC", "-o", tmp, *objs, "--cudart", "static"]
     r = subprocess.run(cmd, capture_output=True, text=True)

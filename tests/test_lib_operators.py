@@ -167,3 +167,19 @@ def test_dtype_names_match_the_header():
     assert g.DTYPE == {"bf16": 0, "fp32": 1}
     assert g.KERNEL_NAMES[19] == "router_loss" and g.KERNEL_NAMES[27] == "fp8_gemm"
     assert len(g.KERNEL_NAMES) == 28
+
+
+def test_calls_refuse_wrong_arguments(lib):
+    """The classes' own way into the library (csrc/calls.c): counts and conversions of arguments;
+    statuses come back as numbers."""
+    calls = g._load_calls()
+    assert calls.moe_grad_clip(-1, 0, None, 0, 0, 1.0, None, None, 0, None) == 1
+    for args in ((), (0,) * 9, (0,) * 11):
+        with pytest.raises(TypeError):
+            calls.moe_grad_clip(*args)
+    with pytest.raises(TypeError):
+        calls.moe_grad_clip("0", 0, None, 0, 0, 1.0, None, None, 0, None)
+    with pytest.raises(OverflowError):
+        calls.moe_grad_clip(1 << 31, 0, None, 0, 0, 1.0, None, None, 0, None)
+    with pytest.raises(TypeError):
+        calls.bind(0)
