@@ -8,6 +8,7 @@
 // serves both copies. Maxima are taken on the bf16 values themselves (a maximum rounds nothing),
 // two at a time.
 #include "kernels.cuh"
+#include "realign.cuh"
 
 namespace moe {
 namespace {
@@ -53,12 +54,7 @@ struct QuantArgs {
 // 8 consecutive values of a row from column c (zeros past column N).
 MOE_DEVICE uint4 load8(const uint16_t* row, int64_t c, int64_t N, bool vec) {
   if (vec && c + 8 <= N) return *reinterpret_cast<const uint4*>(row + c);
-  uint32_t u[4];
-#pragma unroll
-  for (int j = 0; j < 4; ++j)
-    u[j] = (c + 2 * j < N ? (uint32_t)row[c + 2 * j] : 0u) |
-           (c + 2 * j + 1 < N ? (uint32_t)row[c + 2 * j + 1] << 16 : 0u);
-  return make_uint4(u[0], u[1], u[2], u[3]);
+  return c < N ? load16_any(row + c, (N - c) * 2) : make_uint4(0, 0, 0, 0);
 }
 
 // Rows alone: a warp takes 512 columns (16 a lane, eight lanes a block) of kRows rows.

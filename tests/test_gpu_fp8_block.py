@@ -316,3 +316,20 @@ def test_same_bits_again_on_another_stream_and_in_a_graph(lib):
         torch.cuda.synchronize()
         for a, b, c in zip(first, other, (y, dx, dw)):
             assert torch.equal(a, b) and torch.equal(a, c)
+
+
+@pytest.mark.parametrize("pad,off", [(0, 0), (0, 1), (1, 0), (2, 3), (3, 5), (5, 6), (7, 7)])
+@pytest.mark.parametrize("block", [True, False])
+def test_gemm_rows_off_boundaries(lib, block, pad, off):
+    """Whole tiles whose rows start anywhere in a 16-byte block, and the last, partial ones."""
+    check_gemm(2500, 2301, 130, block, ldc=2301 + pad, c_off=off)
+    check_gemm(1300, 135, 300, block, ldc=135 + pad, c_off=off)
+
+
+@pytest.mark.parametrize("off", range(8))
+def test_quantize_rows_off_boundaries(lib, off):
+    for M, N, ld in ((130, 257, 257), (70, 1000, 1003), (9, 130, 131), (300, 127, 129)):
+        buf = randbf(1, M * ld + 16, seed=off)[0]
+        x = buf[off:off + M * ld].view(M, ld)[:, :N]
+        check_rows(x, quant_rows(x))
+        check_rows(x, quant_rows(x, col=False), col=False)
