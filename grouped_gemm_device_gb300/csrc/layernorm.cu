@@ -10,6 +10,7 @@
 // weight-gradient partials are fp32. Widening bf16 runs at half the rate of the products, so it is
 // done once a value where the registers allow.
 #include "kernels.cuh"
+#include "realign.cuh"
 
 namespace moe {
 namespace {
@@ -18,6 +19,12 @@ namespace {
 // leave small partials and run more blocks.
 constexpr int64_t kShortRow = 1024;
 int64_t max_parts(int64_t N) { return N <= kShortRow ? 960 : 480; }
+// A row of partials: two of this many floats, whole vectors of any type and the place of a row's
+// first element in its first block.
+template <typename I>
+__host__ __device__ I pad_cols(I N) {
+  return (N + 7) / 8 * 8 + 8;
+}
 
 template <typename T>
 MOE_DEVICE float to_f(T v) {
@@ -30,11 +37,11 @@ MOE_DEVICE T from_f(float v) {
   else return v;
 }
 
-// VEC consecutive elements as they lie in memory: 16 bytes, or one element (VEC = 1).
+// VEC consecutive elements as they lie in memory: 16 bytes.
 template <typename T, int VEC>
 struct Raw {
-  uint32_t w[VEC == 1 ? 1 : 4];
-  static_assert(VEC == 1 || VEC * sizeof(T) == 16, "one element or 16 bytes");
+  uint32_t w[4];
+  static_assert(VEC * sizeof(T) == 16, "16 bytes");
 };
 template <typename T, int VEC>
 MOE_DEVICE void zero_raw(Raw<T, VEC>& r) {
@@ -44,14 +51,21 @@ MOE_DEVICE void zero_raw(Raw<T, VEC>& r) {
 // Streamed data is not kept in L1, which the weights of the following rows want.
 template <typename T, int VEC>
 MOE_DEVICE void load_raw(const T* p, Raw<T, VEC>& r) {
-  if constexpr (VEC > 1) {
-    asm volatile("ld.global.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(r.w[0]), "=r"(r.w[1]), "=r"(r.w[2]), "=r"(r.w[3])
-                 : "l"(p));
-  } else if constexpr (sizeof(T) == 2) {
-    r.w[0] = *reinterpret_cast<const uint16_t*>(p);
-  } else {
-    r.w[0] = __float_as_uint(*p);
+  asm volatile("ld.global.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r.w[0]), "=r"(r.w[1]), "=r"(r.w[2]), "=r"(r.w[3])
+               : "l"(p));
+}
+// Zeros before element lo and from element hi on.
+template <typename T, int VEC>
+MOE_DEVICE void clear_outside(Raw<T, VEC>& r, int lo, int hi) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    if constexpr (sizeof(T) == 4) {
+      if (k < lo || k >= hi) r.w[k] = 0u;
+    } else {
+      if (2 * k < lo || 2 * k >= hi) r.w[k] &= 0xFFFF0000u;
+      if (2 * k + 1 < lo || 2 * k + 1 >= hi) r.w[k] &= 0x0000FFFFu;
+    }
   }
 }
 template <typename T, int VEC>
@@ -60,40 +74,87 @@ MOE_DEVICE float raw_at(const Raw<T, VEC>& r, int j) {  // j is a constant after
   else return (j & 1) ? bf16_hi(r.w[j >> 1]) : bf16_lo(r.w[j >> 1]);
 }
 
-// VEC consecutive elements (VEC * sizeof(T) a multiple of 16 bytes, or VEC = 1) as fp32.
+// VEC consecutive elements (VEC * sizeof(T) a multiple of 16 bytes) as fp32.
 template <typename T, int VEC>
 MOE_DEVICE void load_vec(const T* p, float (&v)[VEC]) {
-  if constexpr (VEC == 1) {
-    v[0] = to_f(__ldg(p));
-  } else {
-    constexpr int W = VEC * sizeof(T) / 16;
+  constexpr int W = VEC * sizeof(T) / 16;
 #pragma unroll
-    for (int w = 0; w < W; ++w) {
-      const uint4 q = __ldg(reinterpret_cast<const uint4*>(p) + w);
-      const uint32_t u[4] = {q.x, q.y, q.z, q.w};
+  for (int w = 0; w < W; ++w) {
+    const uint4 q = __ldg(reinterpret_cast<const uint4*>(p) + w);
+    const uint32_t u[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if constexpr (sizeof(T) == 2) {
-          v[8 * w + 2 * i] = bf16_lo(u[i]);
-          v[8 * w + 2 * i + 1] = bf16_hi(u[i]);
-        } else {
-          v[4 * w + i] = __uint_as_float(u[i]);
-        }
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (sizeof(T) == 2) {
+        v[8 * w + 2 * i] = bf16_lo(u[i]);
+        v[8 * w + 2 * i + 1] = bf16_hi(u[i]);
+      } else {
+        v[4 * w + i] = __uint_as_float(u[i]);
       }
     }
   }
 }
+// The weights of columns c .. c + VEC - 1. ANY: c may be any column from 1 - VEC on (zeros outside
+// [0, N)), and (vec false) p off a 16-byte boundary.
+template <bool ANY, typename T, int VEC>
+MOE_DEVICE void load_weights(const T* p, int c, int N, bool vec, float (&v)[VEC]) {
+  if constexpr (!ANY) {
+    load_vec<T, VEC>(p + c, v);
+  } else if (vec) {
+    constexpr int E = 16 / sizeof(T), W = VEC / E;  // elements of 16 bytes, such blocks to fill
+    const int b = (c + VEC) / E - W;                // the block of c, rounded down
+    uint32_t w[4 * W + 4];
+#pragma unroll
+    for (int i = 0; i <= W; ++i) {
+      uint4 q = make_uint4(0, 0, 0, 0);
+      if (b + i >= 0 && (b + i) * E < N) q = __ldg(reinterpret_cast<const uint4*>(p) + b + i);
+      w[4 * i] = q.x;
+      w[4 * i + 1] = q.y;
+      w[4 * i + 2] = q.z;
+      w[4 * i + 3] = q.w;
+    }
+    drop_bytes(w, (c - b * E) * (int)sizeof(T));
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) {
+      if constexpr (sizeof(T) == 4) v[j] = __uint_as_float(w[j]);
+      else v[j] = (j & 1) ? bf16_hi(w[j >> 1]) : bf16_lo(w[j >> 1]);
+    }
+    if (c < 0 || c + VEC > N) {
+#pragma unroll
+      for (int j = 0; j < VEC; ++j)
+        if (c + j < 0 || c + j >= N) v[j] = 0.f;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) v[j] = c + j >= 0 && c + j < N ? to_f(__ldg(p + c + j)) : 0.f;
+  }
+}
 template <typename T, int VEC>
 MOE_DEVICE void store_vec(T* p, const float (&v)[VEC]) {
-  if constexpr (VEC == 1) {
-    *p = from_f<T>(v[0]);
-  } else if constexpr (sizeof(T) == 2) {
+  if constexpr (sizeof(T) == 2) {
     *reinterpret_cast<uint4*>(p) =
         make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
                    pack_bf16x2(v[6], v[7]));
   } else {
     *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
   }
+}
+// The same of the elements [lo, hi).
+template <typename T, int VEC>
+MOE_DEVICE void store_part(T* p, const float (&v)[VEC], int lo, int hi) {
+#pragma unroll
+  for (int j = 0; j < VEC; ++j)
+    if (j >= lo && j < hi) p[j] = from_f<T>(v[j]);
+}
+// Rows off 16-byte boundaries (ANY): a thread owns whole aligned blocks of 16 bytes, so that rows
+// are read and written like aligned ones. Element j of block b is then column b VEC - lead + j,
+// `lead` the row's first element's place in its first block; every kCycle-th row has the same one,
+// and a thread takes only rows that agree. What a row's first and last block hold of the rows
+// beside it is cleared when read and left alone when written. (Moving the bytes between columns
+// and blocks for every row instead: 8192 x 4095 bf16, 52 us forward and 88 us backward.)
+constexpr int kCycle = 8;
+template <typename T>
+MOE_DEVICE int row_lead(const T* row) {
+  return lead_bytes(row) / (int)sizeof(T);
 }
 
 MOE_DEVICE float warp_sum(float a) {
@@ -148,26 +209,33 @@ MOE_DEVICE void row_sum2(float& a, float& b, float (&sm)[2][2][32], int turn) {
 }
 
 // G threads (a warp of four in a block, or a whole block) take RP rows, PER vectors of VEC elements
-// a thread and row: N <= G * PER * VEC. Two rows share each load of the weights.
-template <typename XT, typename WT, int VEC, int G, int PER, int RP>
-__global__ void __launch_bounds__(G < 128 ? 128 : G) ln_fwd_kernel(
+// a thread and row: N <= G * PER * VEC (ANY: N + VEC - 1). The rows share each load of the weights.
+template <typename XT, typename WT, int VEC, int G, int PER, int RP, bool ANY>
+__global__ void __launch_bounds__(G < 128 ? 128 : G, G <= 128 && PER * VEC * RP <= 48 ? 6 : 1)
+    ln_fwd_kernel(
     const XT* x, int64_t ldx, const WT* __restrict__ gamma, const WT* __restrict__ beta, XT* y,
     int64_t ldy, float* __restrict__ mean_out, float* __restrict__ rstd_out, int64_t M, int N,
-    float eps) {
+    float eps, int wvec) {
   MOE_GRIDDEP_ENTRY();
   __shared__ float sm[2][RP][32];
   constexpr int R = (G < 128 ? 128 : G) / G;  // groups a block
+  static_assert(!ANY || RP == 1, "rows beside one another lie differently in their blocks");
   const int t = threadIdx.x % G;
-  const int64_t row0 = ((int64_t)blockIdx.x * R + threadIdx.x / G) * RP;
+  const int64_t g = (int64_t)blockIdx.x * R + threadIdx.x / G;
+  const int64_t row0 = g * RP;
   if (G == 32 && row0 >= M) return;  // a block's groups are its warps; otherwise R = 1
+  const int lead = ANY ? row_lead(x + row0 * ldx) : 0;
   Raw<XT, VEC> raw[RP][PER];
 #pragma unroll
   for (int k = 0; k < RP; ++k)
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-      const int c = (i * G + t) * VEC;
+      const int c = (i * G + t) * VEC - lead;
       zero_raw(raw[k][i]);
-      if (c < N && (RP == 1 || row0 + k < M)) load_raw(x + (row0 + k) * ldx + c, raw[k][i]);
+      if (c < N && (RP == 1 || row0 + k < M)) {
+        load_raw(x + (row0 + k) * ldx + c, raw[k][i]);
+        if (ANY && (c < 0 || c + VEC > N)) clear_outside(raw[k][i], -c, N - c);
+      }
     }
   float v[RP][PER][VEC], rstd[RP];
 #pragma unroll
@@ -182,14 +250,21 @@ __global__ void __launch_bounds__(G < 128 ? 128 : G) ln_fwd_kernel(
       }
     const float mean = row_sum<G>(s, sm[0][k]) / (float)N;
 #pragma unroll
-    for (int i = 0; i < PER; ++i)
-      if ((i * G + t) * VEC < N) {
+    for (int i = 0; i < PER; ++i) {
+      const int c = (i * G + t) * VEC - lead;
+      if (c < N) {
+        if (ANY && (c < 0 || c + VEC > N)) {  // nothing from outside the row
+#pragma unroll
+          for (int j = 0; j < VEC; ++j)
+            if (c + j < 0 || c + j >= N) v[k][i][j] = mean;
+        }
 #pragma unroll
         for (int j = 0; j < VEC; ++j) {
           v[k][i][j] -= mean;
           q += v[k][i][j] * v[k][i][j];
         }
       }
+    }
     rstd[k] = 1.0f / sqrtf(row_sum<G>(q, sm[1][k]) / (float)N + eps);
     if (t == 0 && (RP == 1 || row0 + k < M)) {
       if (mean_out) mean_out[row0 + k] = mean;
@@ -198,11 +273,11 @@ __global__ void __launch_bounds__(G < 128 ? 128 : G) ln_fwd_kernel(
   }
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
-    const int c = (i * G + t) * VEC;
+    const int c = (i * G + t) * VEC - lead;
     if (c < N) {
       float gm[VEC], bt[VEC], o[VEC];
-      if (gamma) load_vec<WT, VEC>(gamma + c, gm);
-      if (beta) load_vec<WT, VEC>(beta + c, bt);
+      if (gamma) load_weights<ANY, WT, VEC>(gamma, c, N, wvec, gm);
+      if (beta) load_weights<ANY, WT, VEC>(beta, c, N, wvec, bt);
 #pragma unroll
       for (int k = 0; k < RP; ++k) {
 #pragma unroll
@@ -210,7 +285,11 @@ __global__ void __launch_bounds__(G < 128 ? 128 : G) ln_fwd_kernel(
           const float h = v[k][i][j] * rstd[k];
           o[j] = (gamma ? h * gm[j] : h) + (beta ? bt[j] : 0.f);
         }
-        if (RP == 1 || row0 + k < M) store_vec<XT, VEC>(y + (row0 + k) * ldy + c, o);
+        if (RP == 1 || row0 + k < M) {
+          XT* at = y + (row0 + k) * ldy + c;
+          if (!ANY || (c >= 0 && c + VEC <= N)) store_vec<XT, VEC>(at, o);
+          else store_part<XT, VEC>(at, o, -c, N - c);
+        }
       }
     }
   }
@@ -246,28 +325,138 @@ __global__ void __launch_bounds__(1024) ln_fwd_long_kernel(
   }
 }
 
-// Backward. A group of G threads (a warp of eight in a block, or a whole block) walks rows; a
-// thread owns the same PER * VEC columns of every row and keeps their dgamma and dbeta sums in
-// registers until the end. Each thread copies its own columns of the next S - 1 rows into a ring
-// in shared memory (cp.async), so that 64 to 190 KB are on their way on an SM and no barrier is
-// spent on the copies; VEC = 1 (rows off 16-byte boundaries) loads directly.
-template <typename XT, int VEC, int B, int PER, int S>
-constexpr int ring_bytes() {
-  return VEC > 1 ? S * PER * 2 * B * 16 : 0;
+// Threads a block of the kernels that walk rows: eight warps with a row each, or one row.
+constexpr int block_of(int G) { return G == 32 ? 256 : G; }
+template <int N>
+MOE_DEVICE void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 MOE_DEVICE void cp_async16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 
+// Many rows off 16-byte boundaries: a group of G threads (a warp of eight in a block, or a whole
+// block) walks rows that lie alike in their blocks, with the weights of its columns in registers
+// and the next S - 1 rows on their way to shared memory (cp.async, a thread's own columns).
+// N + VEC - 1 <= G * PER * VEC.
 template <typename XT, typename WT, int VEC, int G, int PER, int S>
-__global__ void __launch_bounds__(G < 256 ? 256 : G) ln_bwd_kernel(
+__global__ void __launch_bounds__(block_of(G)) ln_fwd_walk_kernel(
+    const XT* x, int64_t ldx, const WT* __restrict__ gamma, const WT* __restrict__ beta, XT* y,
+    int64_t ldy, float* __restrict__ mean_out, float* __restrict__ rstd_out, int64_t M, int N,
+    float eps, int wvec) {
+  MOE_GRIDDEP_ENTRY();
+  constexpr int B = block_of(G), GROUPS = B / G;
+  __shared__ float sm[2][2][32];
+  extern __shared__ uint4 ring[];  // [S][PER][B]
+  const int t = threadIdx.x % G;
+  const int64_t row0 = (int64_t)blockIdx.x * GROUPS + threadIdx.x / G;
+  const int64_t step = (int64_t)gridDim.x * GROUPS;
+  const uint32_t ring0 = smem_u32(ring) + threadIdx.x * 16;
+  const int lead = row_lead(x + row0 * ldx);
+  auto fetch = [&](int64_t row, int slot) {
+    if (row < M) {
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        const int c = (i * G + t) * VEC - lead;
+        if (c < N) cp_async16(ring0 + ((slot * PER + i) * B) * 16, x + row * ldx + c);
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+#pragma unroll
+  for (int k = 0; k < S - 1; ++k) fetch(row0 + k * step, k);
+  float gm[PER][VEC], bt[PER][VEC];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int c = (i * G + t) * VEC - lead;
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) {
+      gm[i][j] = 1.0f;
+      bt[i][j] = 0.f;
+    }
+    if (gamma && c < N) load_weights<true, WT, VEC>(gamma, c, N, wvec, gm[i]);
+    if (beta && c < N) load_weights<true, WT, VEC>(beta, c, N, wvec, bt[i]);
+  }
+  int slot = 0, turn = 0;
+  for (int64_t row = row0; row < M; row += step) {
+    fetch(row + (S - 1) * step, slot == 0 ? S - 1 : slot - 1);
+    cp_async_wait<S - 1>();
+    float v[PER][VEC], s = 0.f, q = 0.f;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int c = (i * G + t) * VEC - lead;
+      const uint4 w = ring[(slot * PER + i) * B + threadIdx.x];
+      Raw<XT, VEC> r;
+      r.w[0] = w.x;
+      r.w[1] = w.y;
+      r.w[2] = w.z;
+      r.w[3] = w.w;
+      if (c < 0 || c + VEC > N) clear_outside(r, -c, N - c);
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) {
+        v[i][j] = raw_at(r, j);
+        s += v[i][j];
+      }
+    }
+    const float mean = row_sum<G>(s, sm[turn][0]) / (float)N;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int c = (i * G + t) * VEC - lead;
+      if (c < 0 || c + VEC > N) {  // nothing from outside the row
+#pragma unroll
+        for (int j = 0; j < VEC; ++j)
+          if (c + j < 0 || c + j >= N) v[i][j] = mean;
+      }
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) {
+        v[i][j] -= mean;
+        q += v[i][j] * v[i][j];
+      }
+    }
+    const float rstd = 1.0f / sqrtf(row_sum<G>(q, sm[turn][1]) / (float)N + eps);
+    turn ^= 1;
+    if (t == 0) {
+      if (mean_out) mean_out[row] = mean;
+      if (rstd_out) rstd_out[row] = rstd;
+    }
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int c = (i * G + t) * VEC - lead;
+      if (c < N) {
+        float o[VEC];
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) {
+          const float h = v[i][j] * rstd;
+          o[j] = (gamma ? h * gm[i][j] : h) + bt[i][j];
+        }
+        XT* at = y + row * ldy + c;
+        if (c >= 0 && c + VEC <= N) store_vec<XT, VEC>(at, o);
+        else store_part<XT, VEC>(at, o, -c, N - c);
+      }
+    }
+    if (++slot == S) slot = 0;
+  }
+  cp_async_wait<0>();
+}
+
+// Backward. A group of G threads (a warp of eight in a block, or a whole block) walks rows; a
+// thread owns the same PER * VEC columns of every row and keeps their dgamma and dbeta sums in
+// registers until the end. Each thread copies its own columns of the next S - 1 rows into a ring
+// in shared memory (cp.async), so that 64 to 190 KB are on their way on an SM and no barrier is
+// spent on the copies. ANY: N + VEC - 1 <= G * PER * VEC, and the groups' number a multiple of
+// kCycle where a group takes more than one row.
+template <int B, int PER, int S>
+constexpr int ring_bytes() {
+  return S * PER * 2 * B * 16;
+}
+template <typename XT, typename WT, int VEC, int G, int PER, int S, bool ANY>
+__global__ void __launch_bounds__(block_of(G)) ln_bwd_kernel(
     const XT* dy, int64_t lddy, const XT* x, int64_t ldx, const WT* __restrict__ gamma,
     const float* __restrict__ mean, const float* __restrict__ rstd, XT* dx, int64_t lddx,
     float* __restrict__ part, WT* __restrict__ dgamma, WT* __restrict__ dbeta, int64_t M,
-    int N) {
+    int N, int wvec) {
   MOE_GRIDDEP_ENTRY();
-  constexpr int B = G < 256 ? 256 : G, GROUPS = B / G;
-  constexpr bool kRing = VEC > 1;
+  constexpr int B = block_of(G), GROUPS = B / G;
   // few enough columns a thread to hold gamma and one row's widened values beside the sums
   constexpr bool kKeep = PER * VEC <= 16 && G <= 512;
   __shared__ float sm[2][2][32];
@@ -276,11 +465,12 @@ __global__ void __launch_bounds__(G < 256 ? 256 : G) ln_bwd_kernel(
   const int64_t row0 = (int64_t)blockIdx.x * GROUPS + threadIdx.x / G;
   const int64_t step = (int64_t)gridDim.x * GROUPS;
   const uint32_t ring0 = smem_u32(ring) + threadIdx.x * 16;
+  const int lead = ANY ? row_lead(x + row0 * ldx) : 0;
   auto fetch = [&](int64_t row, int slot) {
     if (row < M) {
 #pragma unroll
       for (int i = 0; i < PER; ++i) {
-        const int c = (i * G + t) * VEC;
+        const int c = (i * G + t) * VEC - lead;
         if (c < N) {
           cp_async16(ring0 + ((slot * 2 * PER + 2 * i) * B) * 16, x + row * ldx + c);
           cp_async16(ring0 + ((slot * 2 * PER + 2 * i + 1) * B) * 16, dy + row * lddy + c);
@@ -289,15 +479,15 @@ __global__ void __launch_bounds__(G < 256 ? 256 : G) ln_bwd_kernel(
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
-  auto ring_at = [&](int slot, int i) {
-    const uint4 q = ring[(slot * 2 * PER + i) * B + threadIdx.x];
+  auto ring_at = [&](int slot, int i, int which) {  // vector i of a row's x (0) or dy (1)
+    const uint4 q = ring[(slot * 2 * PER + 2 * i + which) * B + threadIdx.x];
     Raw<XT, VEC> r;
     r.w[0] = q.x;
-    if constexpr (VEC > 1) {
-      r.w[1] = q.y;
-      r.w[2] = q.z;
-      r.w[3] = q.w;
-    }
+    r.w[1] = q.y;
+    r.w[2] = q.z;
+    r.w[3] = q.w;
+    const int c = (i * G + t) * VEC - lead;
+    if (ANY && (c < 0 || c + VEC > N)) clear_outside(r, -c, N - c);
     return r;
   };
   float dg[PER][VEC], db[PER][VEC];
@@ -305,42 +495,29 @@ __global__ void __launch_bounds__(G < 256 ? 256 : G) ln_bwd_kernel(
   for (int i = 0; i < PER; ++i)
 #pragma unroll
     for (int j = 0; j < VEC; ++j) dg[i][j] = db[i][j] = 0.f;
-  if constexpr (kRing) {
 #pragma unroll
-    for (int k = 0; k < S - 1; ++k) fetch(row0 + k * step, k);
-  }
+  for (int k = 0; k < S - 1; ++k) fetch(row0 + k * step, k);
   float gm[kKeep ? PER : 1][VEC];
   if constexpr (kKeep) {
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-      const int c = (i * G + t) * VEC;
+      const int c = (i * G + t) * VEC - lead;
 #pragma unroll
       for (int j = 0; j < VEC; ++j) gm[i][j] = 1.0f;
-      if (gamma && c < N) load_vec<WT, VEC>(gamma + c, gm[i]);
+      if (gamma && c < N) load_weights<ANY, WT, VEC>(gamma, c, N, wvec, gm[i]);
     }
   }
   int slot = 0, turn = 0;
   float mu = row0 < M ? mean[row0] : 0.f, rs = row0 < M ? rstd[row0] : 0.f;
   for (int64_t row = row0; row < M; row += step) {
     Raw<XT, VEC> h[PER], u[PER];
-    if constexpr (kRing) {
-      const int ahead = slot == 0 ? S - 1 : slot - 1;
-      fetch(row + (S - 1) * step, ahead);
-      asm volatile("cp.async.wait_group %0;" ::"n"(S - 1) : "memory");
+    const int ahead = slot == 0 ? S - 1 : slot - 1;
+    fetch(row + (S - 1) * step, ahead);
+    cp_async_wait<S - 1>();
 #pragma unroll
-      for (int i = 0; i < PER; ++i) {
-        h[i] = ring_at(slot, 2 * i);
-        u[i] = ring_at(slot, 2 * i + 1);
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < PER; ++i) {
-        const int c = (i * G + t) * VEC;
-        if (c < N) {
-          load_raw(x + row * ldx + c, h[i]);
-          load_raw(dy + row * lddy + c, u[i]);
-        }
-      }
+    for (int i = 0; i < PER; ++i) {
+      h[i] = ring_at(slot, i, 0);
+      u[i] = ring_at(slot, i, 1);
     }
     const float m0 = mu, r0 = rs;
     if (row + step < M) {  // the next row's statistics
@@ -352,10 +529,10 @@ __global__ void __launch_bounds__(G < 256 ? 256 : G) ln_bwd_kernel(
     float s1 = 0.f, s2 = 0.f;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-      const int c = (i * G + t) * VEC;
+      const int c = (i * G + t) * VEC - lead;
       if (c < N) {
         float gv[VEC];
-        if (!kKeep && gamma) load_vec<WT, VEC>(gamma + c, gv);
+        if (!kKeep && gamma) load_weights<ANY, WT, VEC>(gamma, c, N, wvec, gv);
 #pragma unroll
         for (int j = 0; j < VEC; ++j) {
           const float cj = raw_at(h[i], j) - m0, d = raw_at(u[i], j);
@@ -376,14 +553,14 @@ __global__ void __launch_bounds__(G < 256 ? 256 : G) ln_bwd_kernel(
     const float k1 = r0 * (s1 / (float)N), k2 = (r0 * r0) * r0 * (s2 / (float)N);
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-      const int c = (i * G + t) * VEC;
+      const int c = (i * G + t) * VEC - lead;
       if (c < N) {
-        if constexpr (!kKeep && kRing) {  // once more from the ring: registers are short here
-          h[i] = ring_at(slot, 2 * i);
-          u[i] = ring_at(slot, 2 * i + 1);
+        if (!kKeep) {  // once more from the ring: registers are short here
+          h[i] = ring_at(slot, i, 0);
+          u[i] = ring_at(slot, i, 1);
         }
         float gv[VEC], o[VEC];
-        if (!kKeep && gamma) load_vec<WT, VEC>(gamma + c, gv);
+        if (!kKeep && gamma) load_weights<ANY, WT, VEC>(gamma, c, N, wvec, gv);
 #pragma unroll
         for (int j = 0; j < VEC; ++j) {
           float cj, uj;
@@ -397,14 +574,17 @@ __global__ void __launch_bounds__(G < 256 ? 256 : G) ln_bwd_kernel(
           }
           o[j] = (r0 * uj - k1) - cj * k2;
         }
-        store_vec<XT, VEC>(dx + row * lddx + c, o);
+        XT* at = dx + row * lddx + c;
+        if (!ANY || (c >= 0 && c + VEC <= N)) store_vec<XT, VEC>(at, o);
+        else store_part<XT, VEC>(at, o, -c, N - c);
       }
     }
-    if (kRing && ++slot == S) slot = 0;
+    if (++slot == S) slot = 0;
   }
   if (!part) return;
-  float* pg = part + (int64_t)blockIdx.x * 2 * N;  // a single block writes the results
-  if constexpr (kRing) asm volatile("cp.async.wait_all;" ::: "memory");
+  const int NP = pad_cols(N);
+  float* pg = part + (int64_t)blockIdx.x * 2 * NP;  // a single block writes the results
+  cp_async_wait<0>();
   if constexpr (GROUPS > 1) {
     // the block's groups, in order, through the columns of one shared row at a time
     __shared__ float cols[2][G * PER * VEC];
@@ -415,7 +595,8 @@ __global__ void __launch_bounds__(G < 256 ? 256 : G) ln_bwd_kernel(
         for (int i = 0; i < PER; ++i)
 #pragma unroll
           for (int j = 0; j < VEC; ++j) {
-            const int c = (i * G + t) * VEC + j;
+            const int c = (i * G + t) * VEC - lead + j;
+            if (ANY && (c < 0 || c >= N)) continue;
             cols[0][c] = g == 0 ? dg[i][j] : cols[0][c] + dg[i][j];
             cols[1][c] = g == 0 ? db[i][j] : cols[1][c] + db[i][j];
           }
@@ -428,31 +609,30 @@ __global__ void __launch_bounds__(G < 256 ? 256 : G) ln_bwd_kernel(
         if (dbeta) dbeta[c] = from_f<WT>(cols[1][c]);
       } else {
         pg[c] = cols[0][c];
-        pg[N + c] = cols[1][c];
+        pg[NP + c] = cols[1][c];
       }
     }
   } else {
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-      const int c = (i * G + t) * VEC;
+      const int c = (i * G + t) * VEC - lead;
       if (c < N) {
         if (gridDim.x == 1) {
 #pragma unroll
-          for (int j = 0; j < VEC; ++j) {
-            if (dgamma) dgamma[c + j] = from_f<WT>(dg[i][j]);
-            if (dbeta) dbeta[c + j] = from_f<WT>(db[i][j]);
-          }
-        } else if constexpr (VEC > 1) {  // N is a multiple of VEC, the partials 16-byte aligned
+          for (int j = 0; j < VEC; ++j)
+            if (!ANY || (c + j >= 0 && c + j < N)) {
+              if (dgamma) dgamma[c + j] = from_f<WT>(dg[i][j]);
+              if (dbeta) dbeta[c + j] = from_f<WT>(db[i][j]);
+            }
+        } else {  // column c at c + lead: whole vectors, NP being a multiple of VEC
+          const int at = c + lead;
 #pragma unroll
           for (int j = 0; j < VEC; j += 4) {
-            *reinterpret_cast<float4*>(pg + c + j) =
+            *reinterpret_cast<float4*>(pg + at + j) =
                 make_float4(dg[i][j], dg[i][j + 1], dg[i][j + 2], dg[i][j + 3]);
-            *reinterpret_cast<float4*>(pg + N + c + j) =
+            *reinterpret_cast<float4*>(pg + NP + at + j) =
                 make_float4(db[i][j], db[i][j + 1], db[i][j + 2], db[i][j + 3]);
           }
-        } else {
-          pg[c] = dg[i][0];
-          pg[N + c] = db[i][0];
         }
       }
     }
@@ -465,7 +645,8 @@ __global__ void __launch_bounds__(256) ln_bwd_cols_long_kernel(
     const XT* dy, int64_t lddy, const XT* x, int64_t ldx, const float* __restrict__ mean,
     const float* __restrict__ rstd, float* __restrict__ part, int64_t M, int64_t N) {
   MOE_GRIDDEP_ENTRY();
-  float* pg = part + (int64_t)blockIdx.x * 2 * N;
+  const int64_t NP = pad_cols(N);
+  float* pg = part + (int64_t)blockIdx.x * 2 * NP;
   for (int64_t c = threadIdx.x; c < N; c += 256) {
     float dg = 0.f, db = 0.f;
     for (int64_t row = blockIdx.x; row < M; row += gridDim.x) {
@@ -474,7 +655,7 @@ __global__ void __launch_bounds__(256) ln_bwd_cols_long_kernel(
       db += d;
     }
     pg[c] = dg;
-    pg[N + c] = db;
+    pg[NP + c] = db;
   }
 }
 template <typename XT, typename WT>
@@ -507,21 +688,25 @@ __global__ void __launch_bounds__(1024) ln_bwd_rows_long_kernel(
   }
 }
 
-// dgamma[c] (columns [0, N)) and dbeta (columns [N, 2N)) = sum of the blocks' partials. Each of a
-// block's 32 warps sums every 32nd partial of 32 columns; the warps' sums are added in order.
+// dgamma (columns [0, N)) and dbeta (columns [N, 2 N)) = sum of the blocks' partials; block b's
+// column c lies at c + (place + b * pitch) % 16 / size. Each of a block's 32 warps sums every 32nd
+// partial of 32 columns; the warps' sums are added in order.
 template <typename WT>
 __global__ void __launch_bounds__(1024) ln_colsum_kernel(const float* __restrict__ part,
                                                          int nparts, int64_t N,
                                                          WT* __restrict__ dgamma,
-                                                         WT* __restrict__ dbeta) {
+                                                         WT* __restrict__ dbeta, uint32_t place,
+                                                         uint32_t pitch, int size) {
   MOE_GRIDDEP_ENTRY();
   __shared__ float sm[32][33];
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  const int64_t c = (int64_t)blockIdx.x * 32 + lane;
+  const int64_t c = (int64_t)blockIdx.x * 32 + lane, NP = pad_cols(N);
   float s = 0.f;
   if (c < 2 * N) {
+    const float* at = part + (c < N ? c : c - N + NP);
 #pragma unroll 5
-    for (int b = w; b < nparts; b += 32) s += part[(int64_t)b * 2 * N + c];
+    for (int b = w; b < nparts; b += 32)
+      s += at[(int64_t)b * 2 * NP + ((place + (uint32_t)b * pitch) & 15u) / size];
   }
   sm[w][lane] = s;
   __syncthreads();
@@ -543,6 +728,12 @@ bool aligned_to(const void* p, int bytes) {
   return (reinterpret_cast<uintptr_t>(p) & (uintptr_t)(bytes - 1)) == 0;
 }
 
+// Every row of one tensor lies in its 16-byte blocks as the same row of the other.
+bool same_place(const void* a, int64_t lda, const void* b, int64_t ldb) {
+  return ((reinterpret_cast<uintptr_t>(a) ^ reinterpret_cast<uintptr_t>(b)) & 15) == 0 &&
+         (lda - ldb) % 16 == 0;
+}
+
 struct LnArgs {
   const void *x, *dy, *gamma, *beta;
   void *y, *dx;
@@ -554,59 +745,95 @@ struct LnArgs {
   float* part;
   int nparts;
   bool done;  // the weight gradients are final
+  bool wvec;   // gamma and beta lie on 16-byte boundaries
+  bool shifted;  // partials of block b lie like row b in its 16-byte blocks
+  bool mixed;  // the tensors' rows lie differently in their 16-byte blocks
   cudaStream_t s;
 };
 
-template <typename XT, typename WT, int VEC, int G, int PER, int RP = 1>
+// Columns that a row's threads have to hold: with ANY up to V - 1 more, before the first one. Tensors
+// whose rows lie differently cannot share a thread's blocks and go the way of the longest rows.
+template <bool ANY>
+int64_t columns(const LnArgs& a, int V) {
+  return a.mixed ? INT64_MAX : ANY ? a.N + V - 1 : a.N;
+}
+
+template <typename XT, typename WT, bool ANY, int VEC, int G, int PER, int RP = 1>
 cudaError_t fwd_launch(const LnArgs& a) {
   constexpr int B = G < 128 ? 128 : G, rows = B / G * RP;
   const int64_t blocks = (a.M + rows - 1) / rows;
-  return launch_pdl(ln_fwd_kernel<XT, WT, VEC, G, PER, RP>, (unsigned)blocks, B, 0, a.s, 1,
+  return launch_pdl(ln_fwd_kernel<XT, WT, VEC, G, PER, RP, ANY>, (unsigned)blocks, B, 0, a.s, 1,
                     static_cast<const XT*>(a.x), a.ldx, static_cast<const WT*>(a.gamma),
                     static_cast<const WT*>(a.beta), static_cast<XT*>(a.y), a.ldy, a.mean, a.rstd,
-                    a.M, (int)a.N, a.eps);
+                    a.M, (int)a.N, a.eps, (int)a.wvec);
 }
 
-template <typename XT, typename WT>
+// As many blocks as fit at once; their groups' number a multiple of kCycle.
+template <typename XT, typename WT, int VEC, int G, int PER>
+cudaError_t fwd_walk(const LnArgs& a) {
+  constexpr int B = block_of(G), GROUPS = B / G, S = 4, smem = S * PER * B * 16;
+  auto kern = ln_fwd_walk_kernel<XT, WT, VEC, G, PER, S>;
+  cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kern), smem);
+  if (e != cudaSuccess) return e;
+  static const int per_sm = [&] {
+    int n = 0;
+    return cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, B, smem) == cudaSuccess && n > 0
+               ? n : 1;
+  }();
+  int64_t blocks = std::min<int64_t>((a.M + GROUPS - 1) / GROUPS,
+                                     (int64_t)std::max(device_sms(), kCycle) * per_sm);
+  if (blocks * GROUPS < a.M) blocks = blocks * GROUPS / kCycle * kCycle / GROUPS;
+  return launch_pdl(kern, (unsigned)blocks, B, smem, a.s, 1, static_cast<const XT*>(a.x), a.ldx,
+                    static_cast<const WT*>(a.gamma), static_cast<const WT*>(a.beta),
+                    static_cast<XT*>(a.y), a.ldy, a.mean, a.rstd, a.M, (int)a.N, a.eps,
+                    (int)a.wvec);
+}
+
+template <typename XT, typename WT, bool ANY>
 cudaError_t fwd_typed(const LnArgs& a) {
   constexpr int V = 16 / sizeof(XT);
   // Weights wider than the rows cost more L1 reads than the rows: two rows share them (16384 x
   // 2880 bf16 rows, fp32 weights: 35.4 us against 42.7). With equal types the registers of a
   // second row cost more than it saves (8192 x 4096 bf16: 29.8 us against 23.2).
   constexpr int RP = sizeof(WT) > sizeof(XT) ? 2 : 1;
-  const bool vec = a.N % V == 0 && a.ldx % V == 0 && a.ldy % V == 0 && aligned_to(a.x, 16) &&
-                   aligned_to(a.y, 16) && aligned_to(a.gamma, 16) && aligned_to(a.beta, 16);
-  const int64_t N = a.N;
+  const int64_t N = columns<ANY>(a, V);
   // Up to 32 elements a thread: as few warps a row as hold it, for many rows in flight; with too
   // few rows to fill the GPU that way, as many threads as the row feeds, which is there sooner.
   const bool many = a.M >= (int64_t)std::max(device_sms(), 1) * 2;
-  if (vec) {
-    constexpr int P = 32 / V;  // vectors of 32 elements
-    if (N <= 32 * V) return fwd_launch<XT, WT, V, 32, 1>(a);
+  constexpr int P = 32 / V;  // vectors of 32 elements
+  if constexpr (ANY) {
+    // Many rows: weights moved to the rows' columns once a group. Longer rows, whose groups hold
+    // few of them at a time, move them for every row (8192 x 4095 bf16: 55 us against 64), as do
+    // few rows.
     if (many) {
-      if (N <= 32 * 2 * V) return fwd_launch<XT, WT, V, 32, 2>(a);
-      if (N <= 32 * 32) return fwd_launch<XT, WT, V, 32, P>(a);
-      if (N <= 128 * 16) return fwd_launch<XT, WT, V, 128, P / 2, RP>(a);
-      if (N <= 128 * 24) return fwd_launch<XT, WT, V, 128, P / 4 * 3, RP>(a);
-      if (N <= 128 * 32) return fwd_launch<XT, WT, V, 128, P, RP>(a);
-      if (N <= 256 * 32) return fwd_launch<XT, WT, V, 256, P, RP>(a);
-      if (N <= 512 * 32) return fwd_launch<XT, WT, V, 512, P, RP>(a);
+      if (N <= 32 * V) return fwd_walk<XT, WT, V, 32, 1>(a);
+      if constexpr (V == 4)
+        if (N <= 32 * 8) return fwd_walk<XT, WT, V, 32, 2>(a);
+      if (N <= 32 * 16) return fwd_walk<XT, WT, V, 32, 16 / V>(a);
+      if (N <= 128 * 8) return fwd_walk<XT, WT, V, 128, 8 / V>(a);
+      if (N <= 128 * 16) return fwd_walk<XT, WT, V, 128, 16 / V>(a);
+      if (N <= 128 * 24) return fwd_walk<XT, WT, V, 128, 24 / V>(a);
+      if (N <= 128 * (32 + V)) return fwd_launch<XT, WT, ANY, V, 128, P + 1>(a);
+      if (N <= 256 * (32 + V)) return fwd_launch<XT, WT, ANY, V, 256, P + 1>(a);
     }
-    if (N <= 256 * V) return fwd_launch<XT, WT, V, 256, 1>(a);
-    if (N <= 512 * V) return fwd_launch<XT, WT, V, 512, 1>(a);
-    if (N <= 1024 * V) return fwd_launch<XT, WT, V, 1024, 1>(a);
-    if (N <= 1024 * 16) return fwd_launch<XT, WT, V, 1024, 16 / V>(a);
-    if (N <= 1024 * 32) return fwd_launch<XT, WT, V, 1024, P>(a);
+    if (N <= 32 * V) return fwd_launch<XT, WT, ANY, V, 32, 1>(a);
   } else {
-    if (N <= 32 * 8) return fwd_launch<XT, WT, 1, 32, 8>(a);
+    if (N <= 32 * V) return fwd_launch<XT, WT, ANY, V, 32, 1>(a);
     if (many) {
-      if (N <= 32 * 16) return fwd_launch<XT, WT, 1, 32, 16>(a);
-      if (N <= 32 * 32) return fwd_launch<XT, WT, 1, 32, 32>(a);
-      if (N <= 128 * 24) return fwd_launch<XT, WT, 1, 128, 24>(a);
+      if (N <= 32 * 2 * V) return fwd_launch<XT, WT, ANY, V, 32, 2>(a);
+      if (N <= 32 * 32) return fwd_launch<XT, WT, ANY, V, 32, P>(a);
+      if (N <= 128 * 16) return fwd_launch<XT, WT, ANY, V, 128, P / 2, RP>(a);
+      if (N <= 128 * 24) return fwd_launch<XT, WT, ANY, V, 128, P / 4 * 3, RP>(a);
+      if (N <= 128 * 32) return fwd_launch<XT, WT, ANY, V, 128, P, RP>(a);
+      if (N <= 256 * 32) return fwd_launch<XT, WT, ANY, V, 256, P, RP>(a);
+      if (N <= 512 * 32) return fwd_launch<XT, WT, ANY, V, 512, P, RP>(a);
     }
-    if (N <= 1024 * 4) return fwd_launch<XT, WT, 1, 1024, 4>(a);
-    if (N <= 1024 * 16) return fwd_launch<XT, WT, 1, 1024, 16>(a);
   }
+  if (N <= 256 * V) return fwd_launch<XT, WT, ANY, V, 256, 1>(a);
+  if (N <= 512 * V) return fwd_launch<XT, WT, ANY, V, 512, 1>(a);
+  if (N <= 1024 * V) return fwd_launch<XT, WT, ANY, V, 1024, 1>(a);
+  if (N <= 1024 * 16) return fwd_launch<XT, WT, ANY, V, 1024, 16 / V>(a);
+  if (N <= 1024 * 32) return fwd_launch<XT, WT, ANY, V, 1024, P>(a);
   const int grid = (int)std::min<int64_t>(a.M, (int64_t)std::max(device_sms(), 1) * 2);
   return launch_pdl(ln_fwd_long_kernel<XT, WT>, grid, 1024, 0, a.s, 1,
                     static_cast<const XT*>(a.x), a.ldx, static_cast<const WT*>(a.gamma),
@@ -614,15 +841,13 @@ cudaError_t fwd_typed(const LnArgs& a) {
                     a.M, a.N, a.eps);
 }
 
-template <typename XT, typename WT, int VEC, int G, int PER, int S>
+template <typename XT, typename WT, bool ANY, int VEC, int G, int PER, int S>
 cudaError_t bwd_launch(LnArgs& a) {
-  constexpr int B = G < 256 ? 256 : G, GROUPS = B / G;
-  constexpr int smem = ring_bytes<XT, VEC, B, PER, S>();
-  auto kern = ln_bwd_kernel<XT, WT, VEC, G, PER, S>;
-  if (smem > 0) {
-    cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kern), smem);
-    if (e != cudaSuccess) return e;
-  }
+  constexpr int B = block_of(G), GROUPS = B / G;
+  constexpr int smem = ring_bytes<B, PER, S>();
+  auto kern = ln_bwd_kernel<XT, WT, VEC, G, PER, S, ANY>;
+  cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kern), smem);
+  if (e != cudaSuccess) return e;
   // as many blocks as fit at once (at least two where registers allow), each a row of partials
   static const int per_sm = [&] {
     int n = 0;
@@ -632,40 +857,35 @@ cudaError_t bwd_launch(LnArgs& a) {
   const int64_t fit = (int64_t)std::max(device_sms(), 1) * per_sm;
   a.nparts = (int)std::max<int64_t>(
       1, std::min<int64_t>((a.M + GROUPS - 1) / GROUPS, std::min<int64_t>(fit, max_parts(a.N))));
+  if (ANY && a.nparts * GROUPS < a.M) a.nparts = a.nparts * GROUPS / kCycle * kCycle / GROUPS;
   a.done = a.nparts == 1;
+  a.shifted = ANY && GROUPS == 1;
   return launch_pdl(kern, a.nparts, B, smem, a.s, 1, static_cast<const XT*>(a.dy), a.lddy,
                     static_cast<const XT*>(a.x), a.ldx, static_cast<const WT*>(a.gamma), a.mean,
                     a.rstd, static_cast<XT*>(a.dx), a.lddx, a.part, static_cast<WT*>(a.dgamma),
-                    static_cast<WT*>(a.dbeta), a.M, (int)a.N);
+                    static_cast<WT*>(a.dbeta), a.M, (int)a.N, (int)a.wvec);
 }
 
-template <typename XT, typename WT>
+template <typename XT, typename WT, bool ANY>
 cudaError_t bwd_typed(LnArgs& a) {
   constexpr int V = 16 / sizeof(XT);
-  const bool vec = a.N % V == 0 && a.ldx % V == 0 && a.lddy % V == 0 && a.lddx % V == 0 &&
-                   aligned_to(a.x, 16) && aligned_to(a.dy, 16) && aligned_to(a.dx, 16) &&
-                   aligned_to(a.gamma, 16);
-  const int64_t N = a.N;
-  if (vec) {
-    if (N <= 32 * V) return bwd_launch<XT, WT, V, 32, 1, 4>(a);
-    if (N <= 32 * 2 * V) return bwd_launch<XT, WT, V, 32, 2, 3>(a);
-    if (N <= 32 * 4 * V) return bwd_launch<XT, WT, V, 32, 4, 3>(a);
-    if (N <= 256 * V) return bwd_launch<XT, WT, V, 256, 1, 4>(a);
-    if (N <= 256 * 2 * V) return bwd_launch<XT, WT, V, 256, 2, 4>(a);
-    if constexpr (sizeof(XT) == 4) {
-      if (N <= 256 * 4 * V) return bwd_launch<XT, WT, V, 256, 4, 3>(a);
-    } else {
-      if (N <= 512 * 2 * V) return bwd_launch<XT, WT, V, 512, 2, 3>(a);
-    }
-    if (N <= 512 * 4 * V) return bwd_launch<XT, WT, V, 512, 4, 3>(a);
-    if constexpr (sizeof(XT) == 4)
-      if (N <= 512 * 8 * V) return bwd_launch<XT, WT, V, 512, 8, 1>(a);
+  const int64_t N = a.N, C = columns<ANY>(a, V);
+  if (C <= 32 * V) return bwd_launch<XT, WT, ANY, V, 32, 1, 4>(a);
+  if (C <= 32 * 2 * V) return bwd_launch<XT, WT, ANY, V, 32, 2, 3>(a);
+  if constexpr (V == 4)
+    if (C <= 32 * 16) return bwd_launch<XT, WT, ANY, V, 32, 4, 3>(a);
+  if (C <= 128 * 8) return bwd_launch<XT, WT, ANY, V, 128, 8 / V, 4>(a);
+  if constexpr (V == 8)
+    if (C <= 256 * V) return bwd_launch<XT, WT, ANY, V, 256, 1, 4>(a);
+  if (C <= 256 * 2 * V) return bwd_launch<XT, WT, ANY, V, 256, 2, 4>(a);
+  if constexpr (sizeof(XT) == 4) {
+    if (C <= 256 * 4 * V) return bwd_launch<XT, WT, ANY, V, 256, 4, 3>(a);
   } else {
-    if (N <= 32 * 8) return bwd_launch<XT, WT, 1, 32, 8, 1>(a);
-    if (N <= 256 * 4) return bwd_launch<XT, WT, 1, 256, 4, 1>(a);
-    if (N <= 512 * 8) return bwd_launch<XT, WT, 1, 512, 8, 1>(a);
-    if (N <= 512 * 32) return bwd_launch<XT, WT, 1, 512, 32, 1>(a);
+    if (C <= 512 * 2 * V) return bwd_launch<XT, WT, ANY, V, 512, 2, 3>(a);
   }
+  if (C <= 512 * 4 * V) return bwd_launch<XT, WT, ANY, V, 512, 4, 3>(a);
+  if constexpr (sizeof(XT) == 4)
+    if (C <= 512 * 8 * V) return bwd_launch<XT, WT, ANY, V, 512, 8, 1>(a);
   const int64_t most = std::min<int64_t>(std::max(device_sms(), 1), max_parts(N));
   a.nparts = (int)std::min<int64_t>(a.M, most);
   if (a.part) {
@@ -680,6 +900,17 @@ cudaError_t bwd_typed(LnArgs& a) {
                     static_cast<const XT*>(a.dy), a.lddy, static_cast<const XT*>(a.x), a.ldx,
                     static_cast<const WT*>(a.gamma), a.mean, a.rstd, static_cast<XT*>(a.dx),
                     a.lddx, a.M, a.N);
+}
+
+// Calls fn with a value of the rows' type, one of the weights', and ANY.
+template <class F>
+cudaError_t typed(int32_t xd, int32_t wd, bool any, F&& fn) {
+  auto with = [&](auto xt, auto wt) {
+    return any ? fn(xt, wt, std::true_type()) : fn(xt, wt, std::false_type());
+  };
+  if (xd == MOE_DT_FP32) return with(float(), float());
+  if (wd == MOE_DT_FP32) return with(__nv_bfloat16(), float());
+  return with(__nv_bfloat16(), __nv_bfloat16());
 }
 
 moe_status_t check_types(int64_t M, int64_t N, int32_t xd, int32_t wd) {
@@ -717,9 +948,13 @@ moe_status_t moe_layernorm_fwd(const void* x, int64_t ldx, const void* gamma, co
   a.x = x; a.ldx = ldx; a.gamma = gamma; a.beta = beta; a.y = y; a.ldy = ldy;
   a.mean = mean; a.rstd = rstd; a.M = M; a.N = N; a.eps = eps;
   a.s = reinterpret_cast<cudaStream_t>(stream);
-  cudaError_t e = x_dtype == MOE_DT_FP32   ? fwd_typed<float, float>(a)
-                  : w_dtype == MOE_DT_FP32 ? fwd_typed<__nv_bfloat16, float>(a)
-                                           : fwd_typed<__nv_bfloat16, __nv_bfloat16>(a);
+  a.wvec = aligned_to(gamma, 16) && aligned_to(beta, 16);
+  const bool any = !(a.wvec && aligned_to(x, 16) && aligned_to(y, 16) && N * xb % 16 == 0 &&
+                     ldx * xb % 16 == 0 && ldy * xb % 16 == 0);
+  a.mixed = any && !same_place(x, ldx * xb, y, ldy * xb);
+  const cudaError_t e = typed(x_dtype, w_dtype, any, [&](auto xt, auto wt, auto w) {
+    return fwd_typed<decltype(xt), decltype(wt), w.value>(a);
+  });
   count_launch(a.s, MOE_K_LAYERNORM_FWD);
   if (e != cudaSuccess) return cuda_fail(e, "layernorm forward launch");
   return MOE_OK;
@@ -730,7 +965,8 @@ size_t moe_layernorm_workspace(int64_t M, int64_t N) {
     fail(MOE_ERR_INVALID_ARG, "M must be in [0, 2^31) and N in [1, 2^31)");
     return 0;
   }
-  return (size_t)std::max<int64_t>(1, std::min<int64_t>(M, max_parts(N))) * 2 * N * sizeof(float);
+  return (size_t)std::max<int64_t>(1, std::min<int64_t>(M, max_parts(N))) * 2 * pad_cols(N) *
+         sizeof(float);
 }
 
 moe_status_t moe_layernorm_bwd(const void* dy, int64_t lddy, const void* x, int64_t ldx,
@@ -768,21 +1004,30 @@ moe_status_t moe_layernorm_bwd(const void* dy, int64_t lddy, const void* x, int6
   a.s = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e = cudaSuccess;
   if (M > 0) {
-    e = x_dtype == MOE_DT_FP32   ? bwd_typed<float, float>(a)
-        : w_dtype == MOE_DT_FP32 ? bwd_typed<__nv_bfloat16, float>(a)
-                                 : bwd_typed<__nv_bfloat16, __nv_bfloat16>(a);
+    a.wvec = aligned_to(gamma, 16);
+    const bool any = !(a.wvec && aligned_to(x, 16) && aligned_to(dy, 16) && aligned_to(dx, 16) &&
+                       N * xb % 16 == 0 && ldx * xb % 16 == 0 && lddy * xb % 16 == 0 &&
+                       lddx * xb % 16 == 0);
+    a.mixed = any && !(same_place(x, ldx * xb, dy, lddy * xb) &&
+                       same_place(x, ldx * xb, dx, lddx * xb));
+    e = typed(x_dtype, w_dtype, any, [&](auto xt, auto wt, auto w) {
+      return bwd_typed<decltype(xt), decltype(wt), w.value>(a);
+    });
     count_launch(a.s, MOE_K_LAYERNORM_BWD);
     if (e != cudaSuccess) return cuda_fail(e, "layernorm backward launch");
   }  // no rows: no partials, the sums are zero
   if (weights && !a.done) {
     const unsigned grid = (unsigned)((2 * N + 31) / 32);
+    const uint32_t place = a.shifted ? (uint32_t)(reinterpret_cast<uintptr_t>(x) & 15) : 0u;
+    const uint32_t pitch = a.shifted ? (uint32_t)(ldx * xb) : 0u;
     if (w_dtype == MOE_DT_FP32)
       e = launch_pdl(ln_colsum_kernel<float>, grid, 1024, 0, a.s, 1, (const float*)a.part,
-                         a.nparts, N, static_cast<float*>(dgamma), static_cast<float*>(dbeta));
+                         a.nparts, N, static_cast<float*>(dgamma), static_cast<float*>(dbeta), place,
+                     pitch, xb);
     else
       e = launch_pdl(ln_colsum_kernel<__nv_bfloat16>, grid, 1024, 0, a.s, 1,
                          (const float*)a.part, a.nparts, N, static_cast<__nv_bfloat16*>(dgamma),
-                         static_cast<__nv_bfloat16*>(dbeta));
+                     static_cast<__nv_bfloat16*>(dbeta), place, pitch, xb);
     count_launch(a.s, MOE_K_LAYERNORM_REDUCE);
     if (e != cudaSuccess) return cuda_fail(e, "layernorm reduction launch");
   }

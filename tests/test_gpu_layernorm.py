@@ -237,3 +237,64 @@ def test_same_bits_again_on_another_stream_and_in_a_graph(lib):
     torch.cuda.synchronize()
     for a, b, c in zip(first, other, (y, mean, rstd, dx, dg, db)):
         assert torch.equal(a, b) and torch.equal(a, c)
+
+
+OFF = [(2500, 1), (2500, 7), (2500, 63), (2500, 130), (2500, 249), (2500, 250), (2500, 257),
+       (1300, 333), (1300, 505), (1300, 511), (700, 1017), (700, 1018), (700, 1025), (700, 2041),
+       (700, 2047), (400, 3065), (400, 3071), (400, 4089), (400, 5113), (400, 5121), (320, 8185),
+       (320, 10233), (320, 10241), (320, 16377), (320, 16383)]
+
+
+@pytest.mark.parametrize("M,N", OFF)
+@pytest.mark.parametrize("xt,wt", TYPES)
+def test_many_rows_off_boundaries(lib, M, N, xt, wt):
+    x, dy, gamma, beta = make(M, N, xt, wt, seed=5)
+    ln = g.LayerNorm(N, M, dtype=xt, weight_dtype=wt)
+    out = ln.forward(x, gamma, beta)
+    check_fwd(x, gamma, beta, out, 1e-5)
+    check_bwd(dy, x, gamma, out[1], out[2], ln.backward(dy, x, gamma))
+
+
+@pytest.mark.parametrize("shift", [0, 1, 3, 6])
+@pytest.mark.parametrize("M,N,pad", [(33, 301, 2), (700, 61, 1), (700, 301, 3), (700, 1003, 5),
+                                     (400, 2200, 9), (330, 4097, 2), (320, 9000, 1)])
+@pytest.mark.parametrize("xt", [BF, F32])
+def test_rows_beside_not_a_number(lib, M, N, pad, shift, xt):
+    """Rows that share 16-byte blocks with NaNs: none gets in, and none is overwritten."""
+    x0, dy0, gamma0, beta0 = make(M, N, xt, xt, seed=6)
+    ld = N + pad
+
+    def strided(t=None):
+        buf = torch.full((M * ld + 16,), float("nan"), dtype=xt, device="cuda")
+        v = buf[shift:shift + M * ld].view(M, ld)[:, :N]
+        if t is not None:
+            v.copy_(t)
+        return buf, v
+
+    def weight(t):  # off 16-byte boundaries, NaNs around it
+        buf = torch.full((N + 16,), float("nan"), dtype=xt, device="cuda")
+        buf[shift:shift + N] = t
+        return buf[shift:shift + N]
+
+    code = 0 if xt is BF else 1
+    (_, x), (_, dy), (yb, y), (dxb, dx) = strided(x0), strided(dy0), strided(), strided()
+    gamma, beta = weight(gamma0), weight(beta0)
+    mean = torch.empty(M, device="cuda")
+    rstd = torch.empty(M, device="cuda")
+    dg, db = torch.empty(N, dtype=xt, device="cuda"), torch.empty(N, dtype=xt, device="cuda")
+    n = g.moe_layernorm_workspace(M, N)
+    ws = torch.full((n,), 255, dtype=torch.uint8, device="cuda")
+    g.moe_layernorm_fwd(x, ld, gamma, beta, y, ld, mean, rstd, M, N, 1e-5, code, code)
+    check_fwd(x0, gamma0, beta0, (y, mean, rstd), 1e-5)
+    g.moe_layernorm_bwd(dy, ld, x, ld, gamma, mean, rstd, dx, ld, dg, db, M, N, code, code, ws, n)
+    check_bwd(dy0, x0, gamma0, mean, rstd, (dx, dg, db))
+    for buf, v in ((yb, y), (dxb, dx)):
+        keep = torch.ones_like(buf, dtype=torch.bool)
+        keep[shift:shift + M * ld].view(M, ld)[:, :N] = False
+        assert torch.isnan(buf[keep]).all()
+    want = dx.clone()
+    g.moe_layernorm_bwd(dy, ld, x, ld, gamma, mean, rstd, dy, ld, dg, db, M, N, code, code, ws, n)
+    assert torch.equal(dy, want)  # in place
+    want = y.clone()
+    g.moe_layernorm_fwd(x, ld, gamma, beta, x, ld, mean, rstd, M, N, 1e-5, code, code)
+    assert torch.equal(x, want)
