@@ -173,3 +173,15 @@ def test_graph_capture(lib):
     torch.cuda.synchronize()
     ed, size = ob.router_grad(lg2, ids, 0.02, m, 1.0, w, dw)
     assert (np.abs(d.cpu().numpy() - ed) <= 80 * ULP * size + 1e-42).all()
+
+
+@pytest.mark.parametrize("E,k", [(1, 1), (2, 2), (3, 3), (6, 5), (8, 8), (64, 8), (256, 8)])
+def test_slots_that_share_an_expert(lib, E, k):
+    """Ids that repeat, all of them or some, invalid ones among them: summed in their order."""
+    lg, ids, w, dw, m = make(777, E, k, mask=True)
+    r = np.random.default_rng(E)
+    ids[::3] = r.integers(0, E, (len(ids[::3]), 1))           # one expert for every slot
+    ids[1::3] = r.integers(-1, E, (len(ids[1::3]), k))
+    first = check(lg, ids, w, dw, m)
+    again = check(lg, ids, w, dw, m)
+    assert torch.equal(first, again)
