@@ -13,12 +13,21 @@
 // kind::f8f6f4), warps 4-11 hold the 128 x BN fp32 sums (warp w: TMEM lanes 32 (w % 4).., half of
 // the columns). P is the operand on the 128-row side, Q the one on the BN-column side.
 //   Many rows: P = a, Q = b, tiles of 128 x 256; a result row is contiguous in a thread.
-//   Few rows (M <= 128): P = b, Q = a (BN = M rounded up), so that the whole 128-row side is
+//   Few rows (M <= 64): P = b, Q = a (BN = M rounded up), so that the whole 128-row side is
 //   filled with features and the small operand costs what it holds; the result is written
 //   transposed, one feature a lane.
 //   Tiles that do not fill the GPU (all of them, or those of the last round): the k-blocks are
 //   split over a cluster of 2-8 CTAs, whose sums are added through distributed shared memory in
 //   the order of their ranks.
+//
+// What bounds it. Many rows: a k-block of 128 x 256 moves 48 KB into shared memory and 48 KB out of
+// it into the tensor cores, and its product waits for the sums of the one before the last to leave
+// TMEM: 400 to 450 ns where the MMAs alone take about 300. 8192 x 14336 x 4096 (M x N x K): 345 us,
+// 2.8 PFLOP/s; 8192 x 4096 x 14336: 319 us, 3.0; 4096 x 4096 x 7168: 90 us, 2.7. Two 1 x 128
+// operands (weight gradients) need a second packed product a pair of results, and every lane reads
+// every column's scale: 14336 x 4096 x 8192: 455 to 470 us, 2.1 PFLOP/s. Few rows: the weights'
+// bytes and some 4 us of launch, first loads and cluster sums: 1 x 4096 x 7168 7.5 us, 1 x 14336 x
+// 4096 10.7 us (5.5 TB/s, from L2), 128 x 4096 x 7168 11.0 us.
 #include <mutex>
 
 #include "gemm_common.cuh"
@@ -220,7 +229,8 @@ MOE_DEVICE void store_swapped(const Fp8Args& p, int prow, int64_t qrow, float v)
 }
 
 // First row of P and of Q of a tile. Tiles are dealt in bands of kBand P tiles, Q tile by Q tile,
-// so that the tiles in flight together read about as many rows of one side as of the other.
+// so that the tiles in flight together read about as many rows of one side as of the other (8192 x
+// 14336 x 4096: 350 us, in bands of one 358).
 constexpr int kBand = 16;
 template <int BN>
 MOE_DEVICE void tile_at(const Fp8Args& p, int tile, int& p0, int& q0) {
@@ -555,7 +565,8 @@ __global__ void __launch_bounds__(Smem<BN>::THREADS, 1)
       } else if (p.align < 16 && !p.c_fp32) {
         const int col = q0 + c0, n = min(CW, p.rows_q - col);
         if (n > 0)
-          store_row_any<CW>(static_cast<uint16_t*>(p.c) + (int64_t)(p0 + row) * p.ldc + col, n, acc);
+          store_row_any<CW>(
+              static_cast<uint16_t*>(p.c) + (int64_t)(p0 + row) * p.ldc + col, n, acc);
       } else {
 #pragma unroll
         for (int j = 0; j < CW / CH; ++j) {
@@ -734,8 +745,14 @@ cudaError_t launch_gemm(Fp8Args& a, const Plan& plan, const Operand& P, const Op
   return e;
 }
 
+// Rows up to which the swapped form is taken. 64 x 4096 x 7168: 9.0 us, not swapped 10.7 (though
+// 64 x 14336 x 4096 13.2 against 12.3); 128 rows: 11.3 against 11.0, 128 x 14336 x 4096 17.1 against
+// 13.0.
+constexpr int kFewRows = 64;
+
 // The widths in turn: the one whose plan ends first. Few rows take the narrowest tile that holds
-// them (swapped form); otherwise tiles of 64, 128 or 256 columns.
+// them (swapped form); otherwise
+// tiles of 64, 128 or 256 columns.
 template <bool PV, bool QV>
 cudaError_t launch_any(Fp8Args& a, const Operand& P, const Operand& Q, cudaStream_t s) {
   const int64_t nkb = (a.K + BK - 1) / BK;
@@ -745,9 +762,7 @@ cudaError_t launch_any(Fp8Args& a, const Operand& P, const Operand& Q, cudaStrea
         return launch_gemm<16, PV, QV>(a, plan_tiles<16, PV, QV>(P.rows, Q.rows, nkb), P, Q, s);
       if (Q.rows <= 32)
         return launch_gemm<32, PV, QV>(a, plan_tiles<32, PV, QV>(P.rows, Q.rows, nkb), P, Q, s);
-      if (Q.rows <= 64)
-        return launch_gemm<64, PV, QV>(a, plan_tiles<64, PV, QV>(P.rows, Q.rows, nkb), P, Q, s);
-      return launch_gemm<128, PV, QV>(a, plan_tiles<128, PV, QV>(P.rows, Q.rows, nkb), P, Q, s);
+      return launch_gemm<64, PV, QV>(a, plan_tiles<64, PV, QV>(P.rows, Q.rows, nkb), P, Q, s);
     }
   } else if constexpr (PV) {
     const Plan p64 = plan_tiles<64, PV, QV>(P.rows, Q.rows, nkb);
@@ -792,7 +807,7 @@ extern "C" moe_status_t fp8_block_gemm(const uint8_t* a, int64_t lda, const floa
   if (!at(c, es) || !at(err, 4))
     return fail(MOE_ERR_INVALID_ARG, "tensors must be aligned to their elements");
   const Operand A = {a, M, lda, sa, ld_sa, true}, B = {b, N, ldb, sb, ld_sb, b_scale == 0};
-  const bool swapped = M <= BM;
+  const bool swapped = M <= kFewRows;
   const Operand &P = swapped ? B : A, &Q = swapped ? A : B;
   if ((P.rows + BM - 1) / BM * ((Q.rows + 15) / 16) > most)
     return fail(MOE_ERR_UNSUPPORTED, "too many tiles");

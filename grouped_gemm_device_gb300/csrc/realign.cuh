@@ -1,7 +1,7 @@
-// Bytes off 16-byte boundaries: rows whose stride is not a multiple of 16 bytes are read and written
-// in the aligned 16-byte blocks that they straddle, and the bytes moved in registers (three
-// conditional moves by 8, 4 and 2 bytes). An aligned block that holds a wanted byte lies in the same
-// allocation as that byte.
+// Bytes off 16-byte boundaries: rows whose stride is not a multiple of 16 bytes are read and
+// written in the aligned 16-byte blocks that they straddle, and the bytes moved in registers (three
+// conditional moves by 8, 4 and 2 bytes). An aligned block that holds a wanted byte lies in the
+// same allocation as that byte.
 #pragma once
 
 #include "common.cuh"
