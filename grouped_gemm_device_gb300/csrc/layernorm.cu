@@ -514,22 +514,23 @@ __global__ void __launch_bounds__(block_of(G)) ln_bwd_kernel(
   int slot = 0, turn = 0;
   float mu = row0 < M ? mean[row0] : 0.f, rs = row0 < M ? rstd[row0] : 0.f;
   for (int64_t row = row0; row < M; row += step) {
-    Raw<XT, VEC> h[PER], u[PER];
+    Raw<XT, VEC> xv[PER], dv[PER];
     const int ahead = slot == 0 ? S - 1 : slot - 1;
     fetch(row + (S - 1) * step, ahead);
     cp_async_wait<S - 1>();
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-      h[i] = ring_at(slot, i, 0);
-      u[i] = ring_at(slot, i, 1);
+      xv[i] = ring_at(slot, i, 0);
+      dv[i] = ring_at(slot, i, 1);
     }
     const float m0 = mu, r0 = rs;
     if (row + step < M) {  // the next row's statistics
       mu = mean[row + step];
       rs = rstd[row + step];
     }
-    // c = x - mean; the sums over the row are of u and u c, rstd goes into their factors
-    float c_[kKeep ? PER : 1][VEC], u_[kKeep ? PER : 1][VEC];
+    // h = (x - mean) rstd is formed first: products of rstd alone leave fp32's range (rstd^3 is 0
+    // for rows of a spread above 1e15) where h, u and dx do not
+    float h_[kKeep ? PER : 1][VEC], u_[kKeep ? PER : 1][VEC];
     float s1 = 0.f, s2 = 0.f;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
@@ -539,14 +540,14 @@ __global__ void __launch_bounds__(block_of(G)) ln_bwd_kernel(
         if (!kKeep && gamma) load_weights<ANY, WT, VEC>(gamma, c, N, wvec, gv);
 #pragma unroll
         for (int j = 0; j < VEC; ++j) {
-          const float cj = raw_at(h[i], j) - m0, d = raw_at(u[i], j);
-          dg[i][j] += (d * r0) * cj;
+          const float hj = (raw_at(xv[i], j) - m0) * r0, d = raw_at(dv[i], j);
+          dg[i][j] += d * hj;
           db[i][j] += d;
           const float uj = kKeep ? d * gm[kKeep ? i : 0][j] : gamma ? d * gv[j] : d;
           s1 += uj;
-          s2 += uj * cj;
+          s2 += uj * hj;
           if (kKeep) {
-            c_[kKeep ? i : 0][j] = cj;
+            h_[kKeep ? i : 0][j] = hj;
             u_[kKeep ? i : 0][j] = uj;
           }
         }
@@ -554,29 +555,29 @@ __global__ void __launch_bounds__(block_of(G)) ln_bwd_kernel(
     }
     row_sum2<G>(s1, s2, sm, turn);
     turn ^= 1;
-    const float k1 = r0 * (s1 / (float)N), k2 = (r0 * r0) * r0 * (s2 / (float)N);
+    const float k1 = r0 * (s1 / (float)N), k2 = r0 * (s2 / (float)N);
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
       const int c = (i * G + t) * VEC - lead;
       if (c < N) {
         if (!kKeep) {  // once more from the ring: registers are short here
-          h[i] = ring_at(slot, i, 0);
-          u[i] = ring_at(slot, i, 1);
+          xv[i] = ring_at(slot, i, 0);
+          dv[i] = ring_at(slot, i, 1);
         }
         float gv[VEC], o[VEC];
         if (!kKeep && gamma) load_weights<ANY, WT, VEC>(gamma, c, N, wvec, gv);
 #pragma unroll
         for (int j = 0; j < VEC; ++j) {
-          float cj, uj;
+          float hj, uj;
           if constexpr (kKeep) {
-            cj = c_[i][j];
+            hj = h_[i][j];
             uj = u_[i][j];
           } else {
-            const float d = raw_at(u[i], j);
-            cj = raw_at(h[i], j) - m0;
+            const float d = raw_at(dv[i], j);
+            hj = (raw_at(xv[i], j) - m0) * r0;
             uj = gamma ? d * gv[j] : d;
           }
-          o[j] = (r0 * uj - k1) - cj * k2;
+          o[j] = (r0 * uj - k1) - hj * k2;
         }
         XT* at = dx + row * lddx + c;
         if (!ANY || (c >= 0 && c + VEC <= N)) store_vec<XT, VEC>(at, o);
