@@ -74,16 +74,10 @@ MOE_DEVICE float group_sum(float x, int L) {
   return x;
 }
 
-// 2^x, within 2 units of the last place; results below 2^-126 are 0.
-MOE_DEVICE float exp2_fast(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 // v <- exp(v - max) over the group; returns the reciprocal of their sum (1 to E). Under an
-// infinite maximum the values equal to it weigh 1 and the others 0. The exponent is rounded once
-// more by the factor log2(e), a relative |v - max| 2^-24 of a probability.
+// infinite maximum the values equal to it weigh 1 and the others 0. expf, as the layer's own
+// routing: a power of two with the exponent scaled by a rounded log2(e) would be off by a relative
+// |v - max| 2^-24 of a probability.
 template <int VEC, int V>
 MOE_DEVICE float softmax_row(float (&v)[V * VEC], int E, int L, int sub) {
   float m = v[0];
@@ -94,7 +88,7 @@ MOE_DEVICE float softmax_row(float (&v)[V * VEC], int E, int L, int sub) {
   if (fabsf(m) < INFINITY) {
 #pragma unroll
     for (int i = 0; i < V * VEC; ++i) {
-      v[i] = exp2_fast((v[i] - m) * 1.44269504f);
+      v[i] = expf(v[i] - m);
       s += v[i];
     }
   } else {

@@ -1,0 +1,55 @@
+"""The router loss's arithmetic beside its formula: exponentials of far logits, the reciprocal of a
+row's sum, and the sums over blocks, each where fewer bits would show."""
+import numpy as np
+import pytest
+import torch
+
+import grouped_gemm_device_gb300 as g
+from oracle import block_ops as ob
+
+pytestmark = pytest.mark.gpu
+ULP = 2.0 ** -24        # half an ulp of fp32, relative
+LEAST = 2.0 ** -149     # the smallest subnormal number
+
+
+def dev(a):
+    return torch.from_numpy(np.ascontiguousarray(a)).cuda()
+
+
+def far_rows(T, E, lo, hi, seed=0):
+    """Expert 0 at 0, the others at multiples of 1/8 in [lo, hi] below it, so that differences of
+    logits are exact and, with hi <= -24, the other weights together are below half an ulp of 1."""
+    r = np.random.default_rng([seed, T, E])
+    x = r.integers(8 * lo, 8 * hi + 1, (T, E)).astype(np.float32) / np.float32(8)
+    x[:, 0] = 0.0
+    return x, np.zeros((T, 1), np.int32)
+
+
+# exp: 2 ulp (4 units); the row's sum, its reciprocal and the product with it: one unit each; the
+# mean over one token: one more
+P_UNITS = 8
+
+
+@pytest.mark.parametrize("E", [5, 64, 255, 256])
+@pytest.mark.parametrize("lo,hi", [(-86, -24), (-103, -88)])
+def test_probabilities_of_far_logits(lib, E, lo, hi):
+    plan = g.RouterLoss(E, 1, 1)
+    for seed in range(6):
+        x, ids = far_rows(1, E, lo, hi, seed)
+        p = plan.forward(dev(x), dev(ids))[2].double().cpu().numpy()
+        want = ob.softmax(x.astype(np.float64))[0]
+        assert (np.abs(p - want) <= P_UNITS * ULP * want + 2 * LEAST).all()
+
+
+@pytest.mark.parametrize("E", [5, 64, 255, 256])
+@pytest.mark.parametrize("lo,hi", [(-86, -24), (-103, -88)])
+def test_gradient_of_far_logits(lib, E, lo, hi):
+    """d = c p (f - s) with f = (E, 0, ..), s = E to half an ulp: beside p's units four roundings
+    of the factors and of s."""
+    T = 64
+    x, ids = far_rows(T, E, lo, hi)
+    plan = g.RouterLoss(E, 1, T, coef=float(T))
+    plan.forward(dev(x), dev(ids))
+    d = plan.backward(dev(x), dev(ids)).double().cpu().numpy()
+    want, size = ob.router_grad(x.astype(np.float64), ids, float(T))
+    assert (np.abs(d - want) <= (P_UNITS + 4) * ULP * size + 3 * E * LEAST).all()
