@@ -102,7 +102,7 @@ MOE_DEVICE float softmax_row(float (&v)[V * VEC], int E, int L, int sub) {
       }
   }
   __syncwarp();
-  return __fdividef(1.0f, group_sum(s, L));
+  return 1.0f / group_sum(s, L);
 }
 
 struct Results {

@@ -53,3 +53,12 @@ def test_gradient_of_far_logits(lib, E, lo, hi):
     d = plan.backward(dev(x), dev(ids)).double().cpu().numpy()
     want, size = ob.router_grad(x.astype(np.float64), ids, float(T))
     assert (np.abs(d - want) <= (P_UNITS + 4) * ULP * size + 3 * E * LEAST).all()
+
+
+def test_equal_logits_have_the_rounded_reciprocal(lib):
+    """E equal weights of 1: a probability is fp32's 1 / E, every other step being exact."""
+    for E in range(1, 257):
+        plan = g.RouterLoss(E, 1, 1)
+        x = torch.full((1, E), 0.75, device="cuda")
+        p = plan.forward(x, torch.zeros(1, 1, dtype=torch.int32, device="cuda"))[2]
+        assert (p.cpu().numpy() == np.float32(1) / np.float32(E)).all(), E
