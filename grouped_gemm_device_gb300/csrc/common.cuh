@@ -105,6 +105,14 @@ MOE_DEVICE void st_global_v8(void* dst, const uint32_t* w) {
                : "memory");
 }
 
+// ----------------------------------------------------------------------------- sums as pairs
+// (hi, lo) += x with no error but the rounding of lo (error-free sum of two numbers, Knuth 1969)
+MOE_DEVICE void add_to(float& hi, float& lo, float x) {
+  const float s = hi + x, v = s - hi;
+  lo += (hi - (s - v)) + (x - v);
+  hi = s;
+}
+
 // ----------------------------------------------------------------------------- smem / timer
 MOE_DEVICE uint32_t smem_u32(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));

@@ -88,12 +88,6 @@ struct Sum {
   float hi, lo;
   double odd;
 };
-// (hi, lo) += x with no error but the rounding of lo
-MOE_DEVICE void add_to(float& hi, float& lo, float x) {
-  const float s = hi + x, v = s - hi;
-  lo += (hi - (s - v)) + (x - v);
-  hi = s;
-}
 
 // Adds the squares of one thread's share of a chunk: at most 32 of them in fp32 where their sum
 // is well inside its range; otherwise (an overflow, a NaN, or squares that may have been lost

@@ -110,14 +110,35 @@ struct Results {
   int32_t* counts;
   float* mean_prob;
   int32_t* n_valid;
-  float coef;
+  double scale;  // coef E / k
 };
-// Writes an expert's count and mean probability; returns its term of the loss.
-MOE_DEVICE float finish_expert(int e, float p, int c, int n, int E, int k, const Results& out) {
+// Writes an expert's count and mean probability; returns its term of the loss but for scale / n, as
+// a pair: the terms are added with more bits than one of them has.
+MOE_DEVICE float2 finish_expert(int e, float p, int c, int n, const Results& out) {
   const float mp = n > 0 ? p / (float)n : 0.f;
   out.mean_prob[e] = mp;
   out.counts[e] = c;
-  return n > 0 ? mp * ((float)E * (float)c / ((float)k * (float)n)) : 0.f;
+  const float x = mp * (float)c;
+  return make_float2(x, __fmaf_rn(mp, (float)c, -x));
+}
+MOE_DEVICE void add_pair(float2& x, float2 y) {
+  add_to(x.x, x.y, y.x);
+  x.y += y.y;
+}
+MOE_DEVICE float2 warp_sum(float2 x) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+    add_pair(x, make_float2(__shfl_xor_sync(0xFFFFFFFFu, x.x, o),
+                            __shfl_xor_sync(0xFFFFFFFFu, x.y, o)));
+  return x;
+}
+// The loss from the sum of its terms, rounded once. 1/n is fp32's with a step of Newton's method
+// in fp64, 46 bits; an fp64 division takes a microsecond of a kernel this short (4096 x 256: 8.6 us
+// against 7.3).
+MOE_DEVICE float scaled(float2 sum, int n, const Results& out) {
+  if (n == 0) return 0.f;
+  const double r = 1.0f / (float)n;
+  return (float)(((double)sum.x + sum.y) * (out.scale * (r + r * (1.0 - n * r))));
 }
 
 // FULL: a token has the whole warp, known when compiling, so that the reductions are straight code.
@@ -189,42 +210,43 @@ __global__ void __launch_bounds__(kLossThreads) router_loss_kernel(
     return;
   }
   // a single block: the results themselves
-  __shared__ float terms[8];
+  __shared__ float2 terms[8];
   const int n = hist[E];
-  float x = e < E ? finish_expert(e, o.p, o.c, n, E, k, out) : 0.f;
-  if (e < 256) {  // whole warps; E <= 256
-    x = group_sum(x, 32);
+  if (warp * 32 < E) {  // E <= 256
+    const float2 x = warp_sum(e < E ? finish_expert(e, o.p, o.c, n, out) : make_float2(0.f, 0.f));
     if (lane == 0) terms[warp] = x;
   }
   __syncthreads();
   if (threadIdx.x == 0) {
-    x = 0.f;
-    for (int w = 0; w < 8; ++w) x += terms[w];
-    *out.loss = out.coef * x;
+    float2 x = make_float2(0.f, 0.f);
+    for (int w = 0; w * 32 < E; ++w) add_pair(x, terms[w]);
+    *out.loss = scaled(x, n, out);
     *out.n_valid = n;
   }
 }
 
 // Sums the blocks' partials in a fixed order and forms the loss: one cluster, CTA c for experts
-// 32 c .., its warp w for every eighth partial.
+// 32 c .., its warp w for every eighth partial. The sums are pairs of fp32 numbers (65536 x 256:
+// fp64 ones, two a cycle and SM, would take 1.2 us): a block's share that fp32 loses beside a
+// larger one counts.
 __global__ void __launch_bounds__(256)
-    router_loss_finish_kernel(const Partial* __restrict__ part, int nblk, int E, int k,
+    router_loss_finish_kernel(const Partial* __restrict__ part, int nblk, int E,
                               const Results out) {
   MOE_GRIDDEP_ENTRY();
-  __shared__ float sp[8][32];
+  __shared__ float sp[8][32], sl[8][32];
   __shared__ int sc[8][32];
   __shared__ int sn[8];
-  __shared__ float term;
+  __shared__ float2 term;
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const uint32_t rank = cluster_ctarank();
   const int e = (int)rank * 32 + lane;
-  float p = 0.f;
+  float p = 0.f, lo = 0.f;
   int c = 0, n = 0;
   if (e < E) {
 #pragma unroll 4
     for (int b = w; b < nblk; b += 8) {
       const Partial q = part[(int64_t)b * (E + 1) + e];
-      p += q.p;
+      add_to(p, lo, q.p);
       c += q.c;
     }
   }
@@ -232,36 +254,39 @@ __global__ void __launch_bounds__(256)
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xFFFFFFFFu, n, o);
   sp[w][lane] = p;
+  sl[w][lane] = lo;
   sc[w][lane] = c;
   if (lane == 0) sn[w] = n;
   __syncthreads();
   n = 0;
   for (int i = 0; i < 8; ++i) n += sn[i];
   if (w == 0) {
-    float x = 0.f;
+    float2 x = make_float2(0.f, 0.f);
     if (e < E) {
-      p = 0.f;
+      p = lo = 0.f;
       c = 0;
       for (int i = 0; i < 8; ++i) {
-        p += sp[i][lane];
+        add_to(p, lo, sp[i][lane]);
+        lo += sl[i][lane];
         c += sc[i][lane];
       }
-      x = finish_expert(e, p, c, n, E, k, out);
+      x = finish_expert(e, p + lo, c, n, out);
     }
-    x = group_sum(x, 32);
+    x = warp_sum(x);
     if (lane == 0) term = x;
   }
   __syncthreads();
   cluster_sync_all();
   if (rank == 0 && threadIdx.x == 0) {
-    float s = 0.f;
+    float2 s = make_float2(0.f, 0.f);
+#pragma unroll
     for (uint32_t r = 0; r < kFinishCtas; ++r) {
-      float v;
-      asm volatile("ld.shared::cluster.f32 %0, [%1];"
-                   : "=f"(v) : "r"(mapa_shared(smem_u32(&term), r)) : "memory");
-      s += v;
+      float2 v;
+      asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];"
+                   : "=f"(v.x), "=f"(v.y) : "r"(mapa_shared(smem_u32(&term), r)) : "memory");
+      add_pair(s, v);
     }
-    *out.loss = out.coef * s;
+    *out.loss = scaled(s, n, out);
     *out.n_valid = n;
   }
   __syncthreads();
@@ -468,7 +493,7 @@ moe_status_t moe_router_loss_fwd(const float* logits, int64_t ld_logits, const i
   // two, 2048 x 8: 5.6 against 5.4; eight turns 8.3 against 5.5), and 2 us less on the host
   int nblk = router_blocks(T, m, kLossWarps, std::min(std::max(device_sms(), 1), kMaxBlocks));
   if (nblk <= 4) nblk = 1;
-  const Results out = {loss, counts, mean_prob, n_valid, coef};
+  const Results out = {loss, counts, mean_prob, n_valid, (double)coef * E / k};
   Partial* part = static_cast<Partial*>(ws);
   cudaError_t e = cudaSuccess;
   with_map(m, [&](auto vec, auto v, auto full) {
@@ -479,7 +504,7 @@ moe_status_t moe_router_loss_fwd(const float* logits, int64_t ld_logits, const i
   if (e != cudaSuccess) return cuda_fail(e, "router loss launch");
   if (nblk == 1) return MOE_OK;
   e = launch_pdl(router_loss_finish_kernel, kFinishCtas, 256, 0, s, kFinishCtas,
-                 (const Partial*)part, nblk, E, k, out);
+                 (const Partial*)part, nblk, E, out);
   count_launch(s, MOE_K_ROUTER_LOSS);
   if (e != cudaSuccess) return cuda_fail(e, "router loss finish launch");
   return MOE_OK;

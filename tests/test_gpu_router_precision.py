@@ -62,3 +62,41 @@ def test_equal_logits_have_the_rounded_reciprocal(lib):
         x = torch.full((1, E), 0.75, device="cuda")
         p = plan.forward(x, torch.zeros(1, 1, dtype=torch.int32, device="cuda"))[2]
         assert (p.cpu().numpy() == np.float32(1) / np.float32(E)).all(), E
+
+
+def test_blocks_are_added_with_more_bits_than_a_block_has(lib):
+    """One warp's worth of tokens an SM and warp. The first 32 put all weight on expert 0, the
+    others 5.5e-8: 32 of those are less than half an ulp of 32, all of them together 35 ulp."""
+    E, per = 256, 32
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    T = per * sms
+    x = np.full((T, E), -40.0, np.float32)
+    x[:per, 0] = 0.0
+    x[per:, 1] = 0.0
+    x[per:, 0] = np.log(5.5e-8)
+    ids = np.zeros((T, 1), np.int32)
+    plan = g.RouterLoss(E, 1, T, coef=1.0)
+    loss, _, mean_prob = plan.forward(dev(x), dev(ids))
+    want_loss, _, want, _, _ = ob.router_loss(x.astype(np.float64), ids, 1.0)
+    # expert 0: exact ones, small terms to a few units of themselves, one sum rounded and divided
+    assert abs(float(mean_prob[0].double()) - want[0]) <= 3 * ULP * want[0]
+    assert abs(float(loss.double()) - want_loss) <= 4 * ULP * want_loss
+
+
+@pytest.mark.parametrize("T", [25, 1000])
+def test_loss_is_the_sum_of_its_terms(lib, T):
+    """Against its own counts and mean probabilities in 64 bits. Seven experts, 32 apart, have terms
+    just below half an ulp of expert 0's. mean_prob's rounding and the loss's own: 2 units."""
+    E = 256
+    x = np.full((T, E), -60.0, np.float32)
+    x[:, 0] = 0.0
+    x[:, 32::32] = -14.75
+    ids = np.zeros((T, 1), np.int32)
+    few = max(1, 68 * T // 1000)
+    for i in range(1, 8):
+        ids[(i - 1) * few:i * few] = 32 * i
+    plan = g.RouterLoss(E, 1, T, coef=1.0)
+    loss, counts, mean_prob = plan.forward(dev(x), dev(ids))
+    f = counts.double() * E / T
+    want = float((f * mean_prob.double()).sum())
+    assert abs(float(loss.double()) - want) <= 2.5 * ULP * want
