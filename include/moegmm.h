@@ -433,7 +433,8 @@ moe_status_t moe_layernorm_bwd(const void *dy, int64_t lddy, const void *x, int6
  *   norm = sqrt(sum over all elements of g^2),  c = min(1, max_norm / (norm + 1e-6)),  out = c*g
  * A NaN anywhere makes norm and c NaN; an infinite element makes c 0 (and itself NaN). Finite
  * gradients of any magnitude have a finite sum: up to 32 squares at a time are added in fp32, those
- * sums as pairs of fp32 numbers, and what leaves fp32's range in fp64. norm is rounded to fp32.
+ * sums as pairs of fp32 numbers, and what leaves fp32's range in fp64. norm is rounded to fp32:
+ * above 3.4e38 it is returned as +inf, while c and out are those of the finite norm.
  *   grads   HOST array of n device pointers (element-aligned; a 16-byte aligned start is not
  *           needed), numel HOST array of their element counts (>= 0), dtypes HOST array of
  *           moe_dtype_t
