@@ -718,9 +718,28 @@ class LayerNorm:
         return _first(self.dx, M), self.dgamma, self.dbeta
 
 
+def _collide(grads, outs) -> bool:
+    """True where a tensor that is written shares memory with another one. (address, bytes) of each
+    gradient and of its out, which may be the gradient itself."""
+    spans = []
+    for g, o in zip(grads, outs):
+        spans.append((o[0], o[0] + o[1], True))
+        if o != g:
+            spans.append((g[0], g[0] + g[1], False))
+    end = end_written = 0
+    for lo, hi, written in sorted(s for s in spans if s[1] > s[0]):
+        if lo < (end if written else end_written):
+            return True
+        end = max(end, hi)
+        if written:
+            end_written = max(end_written, hi)
+    return False
+
+
 class GradClip:
     """Global norm of a fixed list of gradient tensors, and clipping in place or into `outs`
-    (moe_grad_clip). Holds references to the tensors: their memory stays where it is."""
+    (moe_grad_clip). Holds references to the tensors: their memory stays where it is. A tensor that
+    clipping writes shares memory with no other one."""
 
     def __init__(self, grads, outs=None):
         import torch
@@ -740,6 +759,8 @@ class GradClip:
         self._numel = (_I64 * n)(*[g.numel() for g in self.grads])
         self._types = (_I32 * n)(*[_dtype_code(g.dtype) for g in self.grads])
         self._at = [ctypes.addressof(a) for a in (self._in, self._out, self._numel, self._types)]
+        self._shared = _collide(*[[(t.data_ptr(), t.numel() * t.element_size()) for t in ts]
+                                  for ts in (self.grads, self.outs)])
         self.norm = torch.zeros(1, dtype=torch.float32, device=dev)
         self.ws_bytes = moe_grad_clip_workspace()
         self.ws = torch.empty(self.ws_bytes, dtype=torch.uint8, device=dev)
@@ -748,6 +769,8 @@ class GradClip:
 
     def clip(self, max_norm, stream=None):
         """Returns the norm [1] (on the device). max_norm = inf only takes the norm."""
+        if self._shared and max_norm != math.inf:
+            raise ValueError("a tensor to be written shares memory with another one")
         at = self._at
         _check(self._lib.moe_grad_clip(self.n, at[0], None if max_norm == math.inf else at[1],
                                        at[2], at[3], max_norm, *self._work, _stream(stream)))

@@ -1,0 +1,32 @@
+"""What the operator classes keep between calls: calls that need an earlier one, and the streams on
+which a call's own memory is made and written."""
+import pytest
+import torch
+
+import grouped_gemm_device_gb300 as g
+
+pytestmark = pytest.mark.gpu
+BF = torch.bfloat16
+
+
+def rows(M, N, dtype=BF, seed=0):
+    gen = torch.Generator().manual_seed(seed)
+    return torch.randn(M, N, generator=gen).to(dtype).cuda()
+
+
+def test_clip_refuses_tensors_that_share_memory(lib):
+    t = torch.ones(100, device="cuda")
+    with pytest.raises(ValueError):
+        g.GradClip([t, t]).clip(1.0)
+    with pytest.raises(ValueError):
+        g.GradClip([t[:60], t[40:]]).clip(1.0)
+    with pytest.raises(ValueError):
+        g.GradClip([t[:50]], [t[25:75]]).clip(1.0)
+    assert torch.equal(t, torch.ones_like(t))
+    # reading a tensor twice is a matter of the caller's norm
+    assert abs(float(g.GradClip([t, t]).clip(float("inf"))) - 200 ** 0.5) <= 1e-5
+    outs = [torch.empty_like(t), torch.empty_like(t)]
+    g.GradClip([t, t], outs).clip(1.0)
+    assert torch.equal(outs[0], outs[1])
+    g.GradClip([t[:50], t[50:]]).clip(1.0)
+    assert abs(float(t.norm()) - 1.0) <= 1e-5
