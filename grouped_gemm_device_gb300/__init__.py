@@ -675,6 +675,7 @@ class LayerNorm:
         self.mean = torch.empty(M_max, dtype=torch.float32, device=dev)
         self.rstd = torch.empty(M_max, dtype=torch.float32, device=dev)
         self.dx = None
+        self.M = None  # rows of the last forward
         self._lib = _load_calls()
         self._out = self.y.data_ptr(), N, self.mean.data_ptr(), self.rstd.data_ptr()
 
@@ -693,15 +694,18 @@ class LayerNorm:
             x.data_ptr(), _ld(x), _ptr(self._weight(gamma, "gamma")),
             _ptr(self._weight(beta, "beta")), *self._out, M, self.N, self.eps, *self._codes,
             _stream(stream)))
+        self.M = M
         return _first(self.y, M), _first(self.mean, M), _first(self.rstd, M)
 
     def backward(self, dy, x, gamma=None, mean=None, rstd=None, stream=None):
-        """mean, rstd: the forward's (None: those of the last forward). Returns
-        (dx [M, N], dgamma [N], dbeta [N])."""
+        """mean, rstd: the forward's (None: those of the last forward, which had as many rows or
+        more). Returns (dx [M, N], dgamma [N], dbeta [N])."""
         import torch
         M = self._rows(x, "x")
         if self._rows(dy, "dy") != M:
             raise ValueError("dy and x differ in rows")
+        if (mean is None or rstd is None) and (self.M is None or M > self.M):
+            raise ValueError(f"no forward of {M} rows has left mean and rstd")
         mean = self.mean if mean is None else _expect(mean, "mean", torch.float32, (M,))
         rstd = self.rstd if rstd is None else _expect(rstd, "rstd", torch.float32, (M,))
         if self.dx is None:

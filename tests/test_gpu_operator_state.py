@@ -14,6 +14,33 @@ def rows(M, N, dtype=BF, seed=0):
     return torch.randn(M, N, generator=gen).to(dtype).cuda()
 
 
+def test_layernorm_backward_needs_statistics(lib):
+    ln, other = g.LayerNorm(64, 8), g.LayerNorm(64, 8)
+    x, dy = rows(8, 64), rows(8, 64, seed=1)
+    with pytest.raises(ValueError):
+        ln.backward(dy, x)
+    _, mean, rstd = other.forward(x)
+    for kw in (dict(mean=mean), dict(rstd=rstd)):
+        with pytest.raises(ValueError):
+            ln.backward(dy, x, **kw)
+    want = [t.clone() for t in other.backward(dy, x)]
+    for a, b in zip(want, ln.backward(dy, x, mean=mean, rstd=rstd)):  # both given: no forward needed
+        assert torch.equal(a, b)
+
+
+def test_layernorm_backward_of_more_rows_than_the_forward_had(lib):
+    ln = g.LayerNorm(64, 8)
+    x, dy = rows(8, 64), rows(8, 64, seed=1)
+    want = [t.clone() for t in (ln.forward(x)[0], *ln.backward(dy, x))]
+    ln.forward(x[:4])
+    with pytest.raises(ValueError):
+        ln.backward(dy, x)
+    with pytest.raises(ValueError):
+        ln.backward(dy[:5], x[:5])
+    for m in (4, 2):
+        assert torch.equal(ln.backward(dy[:m], x[:m])[0], want[1][:m])
+
+
 def test_clip_refuses_tensors_that_share_memory(lib):
     t = torch.ones(100, device="cuda")
     with pytest.raises(ValueError):
