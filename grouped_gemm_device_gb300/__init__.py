@@ -610,6 +610,7 @@ class RouterLoss:
         self.mean_prob = torch.zeros(E, dtype=torch.float32, device=dev)
         self.n_valid = torch.zeros(1, dtype=torch.int32, device=dev)
         self.d_logits = torch.empty(T_max, E, dtype=torch.float32, device=dev)
+        self.has_counts = False
         # the buffers' addresses, taken once: a small call's time is the host's
         self._lib = _load_calls()
         self._p = {n: getattr(self, n).data_ptr() for n in
@@ -637,12 +638,16 @@ class RouterLoss:
             logits.data_ptr(), _ld(logits), topk_ids.data_ptr(), _ptr(token_mask), T, self.E,
             self.k, self.coef, p["loss"], p["counts"], p["mean_prob"], p["n_valid"], p["ws"],
             self.ws_bytes, _stream(stream)))
+        self.has_counts = True
         return self.loss, self.counts, self.mean_prob
 
     def backward(self, logits, topk_ids, topk_probs=None, d_probs=None, token_mask=None,
                  d_loss=None, stream=None):
-        """topk_probs and d_probs fp32 [T, k] (the layer's routing probabilities and the
-        gradient its backward gives them), d_loss fp32 [1] (None: 1). Returns d_logits [T, E]."""
+        """Of the last forward's tokens, all or some. topk_probs and d_probs fp32 [T, k] (the
+        layer's routing probabilities and the gradient its backward gives them), d_loss fp32 [1]
+        (None: 1). Returns d_logits [T, E]."""
+        if not self.has_counts:
+            raise ValueError("backward needs a forward's counts")
         T = self._tokens(logits, topk_ids, token_mask)
         for t, name in ((topk_probs, "topk_probs"), (d_probs, "d_probs")):
             if t is not None:

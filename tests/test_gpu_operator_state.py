@@ -41,6 +41,23 @@ def test_layernorm_backward_of_more_rows_than_the_forward_had(lib):
         assert torch.equal(ln.backward(dy[:m], x[:m])[0], want[1][:m])
 
 
+def test_router_loss_backward_needs_a_forward(lib):
+    plan = g.RouterLoss(8, 2, 16)
+    lg = rows(16, 8, torch.float32)
+    ids = torch.topk(lg, 2).indices.int()
+    with pytest.raises(ValueError):
+        plan.backward(lg, ids)
+    with pytest.raises(ValueError):
+        plan.forward(lg, ids.long())
+    with pytest.raises(ValueError):  # a refused forward is none
+        plan.backward(lg, ids)
+    plan.forward(lg, ids)
+    whole = plan.backward(lg, ids).clone()
+    assert whole.any()
+    # a part of the tokens under the whole forward's counts
+    assert torch.equal(plan.backward(lg[:5], ids[:5]), whole[:5])
+
+
 def test_clip_refuses_tensors_that_share_memory(lib):
     t = torch.ones(100, device="cuda")
     with pytest.raises(ValueError):
