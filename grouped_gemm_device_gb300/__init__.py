@@ -570,10 +570,32 @@ def _dtype_code(dtype) -> int:
     return code
 
 
-def _expect(t, name, dtype, shape, rows=False):
-    """A tensor argument's place, type, shape and strides: contiguous, or (rows) any row stride."""
-    if not t.is_cuda:
-        raise ValueError(f"{name}: must be on the GPU")
+def _gpu(device):
+    """A GPU, with its index."""
+    import torch
+    dev = torch.device(device)
+    if dev.type != "cuda":
+        raise ValueError(f"device must be a GPU, not {dev}")
+    return dev if dev.index is not None else torch.device("cuda", torch.cuda.current_device())
+
+
+def _call_stream(index, stream):
+    """The stream's handle, for a call whose memory is on GPU `index`: kernels go to the current
+    one."""
+    global _cuda
+    if _cuda is None:
+        import torch
+        torch.cuda.current_device()  # initialises CUDA
+        _cuda = torch._C
+    if _cuda._cuda_getDevice() != index:
+        raise ValueError(f"the buffers are on cuda:{index}, which is not the current device")
+    return _cuda._cuda_getCurrentRawStream(index) if stream is None else _stream(stream)
+
+
+def _expect(t, name, dtype, shape, index, rows=False):
+    """A tensor argument's GPU, type, shape and strides: contiguous, or (rows) any row stride."""
+    if t.get_device() != index:
+        raise ValueError(f"{name}: must be on cuda:{index}, not {t.device}")
     if t.dtype != dtype or t.shape != shape:
         raise ValueError(f"{name}: expected {dtype} {tuple(shape)}, "
                          f"got {t.dtype} {tuple(t.shape)}")
@@ -601,7 +623,8 @@ class RouterLoss:
 
     def __init__(self, E, k, T_max, coef=0.01, device="cuda"):
         import torch
-        dev = torch.device(device)
+        dev = self.device = _gpu(device)
+        self._gpu = dev.index
         self.E, self.k, self.T_max, self.coef = E, k, T_max, float(coef)
         self.ws_bytes = moe_router_loss_workspace(E)
         self.ws = torch.empty(self.ws_bytes, dtype=torch.uint8, device=dev)
@@ -620,13 +643,13 @@ class RouterLoss:
         T = logits.shape[0]
         if T > self.T_max:
             raise ValueError(f"{T} tokens, but T_max is {self.T_max}")
-        _expect(logits, "logits", self.loss.dtype, (T, self.E), rows=True)
-        _expect(topk_ids, "topk_ids", self.counts.dtype, (T, self.k))
+        _expect(logits, "logits", self.loss.dtype, (T, self.E), self._gpu, rows=True)
+        _expect(topk_ids, "topk_ids", self.counts.dtype, (T, self.k), self._gpu)
         if token_mask is not None:
             import torch
             if token_mask.dtype not in (torch.bool, torch.uint8):
                 raise ValueError("token_mask must be bool or uint8")
-            _expect(token_mask, "token_mask", token_mask.dtype, (T,))
+            _expect(token_mask, "token_mask", token_mask.dtype, (T,), self._gpu)
         return T
 
     def forward(self, logits, topk_ids, token_mask=None, stream=None):
@@ -637,7 +660,7 @@ class RouterLoss:
         _check(self._lib.moe_router_loss_fwd(
             logits.data_ptr(), _ld(logits), topk_ids.data_ptr(), _ptr(token_mask), T, self.E,
             self.k, self.coef, p["loss"], p["counts"], p["mean_prob"], p["n_valid"], p["ws"],
-            self.ws_bytes, _stream(stream)))
+            self.ws_bytes, _call_stream(self._gpu, stream)))
         self.has_counts = True
         return self.loss, self.counts, self.mean_prob
 
@@ -651,16 +674,16 @@ class RouterLoss:
         T = self._tokens(logits, topk_ids, token_mask)
         for t, name in ((topk_probs, "topk_probs"), (d_probs, "d_probs")):
             if t is not None:
-                _expect(t, name, self.loss.dtype, (T, self.k))
+                _expect(t, name, self.loss.dtype, (T, self.k), self._gpu)
         if d_loss is not None:
-            _expect(d_loss, "d_loss", self.loss.dtype, d_loss.shape)
+            _expect(d_loss, "d_loss", self.loss.dtype, d_loss.shape, self._gpu)
             if d_loss.numel() != 1:
                 raise ValueError("d_loss must hold one value")
         p = self._p
         _check(self._lib.moe_router_loss_bwd(
             logits.data_ptr(), _ld(logits), topk_ids.data_ptr(), _ptr(topk_probs), _ptr(d_probs),
             _ptr(token_mask), T, self.E, self.k, self.coef, _ptr(d_loss), p["counts"],
-            p["n_valid"], p["d_logits"], self.E, _stream(stream)))
+            p["n_valid"], p["d_logits"], self.E, _call_stream(self._gpu, stream)))
         return _first(self.d_logits, T)
 
 
@@ -670,12 +693,12 @@ class LayerNorm:
 
     def __init__(self, N, M_max, dtype=None, weight_dtype=None, eps=1e-5, device="cuda"):
         import torch
-        dev = torch.device(device)
+        dev = self.device = _gpu(device)
+        self._gpu = dev.index
         self.dtype = torch.bfloat16 if dtype is None else dtype
         self.weight_dtype = self.dtype if weight_dtype is None else weight_dtype
         self._codes = _dtype_code(self.dtype), _dtype_code(self.weight_dtype)
         self.N, self.M_max, self.eps = N, M_max, float(eps)
-        self.device = dev
         self.y = torch.empty(M_max, N, dtype=self.dtype, device=dev)
         self.mean = torch.empty(M_max, dtype=torch.float32, device=dev)
         self.rstd = torch.empty(M_max, dtype=torch.float32, device=dev)
@@ -687,10 +710,12 @@ class LayerNorm:
     def _rows(self, x, name):
         if x.dim() != 2 or x.shape[0] > self.M_max:
             raise ValueError(f"{name}: expected at most {self.M_max} rows of {self.N}")
-        return _expect(x, name, self.dtype, (x.shape[0], self.N), rows=True).shape[0]
+        return _expect(x, name, self.dtype, (x.shape[0], self.N), self._gpu, rows=True).shape[0]
 
     def _weight(self, w, name):
-        return None if w is None else _expect(w, name, self.weight_dtype, (self.N,))
+        if w is None:
+            return None
+        return _expect(w, name, self.weight_dtype, (self.N,), self._gpu)
 
     def forward(self, x, gamma=None, beta=None, stream=None):
         """Returns (y [M, N], mean [M], rstd [M])."""
@@ -698,7 +723,7 @@ class LayerNorm:
         _check(self._lib.moe_layernorm_fwd(
             x.data_ptr(), _ld(x), _ptr(self._weight(gamma, "gamma")),
             _ptr(self._weight(beta, "beta")), *self._out, M, self.N, self.eps, *self._codes,
-            _stream(stream)))
+            _call_stream(self._gpu, stream)))
         self.M = M
         return _first(self.y, M), _first(self.mean, M), _first(self.rstd, M)
 
@@ -711,8 +736,14 @@ class LayerNorm:
             raise ValueError("dy and x differ in rows")
         if (mean is None or rstd is None) and (self.M is None or M > self.M):
             raise ValueError(f"no forward of {M} rows has left mean and rstd")
-        mean = self.mean if mean is None else _expect(mean, "mean", torch.float32, (M,))
-        rstd = self.rstd if rstd is None else _expect(rstd, "rstd", torch.float32, (M,))
+        if mean is None:
+            mean = self.mean
+        else:
+            _expect(mean, "mean", torch.float32, (M,), self._gpu)
+        if rstd is None:
+            rstd = self.rstd
+        else:
+            _expect(rstd, "rstd", torch.float32, (M,), self._gpu)
         if self.dx is None:
             self.dx = torch.empty(self.M_max, self.N, dtype=self.dtype, device=self.device)
             self.dgamma = torch.empty(self.N, dtype=self.weight_dtype, device=self.device)
@@ -723,7 +754,7 @@ class LayerNorm:
             dy.data_ptr(), _ld(dy), x.data_ptr(), _ld(x), _ptr(self._weight(gamma, "gamma")),
             mean.data_ptr(), rstd.data_ptr(), self.dx.data_ptr(), self.N, self.dgamma.data_ptr(),
             self.dbeta.data_ptr(), M, self.N, *self._codes, self.ws.data_ptr(), self.ws_bytes,
-            _stream(stream)))
+            _call_stream(self._gpu, stream)))
         return _first(self.dx, M), self.dgamma, self.dbeta
 
 
@@ -759,10 +790,13 @@ class GradClip:
         for g, o in zip(self.grads, self.outs):
             if not (g.is_cuda and o.is_cuda and g.is_contiguous() and o.is_contiguous()):
                 raise ValueError("gradients and outs must be on the GPU and contiguous")
+            if g.device != self.grads[0].device or o.device != g.device:
+                raise ValueError("gradients and outs must be on one device")
             if g.dtype != o.dtype or g.shape != o.shape:
                 raise ValueError("an out differs from its gradient in type or shape")
         n = self.n = len(self.grads)
-        dev = self.grads[0].device if n else torch.device("cuda")
+        dev = self.device = self.grads[0].device if n else _gpu("cuda")
+        self._gpu = dev.index
         self._in = (_P * n)(*[g.data_ptr() for g in self.grads])
         self._out = (_P * n)(*[o.data_ptr() for o in self.outs])
         self._numel = (_I64 * n)(*[g.numel() for g in self.grads])
@@ -782,7 +816,8 @@ class GradClip:
             raise ValueError("a tensor to be written shares memory with another one")
         at = self._at
         _check(self._lib.moe_grad_clip(self.n, at[0], None if max_norm == math.inf else at[1],
-                                       at[2], at[3], max_norm, *self._work, _stream(stream)))
+                                       at[2], at[3], max_norm, *self._work,
+                                       _call_stream(self._gpu, stream)))
         return self.norm
 
 
@@ -797,7 +832,8 @@ class Fp8Linear:
 
     def __init__(self, N, K, M_max, train=True, device="cuda"):
         import torch
-        dev = torch.device(device)
+        dev = self.device = _gpu(device)
+        self._gpu = dev.index
         self.N, self.K, self.M_max, self.train = N, K, M_max, train
         self.nb, self.kb = -(-N // 128), -(-K // 128)
         self._kp, self._np, self._mp = _up(K, 16), _up(N, 16), _up(max(M_max, 1), 16)
@@ -840,10 +876,11 @@ class Fp8Linear:
     def set_weight(self, w, stream=None):
         """Quantise w bf16 [N, K] (both orders for training); again whenever w has changed."""
         import torch
-        _expect(w, "w", torch.bfloat16, (self.N, self.K), rows=True)
+        _expect(w, "w", torch.bfloat16, (self.N, self.K), self._gpu, rows=True)
         qt, ldqt, st, _ = self._wt if self.train else self._none
         _check(self._lib.fp8_block_quantize_weight(w.data_ptr(), _ld(w), self.N, self.K,
-                                                   *self._w[:3], qt, ldqt, st, _stream(stream)))
+                                                   *self._w[:3], qt, ldqt, st,
+                                                   _call_stream(self._gpu, stream)))
         self.has_weight = True
 
     def _quantize(self, x, M, N, row, col, stream):
@@ -860,8 +897,8 @@ class Fp8Linear:
         M = x.shape[0]
         if M > self.M_max:
             raise ValueError(f"{M} rows, but M_max is {self.M_max}")
-        _expect(x, "x", self.y.dtype, (M, self.K), rows=True)
-        stream = _stream(stream)
+        _expect(x, "x", self.y.dtype, (M, self.K), self._gpu, rows=True)
+        stream = _call_stream(self._gpu, stream)
         self._quantize(x, M, self.K, self._x, self._xt, stream)
         self._product(self._x, self._w, 1, self.y, M, self.N, self.K, stream)
         self.M = M
@@ -872,10 +909,10 @@ class Fp8Linear:
         if not self.train or self.M is None:
             raise ValueError("backward needs a layer made with train=True and a forward")
         M = self.M
-        _expect(dy, "dy", self.y.dtype, (M, self.N), rows=True)
+        _expect(dy, "dy", self.y.dtype, (M, self.N), self._gpu, rows=True)
         if M == 0:
             return self.dx[:0], self.dw.zero_()
-        stream = _stream(stream)
+        stream = _call_stream(self._gpu, stream)
         self._quantize(dy, M, self.N, self._dy, self._dyt, stream)
         self._product(self._dy, self._wt, 1, self.dx, M, self.K, self.N, stream)
         self._product(self._dyt, self._xt, 0, self.dw, self.N, self.K, M, stream)
