@@ -9,6 +9,7 @@ There is no fallback: if the shared library is missing, `load()` raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import importlib.machinery
 import importlib.util
@@ -592,6 +593,18 @@ def _call_stream(index, stream):
     return _cuda._cuda_getCurrentRawStream(index) if stream is None else _stream(stream)
 
 
+def _torch_on(index, stream):
+    """The context in which torch's own part of a call goes to the call's stream (None, torch's or a
+    handle)."""
+    import torch
+    if stream is None:
+        return contextlib.nullcontext()
+    if isinstance(stream, int):
+        stream = (torch.cuda.ExternalStream(stream, device=index) if stream
+                  else torch.cuda.default_stream(index))
+    return torch.cuda.stream(stream)
+
+
 def _expect(t, name, dtype, shape, index, rows=False):
     """A tensor argument's GPU, type, shape and strides: contiguous, or (rows) any row stride."""
     if t.get_device() != index:
@@ -911,7 +924,8 @@ class Fp8Linear:
         M = self.M
         _expect(dy, "dy", self.y.dtype, (M, self.N), self._gpu, rows=True)
         if M == 0:
-            return self.dx[:0], self.dw.zero_()
+            with _torch_on(self._gpu, stream):
+                return self.dx[:0], self.dw.zero_()
         stream = _call_stream(self._gpu, stream)
         self._quantize(dy, M, self.N, self._dy, self._dyt, stream)
         self._product(self._dy, self._wt, 1, self.dx, M, self.K, self.N, stream)

@@ -58,6 +58,24 @@ def test_router_loss_backward_needs_a_forward(lib):
     assert torch.equal(plan.backward(lg[:5], ids[:5]), whole[:5])
 
 
+def test_linear_backward_of_no_rows_writes_on_the_calls_stream(lib):
+    lin = g.Fp8Linear(64, 64, 8)
+    lin.set_weight(rows(64, 64))
+    empty = torch.empty(0, 64, dtype=BF, device="cuda")
+    for handle in (False, True):
+        s = torch.cuda.Stream()
+        torch.cuda.synchronize()
+        stream = s.cuda_stream if handle else s
+        lin.forward(empty, stream=stream)
+        with torch.cuda.stream(s):
+            torch.cuda._sleep(50_000_000)
+            lin.dw.fill_(7.0)
+        _, dw = lin.backward(empty, stream=stream)
+        s.synchronize()
+        torch.cuda.synchronize()
+        assert not dw.any()
+
+
 def test_clip_refuses_tensors_that_share_memory(lib):
     t = torch.ones(100, device="cuda")
     with pytest.raises(ValueError):
