@@ -758,11 +758,13 @@ class LayerNorm:
         else:
             _expect(rstd, "rstd", torch.float32, (M,), self._gpu)
         if self.dx is None:
-            self.dx = torch.empty(self.M_max, self.N, dtype=self.dtype, device=self.device)
-            self.dgamma = torch.empty(self.N, dtype=self.weight_dtype, device=self.device)
-            self.dbeta = torch.empty(self.N, dtype=self.weight_dtype, device=self.device)
             self.ws_bytes = moe_layernorm_workspace(self.M_max, self.N)
-            self.ws = torch.empty(self.ws_bytes, dtype=torch.uint8, device=self.device)
+            # what the current stream has given back may still be in use there
+            with _torch_on(self._gpu, stream):
+                self.dgamma = torch.empty(self.N, dtype=self.weight_dtype, device=self.device)
+                self.dbeta = torch.empty(self.N, dtype=self.weight_dtype, device=self.device)
+                self.ws = torch.empty(self.ws_bytes, dtype=torch.uint8, device=self.device)
+                self.dx = torch.empty(self.M_max, self.N, dtype=self.dtype, device=self.device)
         _check(self._lib.moe_layernorm_bwd(
             dy.data_ptr(), _ld(dy), x.data_ptr(), _ld(x), _ptr(self._weight(gamma, "gamma")),
             mean.data_ptr(), rstd.data_ptr(), self.dx.data_ptr(), self.N, self.dgamma.data_ptr(),

@@ -76,6 +76,30 @@ def test_linear_backward_of_no_rows_writes_on_the_calls_stream(lib):
         assert not dw.any()
 
 
+@pytest.mark.parametrize("handle", [False, True])
+def test_layernorm_backward_makes_its_buffers_on_the_calls_stream(lib, handle):
+    """Memory that the current stream has given back may still be in use there: a call on another
+    stream does not take it."""
+    M, N = 2048, 2048
+    x, dy = rows(M, N), rows(M, N, seed=1)
+    ln = g.LayerNorm(N, M)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    stream = s.cuda_stream if handle else s
+    ln.forward(x, stream=stream)
+    freed = [torch.empty(M, N, dtype=BF, device="cuda") for _ in range(3)]
+    held = [(t.data_ptr(), t.data_ptr() + 2 * M * N) for t in freed]
+    del freed
+    dx, dg, db = ln.backward(dy, x, stream=stream)
+    s.synchronize()
+    for lo, hi in held:
+        assert not lo <= dx.data_ptr() < hi
+    other = g.LayerNorm(N, M)
+    other.forward(x)
+    for a, b in zip((dx, dg, db), other.backward(dy, x)):
+        assert torch.equal(a, b)
+
+
 def test_clip_refuses_tensors_that_share_memory(lib):
     t = torch.ones(100, device="cuda")
     with pytest.raises(ValueError):
