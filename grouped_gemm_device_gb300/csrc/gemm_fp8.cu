@@ -28,8 +28,6 @@
 // every column's scale: 14336 x 4096 x 8192: 455 to 470 us, 2.1 PFLOP/s. Few rows: the weights'
 // bytes and some 4 us of launch, first loads and cluster sums: 1 x 4096 x 7168 7.5 us, 1 x 14336 x
 // 4096 10.7 us (5.5 TB/s, from L2), 128 x 4096 x 7168 11.0 us.
-#include <mutex>
-
 #include "gemm_common.cuh"
 #include "realign.cuh"
 
@@ -656,15 +654,12 @@ struct Operand {
   bool vec;
 };
 
-// Clusters of `split` CTAs of a kernel that fit the GPU at once (1: CTAs), asked once each.
+// Clusters of `split` CTAs of a kernel that fit the GPU at once (1: CTAs).
 template <int BN, bool PV, bool QV>
 int resident(int split) {
-  static int cache[kMaxSplit + 1] = {0};
-  static std::mutex mu;
-  std::lock_guard<std::mutex> lock(mu);
-  if (cache[split]) return cache[split];
-  int n = std::max(device_sms(), 1);
-  if (split > 1) {
+  if (split == 1) return std::max(device_sms(), 1);
+  static DeviceCache cache[kMaxSplit + 1];
+  return std::max(1, cache[split].get(current_device(), [&] {
     auto kern = fp8_gemm_kernel<BN, PV, QV>;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -677,13 +672,14 @@ int resident(int split) {
     cfg.dynamicSmemBytes = Smem<BN>::TOTAL;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
+    int n = 0;
     if (ensure_smem_attr(reinterpret_cast<const void*>(kern), Smem<BN>::TOTAL) != cudaSuccess ||
-        cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n < 1) {
+        cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess) {
       cudaGetLastError();  // clear the sticky-free error of a failed query
-      n = 1;
+      return 0;
     }
-  }
-  return cache[split] = n;
+    return n;
+  }));
 }
 
 struct Plan {
@@ -726,13 +722,17 @@ cudaError_t launch_gemm(Fp8Args& a, const Plan& plan, const Operand& P, const Op
       (QV && !tmap_scales(&a.tmSQ, Q.s, Q.rows, kb, Q.ld_s, BN)))
     return cudaErrorInvalidValue;
   auto kern = fp8_gemm_kernel<BN, PV, QV>;
-  // the register split waits for registers that the launch must have: checked once
-  static const int regs = [&] {
+  // the register split waits for registers that the launch must have
+  static DeviceCache cache;
+  cudaError_t e = cudaSuccess;
+  const int regs = cache.get(current_device(), [&] {
     cudaFuncAttributes at;
-    return cudaFuncGetAttributes(&at, kern) == cudaSuccess ? at.numRegs : 0;
-  }();
+    e = cudaFuncGetAttributes(&at, kern);
+    return e == cudaSuccess ? at.numRegs : 0;
+  });
+  if (e != cudaSuccess) return e;
   if (regs < Smem<BN>::LAUNCH_REGS) return cudaErrorInvalidConfiguration;
-  cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kern), Smem<BN>::TOTAL);
+  e = ensure_smem_attr(reinterpret_cast<const void*>(kern), Smem<BN>::TOTAL);
   if (e != cudaSuccess) return e;
   a.tiles_p = (int)((P.rows + BM - 1) / BM);
   a.tiles_q = (int)((Q.rows + BN - 1) / BN);

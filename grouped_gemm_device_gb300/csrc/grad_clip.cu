@@ -305,11 +305,10 @@ int fill_batch(Batch& b, int i, int n, const void* const* grads, void* const* ou
 // costs its start, 21.5 us against 18.2).
 template <class K>
 int clip_blocks(K kernel, int64_t chunks) {
-  static const int per_sm = [&] {
-    int n = 0;
-    return cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, kThreads, 0) == cudaSuccess &&
-                   n > 0 ? n : 1;
-  }();
+  static DeviceCache cache;
+  const int per_sm = std::max(1, cache.get(current_device(), [&] {
+    return blocks_per_sm(reinterpret_cast<const void*>(kernel), kThreads, 0);
+  }));
   const int64_t fit = (int64_t)std::max(device_sms(), 1) * per_sm;
   const int64_t most = std::min<int64_t>(kMaxBlocks, chunks > 64 * fit ? 2 * fit : fit);
   return (int)std::max<int64_t>(1, std::min(chunks, most));

@@ -5,6 +5,7 @@
 #include <utility>
 
 #include "common.cuh"
+#include "device_cache.h"
 
 namespace moe {
 
@@ -66,6 +67,10 @@ void set_last_error(const char* msg);
 moe_status_t fail(moe_status_t st, const char* fmt, ...);
 moe_status_t cuda_fail(cudaError_t e, const char* where);
 int device_sms();
+// the current device, -1 if there is none; and how many blocks of `threads` threads and `smem` bytes
+// of a kernel fit one of its SMs, 0 if that could not be had
+int current_device();
+int blocks_per_sm(const void* kernel, int threads, size_t smem);
 
 // route.cu
 __global__ void route_topk_kernel(const float* logits, int T, int E, int k, int32_t* ids,

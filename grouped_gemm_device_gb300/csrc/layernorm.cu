@@ -781,11 +781,10 @@ cudaError_t fwd_walk(const LnArgs& a) {
   auto kern = ln_fwd_walk_kernel<XT, WT, VEC, G, PER, S>;
   cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kern), smem);
   if (e != cudaSuccess) return e;
-  static const int per_sm = [&] {
-    int n = 0;
-    return cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, B, smem) == cudaSuccess && n > 0
-               ? n : 1;
-  }();
+  static DeviceCache cache;
+  const int per_sm = std::max(1, cache.get(current_device(), [&] {
+    return blocks_per_sm(reinterpret_cast<const void*>(kern), B, smem);
+  }));
   int64_t blocks = std::min<int64_t>((a.M + GROUPS - 1) / GROUPS,
                                      (int64_t)std::max(device_sms(), kCycle) * per_sm);
   if (blocks * GROUPS < a.M) blocks = blocks * GROUPS / kCycle * kCycle / GROUPS;
@@ -856,11 +855,10 @@ cudaError_t bwd_launch(LnArgs& a) {
   cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kern), smem);
   if (e != cudaSuccess) return e;
   // as many blocks as fit at once (at least two where registers allow), each a row of partials
-  static const int per_sm = [&] {
-    int n = 0;
-    return cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, B, smem) == cudaSuccess && n > 0
-               ? n : 1;
-  }();
+  static DeviceCache cache;
+  const int per_sm = std::max(1, cache.get(current_device(), [&] {
+    return blocks_per_sm(reinterpret_cast<const void*>(kern), B, smem);
+  }));
   const int64_t fit = (int64_t)std::max(device_sms(), 1) * per_sm;
   a.nparts = (int)std::max<int64_t>(
       1, std::min<int64_t>((a.M + GROUPS - 1) / GROUPS, std::min<int64_t>(fit, max_parts(a.N))));
