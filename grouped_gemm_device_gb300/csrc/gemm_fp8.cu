@@ -13,7 +13,7 @@
 // kind::f8f6f4), warps 4-11 hold the 128 x BN fp32 sums (warp w: TMEM lanes 32 (w % 4).., half of
 // the columns). P is the operand on the 128-row side, Q the one on the BN-column side.
 //   Many rows: P = a, Q = b, tiles of 128 x 256; a result row is contiguous in a thread.
-//   Few rows (M <= 64): P = b, Q = a (BN = M rounded up), so that the whole 128-row side is
+//   Few rows (up to 64): P = b, Q = a (BN = M rounded up), so that the whole 128-row side is
 //   filled with features and the small operand costs what it holds; the result is written
 //   transposed, one feature a lane.
 //   Tiles that do not fill the GPU (all of them, or those of the last round): the k-blocks are
@@ -745,10 +745,18 @@ cudaError_t launch_gemm(Fp8Args& a, const Plan& plan, const Operand& P, const Op
   return e;
 }
 
-// Rows up to which the swapped form is taken. 64 x 4096 x 7168: 9.0 us, not swapped 10.7 (though
-// 64 x 14336 x 4096 13.2 against 12.3); 128 rows: 11.3 against 11.0, 128 x 14336 x 4096 17.1 against
-// 13.0.
-constexpr int kFewRows = 64;
+// Whether the swapped form is taken: up to 32 rows always, up to 64 where the 128-feature tiles give
+// every CTA pair of SMs at most one and K has 12 k-blocks. Its tiles stay a load long, while many
+// of 64 rows write 64 transposed results a feature; with few k-blocks that is most of the time.
+// Measured with operands from HBM, swapped and not, us (M x N x K):
+//   32 x 4096 x 7168 9.7, 11.9    64 x 4096 x 7168 10.6, 12.1    64 x 14336 x 4096 15.4, 14.5
+//   32 x 14336 x 4096 13.9, 13.9  64 x 8192 x 8192 16.3, 20.4    64 x 32768 x 4096 29.0, 26.0
+//   32 x 1024 x 1024 4.3, 4.6     64 x 9728 x 4096 11.7, 12.5    64 x 9856 x 2048 9.7, 8.6
+//   32 x 2048 x 512 4.2, 3.5      64 x 2048 x 1536 5.7, 6.0      64 x 4096 x 1152 7.4, 5.9
+// (the rule loses at 32 x 2048 x 512, and 64 x 7168 x 2048: 8.1, 7.6).
+bool few_rows(int64_t M, int64_t N, int64_t K) {
+  return M <= 32 || (M <= 64 && (N + BM - 1) / BM * 2 <= device_sms() && K >= 12 * BK);
+}
 
 // The widths in turn: the one whose plan ends first. Few rows take the narrowest tile that holds
 // them (swapped form); otherwise
@@ -807,7 +815,7 @@ extern "C" moe_status_t fp8_block_gemm(const uint8_t* a, int64_t lda, const floa
   if (!at(c, es) || !at(err, 4))
     return fail(MOE_ERR_INVALID_ARG, "tensors must be aligned to their elements");
   const Operand A = {a, M, lda, sa, ld_sa, true}, B = {b, N, ldb, sb, ld_sb, b_scale == 0};
-  const bool swapped = M <= kFewRows;
+  const bool swapped = few_rows(M, N, K);
   const Operand &P = swapped ? B : A, &Q = swapped ? A : B;
   if ((P.rows + BM - 1) / BM * ((Q.rows + 15) / 16) > most)
     return fail(MOE_ERR_UNSUPPORTED, "too many tiles");
