@@ -6,8 +6,8 @@
 // hold a block. Anything with columns takes 128 x 128 tiles, so that every scale it needs, in
 // either direction, is a maximum over values the thread block holds and one read of the input
 // serves both copies. Rows alone: 8192 x 14336 53 us (6.7 TB/s, all of the measured copy rate);
-// both copies: 93 us (5.1 TB/s; the tile's barriers and its pass through shared memory); weights of
-// 14336 x 4096, both orders: 42 us (5.6 TB/s); one row of 7168: 1.8 us. Maxima are taken on the
+// both copies: 95 us (5.0 TB/s; the tile's barriers and its pass through shared memory); weights of
+// 14336 x 4096, both orders: 42 us (5.6 TB/s); one row of 7168: 1.7 us. Maxima are taken on the
 // bf16 values themselves (a maximum rounds nothing), two at a time.
 #include "kernels.cuh"
 #include "realign.cuh"

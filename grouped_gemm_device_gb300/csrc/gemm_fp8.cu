@@ -22,12 +22,13 @@
 //
 // What bounds it. Many rows: a k-block of 128 x 256 moves 48 KB into shared memory and 48 KB out of
 // it into the tensor cores, and its product waits for the sums of the one before the last to leave
-// TMEM: 400 to 450 ns where the MMAs alone take about 300. 8192 x 14336 x 4096 (M x N x K): 345 us,
-// 2.8 PFLOP/s; 8192 x 4096 x 14336: 319 us, 3.0; 4096 x 4096 x 7168: 90 us, 2.7. Two 1 x 128
-// operands (weight gradients) need a second packed product a pair of results, and every lane reads
-// every column's scale: 14336 x 4096 x 8192: 455 to 470 us, 2.1 PFLOP/s. Few rows: the weights'
-// bytes and some 4 us of launch, first loads and cluster sums: 1 x 4096 x 7168 7.5 us, 1 x 14336 x
-// 4096 10.7 us (5.5 TB/s, from L2), 128 x 4096 x 7168 11.0 us.
+// TMEM: 400 to 450 ns where the MMAs alone take about 300. 8192 x 14336 x 4096 (M x N x K): 345 to
+// 380 us by what the power cap leaves, 2.5 to 2.8 PFLOP/s; 8192 x 4096 x 14336: 334 to 360 us, 2.7 to
+// 2.9; 4096 x 4096 x 7168: 91 us, 2.6. Two 1 x 128 operands (weight gradients) need a second packed
+// product a pair of results, and every lane reads every column's scale: 14336 x 4096 x 8192: 476 us,
+// 2.0 PFLOP/s. Few rows: the weights' bytes and some 4 us of launch, first loads and cluster sums:
+// with the weights from HBM (from L2) 1 x 4096 x 7168 9.1 us (7.6), 1 x 14336 x 4096 12.7 us (11.0),
+// 4.6 TB/s (5.3), 128 x 4096 x 7168 12.3 us (10.9).
 #include "gemm_common.cuh"
 #include "realign.cuh"
 

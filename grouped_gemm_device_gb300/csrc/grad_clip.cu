@@ -4,10 +4,10 @@
 //   norm = sqrt(sum g^2),  c = min(1, max_norm / (norm + 1e-6)),  out = c g
 //
 // Bound by HBM: one read of every gradient for the norm, one read and one write for the product.
-// 1.41 G bf16 elements 1250 us (6.7 TB/s over the three passes, the measured copy rate), 20 M 18
-// us, 60 k fp32 in place and not clipped 3.9 us (two launches). Two kinds of launch: partial sums
-// (one a block), then the product, whose blocks each add up the partial sums in the same order, so
-// that no launch, counter or atomic joins them.
+// 1.41 G bf16 elements 1250 us (6.7 TB/s over the three passes, the measured copy rate), 20 M 22
+// us (17 with its inputs in L2), 60 k fp32 3.9 us in place and not clipped. Two kinds of launch:
+// partial sums (one a block), then the product, whose blocks each add up the partial sums in the
+// same order, so that no launch, counter or atomic joins them.
 // Sums are pairs of fp32 numbers (a running sum and what its roundings lost, by the error-free sum
 // of two numbers, Knuth 1969): about 48 bits at the full fp32 rate, where this GPU adds two fp64
 // numbers an SM and cycle. Squares that fp32 cannot hold go into an fp64 sum of their own.

@@ -7,10 +7,10 @@
 // Bound by HBM: the forward reads and writes M N elements once, the backward reads x and dy and
 // writes dx once. A row stays in registers between its statistics and its use, so the variance is
 // taken about the mean (two passes over registers, not E[x^2] - mean^2). Statistics, sums and the
-// weight-gradient partials are fp32. Forward of 8192 x 4096 bf16 23 us (5.9 TB/s), of 16384 x 2880
-// with fp32 weights 35 us (5.4 TB/s), of 4096 x 7168 fp32 37 us (6.3 TB/s), of one row of 7168 2.3
-// us; backward of 8192 x 4096 bf16 40 us (5.0 TB/s), of 4096 x 7168 fp32 59 us (5.9 TB/s), of which
-// the sum of the partials takes about 4. Widening bf16 runs at half the rate of the products, so it
+// weight-gradient partials are fp32. With inputs from HBM: forward of 8192 x 4096 bf16 23 us (5.7
+// TB/s), of 16384 x 2880 with fp32 weights 35 us (5.3 TB/s), of 4096 x 7168 fp32 38 us (6.2 TB/s),
+// of one row of 7168 2.1 us; backward of 8192 x 4096 bf16 42 us (4.8 TB/s), of 4096 x 7168 fp32 59
+// us (5.9 TB/s), of which the sum of the partials takes about 4. Widening bf16 runs at half the rate of the products, so it
 // is done once a value where the registers allow.
 #include "kernels.cuh"
 #include "realign.cuh"

@@ -7,11 +7,11 @@
 //
 // Both passes stream the fp32 logits once. A token's row is spread over L lanes of a warp (L the
 // power of two that gives each lane one VEC-wide load where it can, so 32/L tokens share a warp),
-// and nothing but the row's own E values is kept in registers. Long ones are bound by HBM and by
-// the instructions of a softmax an element (issue slots 75% full), so the exponential is a
-// subtraction, a product and an ex2, and a row's reductions are straight code; short ones by their
-// launches. Loss and gradient: 65536 x 256, top 8: 15.0 us (4.6 TB/s) and 24 us (5.8 TB/s);
-// 8192 x 8, top 2: 5.7 and 2.3 us; 512 x 4, top 2: 3.5 and 2.3 us.
+// and nothing but the row's own E values is kept in registers. Long ones are bound by the latency of
+// a row's loads (one row in flight a warp) and by the instructions of a softmax an element (issue
+// slots 61 and 75% full), so a row's reductions are straight code; short ones by their launches. Loss
+// and gradient with inputs from HBM: 65536 x 256, top 8: 24.0 us (2.9 TB/s; 18.8 us from L2) and
+// 26.6 us (5.3 TB/s); 8192 x 8, top 2: 5.7 and 2.1 us; 512 x 4, top 2: 3.8 and 2.5 us.
 #include "kernels.cuh"
 
 namespace moe {
@@ -20,7 +20,7 @@ namespace {
 constexpr int kThreads = 256;       // gradient
 constexpr int kWarps = kThreads / 32;
 // Blocks an SM holds, and gets: as many as the registers of eight values a lane allow; more would
-// start with the SMs unevenly loaded (65536 x 256: 25.6 us with 5 an SM, 27.4 with 8, 30 with 40).
+// start with the SMs unevenly loaded (65536 x 256: 26.6 us with 5 an SM, 28.3 with 8, 30.7 with 40).
 constexpr int kGradBlocks = 5;
 constexpr int kLossThreads = 1024;  // loss: one block an SM, so that few partials are left
 constexpr int kLossWarps = kLossThreads / 32;
@@ -56,8 +56,8 @@ MOE_DEVICE void load_row(const float* row, int E, int L, int sub, float (&v)[V *
   for (int i = 0; i < V * VEC; ++i) v[i] = fmaxf(v[i], -INFINITY);  // a NaN loses to -inf
 }
 
-// Maximum over a group of L lanes; a whole warp's is one instruction (65536 x 256: loss 15.0 us
-// against 16.9 with shuffles, gradient 24 against 25.6). x is not a NaN.
+// Maximum over a group of L lanes; a whole warp's is one instruction (65536 x 256: loss 24.0 us
+// against 24.4 with shuffles, gradient 26.6 against 28.0). x is not a NaN.
 MOE_DEVICE float group_max(float x, int L) {
   if (L == 32) {
     float y;
@@ -489,8 +489,8 @@ moe_status_t moe_router_loss_fwd(const float* logits, int64_t ld_logits, const i
                 moe_router_loss_workspace(E));
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const RowMap m = row_map(E, E % 4 == 0 && ld_logits % 4 == 0 && a16(logits));
-  // up to four turns of one block: as soon done as two launches (512 x 4: 3.4 us against 5.6 with
-  // two, 2048 x 8: 5.6 against 5.4; eight turns 8.3 against 5.5), and 2 us less on the host
+  // up to four turns of one block: about as soon done as two launches (2048 x 8, four turns: 6.2 us
+  // against 5.4; 4096 x 8, eight: 9.4 against 5.8), and 2 us less on the host
   int nblk = router_blocks(T, m, kLossWarps, std::min(std::max(device_sms(), 1), kMaxBlocks));
   if (nblk <= 4) nblk = 1;
   const Results out = {loss, counts, mean_prob, n_valid, (double)coef * E / k};

@@ -482,6 +482,8 @@ moe_status_t fp8_block_quantize_weight(const void *w, int64_t ldw, int64_t N, in
  * with ld_sa (ld_sb) a multiple of 4; sb 4-byte aligned otherwise. M, N < 2^31 - 256, K < 2^31 -
  * 256. A linear layer y = x w^T is (q_row of x) x (q of w); its input gradient (q_row of dy) x
  * (qt of w); its weight gradient (q_col of dy) x (q_col of x).
+ * The product of two scales is formed in fp32 first: it should be a normal number (the blocks' amaxes
+ * multiply to between 2.4e-33 and 6.8e43), or results lose bits, or overflow with it.
  *   err device int32 or NULL: MOE_DEVERR_TIMEOUT if a bounded wait inside gave up (sticky) */
 moe_status_t fp8_block_gemm(const uint8_t *a, int64_t lda, const float *sa, int64_t ld_sa,
                             const uint8_t *b, int64_t ldb, const float *sb, int64_t ld_sb,
