@@ -24,6 +24,7 @@ PREC = {"bf16": 0, "mxfp8": 1, "nvfp4": 2}
 ACT = {"swiglu": 0, "clamped_swiglu": 1, "geglu": 2, "srelu": 3}
 EXTRA_BIAS, EXTRA_SCALE = 1, 2  # moe_layer_desc_t.extras bits
 DTYPE = {"bf16": 0, "fp32": 1}  # moe_dtype_t
+SCORE = {"softmax": 0, "sigmoid": 1}  # moe_score_t
 DEVERR = {0: "none", 1: "capacity", 2: "timeout", 3: "bad_id"}
 
 KERNEL_NAMES = ("route_topk", "assign_rows", "gather_x", "gemm_fc1_fprop", "gemm_fc2_fprop",
@@ -32,6 +33,8 @@ KERNEL_NAMES = ("route_topk", "assign_rows", "gather_x", "gemm_fc1_fprop", "gemm
                 "extras_reduce", "nvfp4_amax", "nvfp4_quantize", "route_export", "router_loss",
                 "router_grad", "layernorm_fwd", "layernorm_bwd", "layernorm_reduce", "grad_norm",
                 "grad_scale", "fp8_quantize", "fp8_gemm")
+MORE_KERNEL_NAMES = ("count_ids", "router_topk", "router_topk_grad", "residual_norm_fwd",
+                     "residual_norm_bwd", "residual_norm_reduce", "adamw", "adamw_moments")
 # moe_ws_layout_t.nv_amax slots (fp32 [16], first 10 used)
 NV_AMAX = ("x", "xt", "w1", "w2", "a", "at", "dy", "dyt", "dz", "dzt")
 
@@ -45,7 +48,9 @@ EXPORTS = ("moe_timeline_begin", "moe_timeline_end", "moe_workspace_size", "moe_
            "moe_router_loss_workspace", "moe_router_loss_fwd", "moe_router_loss_bwd",
            "moe_layernorm_fwd", "moe_layernorm_workspace", "moe_layernorm_bwd",
            "moe_grad_clip_workspace", "moe_grad_clip", "fp8_block_quantize_rows",
-           "fp8_block_quantize_weight", "fp8_block_gemm")
+           "fp8_block_quantize_weight", "fp8_block_gemm", "moe_permute", "moe_router_topk_fwd",
+           "moe_router_topk_bwd", "moe_residual_norm_fwd", "moe_residual_norm_workspace",
+           "moe_residual_norm_bwd", "moe_adamw_step", "moe_adamw_moments")
 
 
 class LayerDesc(ctypes.Structure):
@@ -72,12 +77,23 @@ class WsLayout(ctypes.Structure):
                 ("nv_base", ctypes.c_size_t)]
 
 
+class AdamWTensor(ctypes.Structure):
+    """moe_adamw_tensor_t"""
+    _fields_ = [("param", ctypes.c_void_p), ("master", ctypes.c_void_p),
+                ("grad", ctypes.c_void_p), ("m", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("m_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+                ("numel", ctypes.c_int64), ("param_dtype", ctypes.c_int32),
+                ("grad_dtype", ctypes.c_int32), ("decay", ctypes.c_float),
+                ("reserved", ctypes.c_int32)]
+
+
 _lib = None
 _P = ctypes.c_void_p
 _I32 = ctypes.c_int32
 _I64 = ctypes.c_int64
 _SZ = ctypes.c_size_t
 _F32 = ctypes.c_float
+_F64 = ctypes.c_double
 _DP = ctypes.POINTER(LayerDesc)
 
 
@@ -133,6 +149,20 @@ def load():
                                              _P]),
         "fp8_block_gemm": (_I32, [_P, _I64, _P, _I64, _P, _I64, _P, _I64, _I32, _P, _I64, _I32,
                                   _I64, _I64, _I64, _P, _P]),
+        "moe_permute": (_I32, [_DP, _I32, _P, _P, _P, _P, _P, _SZ, _P]),
+        "moe_router_topk_fwd": (_I32, [_P, _I64, _I32, _P, _P, _I32, _I32, _I32, _I32, _I32, _I32,
+                                       _I32, _I32, _F32, _P, _P, _P, _P]),
+        "moe_router_topk_bwd": (_I32, [_P, _I64, _I32, _P, _P, _I32, _I32, _I32, _I32, _I32, _F32,
+                                       _P, _I64, _P, _I64, _P]),
+        "moe_residual_norm_fwd": (_I32, [_P, _I64, _P, _I64, _P, _P, _P, _P, _I64, _P, _I64, _P,
+                                         _P, _I64, _I64, _F32, _I32, _F32, _I32, _I32, _I32, _P]),
+        "moe_residual_norm_workspace": (_SZ, [_I64, _I64]),
+        "moe_residual_norm_bwd": (_I32, [_P, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _P, _P, _P,
+                                         _P, _P, _I64, _P, _I64, _P, _P, _P, _I64, _I64, _F32,
+                                         _I32, _I32, _I32, _I32, _P, _SZ, _P]),
+        "moe_adamw_step": (_I32, [_I32, _P, _I32, _F64, _P, _F64, _F64, _F64, _P, _F32,
+                                  ctypes.c_uint64, _P, _P]),
+        "moe_adamw_moments": (_I32, [_I32, _P, _P, _P, _P]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -146,7 +176,8 @@ def load():
 # bind(): the same arguments as above, without ctypes' time.
 _CALLS = ("moe_router_loss_fwd", "moe_router_loss_bwd", "moe_layernorm_fwd", "moe_layernorm_bwd",
           "moe_grad_clip", "fp8_block_quantize_rows", "fp8_block_quantize_weight",
-          "fp8_block_gemm")
+          "fp8_block_gemm", "moe_router_topk_fwd", "moe_router_topk_bwd", "moe_residual_norm_fwd",
+          "moe_residual_norm_bwd", "moe_adamw_step", "moe_adamw_moments")
 _calls = None
 
 
@@ -339,6 +370,31 @@ def moe_route_export(desc, ws, ws_bytes, T, offsets=None, row_of=None, src_of=No
                                    _ptr(offsets), _ptr(row_of), _ptr(src_of), _ptr(row_prob),
                                    _stream(stream)))
 
+
+def moe_permute(desc, T, topk_ids, topk_probs, x, counts, ws, ws_bytes, stream=None):
+    """Permute by given ids and weights (ids outside [0, E): dropped slots)."""
+    _check(load().moe_permute(ctypes.byref(desc), T, _ptr(topk_ids), _ptr(topk_probs), _ptr(x),
+                              _ptr(counts), _ptr(ws), ws_bytes, _stream(stream)))
+
+
+def moe_router_topk_fwd(logits, ld_logits, logits_dtype, bias, token_mask, T, E, k, score, n_group,
+                        topk_group, group_top, renorm, scale, topk_ids, topk_weights, counts,
+                        stream=None):
+    """logits_dtype: a value of DTYPE, score: one of SCORE."""
+    _check(load().moe_router_topk_fwd(_ptr(logits), ld_logits, logits_dtype, _ptr(bias),
+                                      _ptr(token_mask), T, E, k, score, n_group, topk_group,
+                                      group_top, int(renorm), scale, _ptr(topk_ids),
+                                      _ptr(topk_weights), _ptr(counts), _stream(stream)))
+
+
+def moe_router_topk_bwd(logits, ld_logits, logits_dtype, topk_ids, d_weights, T, E, k, score,
+                        renorm, scale, add_to, ld_add, d_logits, ld_d, stream=None):
+    _check(load().moe_router_topk_bwd(_ptr(logits), ld_logits, logits_dtype, _ptr(topk_ids),
+                                      _ptr(d_weights), T, E, k, score, int(renorm), scale,
+                                      _ptr(add_to), ld_add, _ptr(d_logits), ld_d,
+                                      _stream(stream)))
+
+
 def moe_router_loss_workspace(E) -> int:
     n = load().moe_router_loss_workspace(E)
     if n == 0:
@@ -381,6 +437,48 @@ def moe_layernorm_bwd(dy, lddy, x, ldx, gamma, mean, rstd, dx, lddx, dgamma, dbe
     _check(load().moe_layernorm_bwd(_ptr(dy), lddy, _ptr(x), ldx, _ptr(gamma), _ptr(mean),
                                     _ptr(rstd), _ptr(dx), lddx, _ptr(dgamma), _ptr(dbeta), M, N,
                                     x_dtype, w_dtype, _ptr(ws), ws_bytes, _stream(stream)))
+
+
+def moe_residual_norm_fwd(x, ldx, o, ldo, post_weight, gate, weight, x_new, ldxn, h, ldh,
+                          rstd_post, rstd, M, N, scale, post_norm, eps, x_dtype, o_dtype, w_dtype,
+                          stream=None):
+    """x_dtype, o_dtype, w_dtype: values of DTYPE."""
+    _check(load().moe_residual_norm_fwd(_ptr(x), ldx, _ptr(o), ldo, _ptr(post_weight), _ptr(gate),
+                                        _ptr(weight), _ptr(x_new), ldxn, _ptr(h), ldh,
+                                        _ptr(rstd_post), _ptr(rstd), M, N, scale, int(post_norm),
+                                        eps, x_dtype, o_dtype, w_dtype, _stream(stream)))
+
+
+def moe_residual_norm_workspace(M, N) -> int:
+    n = load().moe_residual_norm_workspace(M, N)
+    if n == 0:
+        raise MoeError(1, load().moe_last_error_string().decode())
+    return n
+
+
+def moe_residual_norm_bwd(dh, lddh, dx_new, lddxn, x_new, ldxn, o, ldo, post_weight, gate, weight,
+                          rstd_post, rstd, dx, lddx, d_o, lddo, d_post_weight, d_weight, d_gate, M,
+                          N, scale, post_norm, x_dtype, o_dtype, w_dtype, ws, ws_bytes,
+                          stream=None):
+    _check(load().moe_residual_norm_bwd(_ptr(dh), lddh, _ptr(dx_new), lddxn, _ptr(x_new), ldxn,
+                                        _ptr(o), ldo, _ptr(post_weight), _ptr(gate), _ptr(weight),
+                                        _ptr(rstd_post), _ptr(rstd), _ptr(dx), lddx, _ptr(d_o),
+                                        lddo, _ptr(d_post_weight), _ptr(d_weight), _ptr(d_gate), M,
+                                        N, scale, int(post_norm), x_dtype, o_dtype, w_dtype,
+                                        _ptr(ws), ws_bytes, _stream(stream)))
+
+
+def moe_adamw_step(n, tensors, state_bits, lr, lr_device, beta1, beta2, eps, grad_norm, max_norm,
+                   seed, counters, stream=None):
+    """tensors: a ctypes array of AdamWTensor in host memory (include/moegmm.h)."""
+    _check(load().moe_adamw_step(n, tensors, state_bits, lr, _ptr(lr_device), beta1, beta2, eps,
+                                 _ptr(grad_norm), max_norm, seed, _ptr(counters),
+                                 _stream(stream)))
+
+
+def moe_adamw_moments(n, tensors, m_out, v_out, stream=None):
+    """m_out, v_out: ctypes arrays of addresses in host memory."""
+    _check(load().moe_adamw_moments(n, tensors, m_out, v_out, _stream(stream)))
 
 
 def moe_grad_clip_workspace() -> int:
@@ -463,7 +561,7 @@ class Timeline:
         out = []
         prev = start_event
         for i, kid in enumerate(self.ids):
-            out.append((KERNEL_NAMES[kid], prev.elapsed_time(self.events[i])))
+            out.append(((KERNEL_NAMES + MORE_KERNEL_NAMES)[kid], prev.elapsed_time(self.events[i])))
             prev = self.events[i]
         return out
 
@@ -515,6 +613,20 @@ class MoELayer:
         T = logits.shape[0] if T is None else T
         moe_route_permute(self.desc, T, logits, x, self.topk_ids, self.topk_probs, self.counts,
                           self.ws, self.ws_bytes, stream)
+
+    def permute(self, topk_ids, topk_probs, x, T=None, stream=None):
+        """In the place of route_permute, by a routing that is given (RouterTopK.forward's): experts
+        int32 [T, k], ids outside [0, E) being dropped slots, and weights fp32 [T, k]. Writes
+        self.counts; self.topk_ids and self.topk_probs stay route_permute's."""
+        T = x.shape[0] if T is None else T
+        if T > self.desc.T_max:
+            raise ValueError(f"{T} tokens, but T_max is {self.desc.T_max}")
+        index, k = self.ws.get_device(), self.desc.k
+        _expect(topk_ids, "topk_ids", self.counts.dtype, (T, k), index)
+        _expect(topk_probs, "topk_probs", self.topk_probs.dtype, (T, k), index)
+        _expect(x, "x", self.y.dtype, (T, self.desc.H), index)
+        moe_permute(self.desc, T, topk_ids, topk_probs, x, self.counts, self.ws, self.ws_bytes,
+                    _call_stream(index, stream))
 
     def forward(self, w1_packed, w2, T, stream=None, fc1_bias=None, feat_scale=None):
         """fc1_bias fp32 [E, N1] (logical order) and feat_scale fp32 [E, F] for a layer made
@@ -700,6 +812,86 @@ class RouterLoss:
         return _first(self.d_logits, T)
 
 
+class RouterTopK:
+    """The choice of experts for up to T_max tokens, and the gradient of its weights
+    (moe_router_topk_fwd / _bwd). score "softmax" or "sigmoid"; groups: the topk_group best of n_group
+    groups stay, each counting its best (group_top 1) or its two best experts (2); renorm: the chosen
+    scores are divided by their sum. Owns the results' buffers: they hold the last call's values."""
+
+    def __init__(self, E, k, T_max, score="sigmoid", n_group=1, topk_group=1, group_top=1,
+                 renorm=True, scale=1.0, dtype=None, device="cuda"):
+        import torch
+        dev = self.device = _gpu(device)
+        self._gpu = dev.index
+        if score not in SCORE:
+            raise ValueError(f"score must be one of {tuple(SCORE)}, not {score!r}")
+        self.E, self.k, self.T_max = E, k, T_max
+        self.dtype = torch.float32 if dtype is None else dtype
+        self._code = _dtype_code(self.dtype)
+        self.score, self.renorm, self.scale = score, bool(renorm), float(scale)
+        self._groups = n_group, topk_group, group_top
+        self.topk_ids = torch.empty(T_max, k, dtype=torch.int32, device=dev)
+        self.topk_weights = torch.empty(T_max, k, dtype=torch.float32, device=dev)
+        self.counts = torch.zeros(E, dtype=torch.int32, device=dev)
+        self.d_logits = None
+        self.T = None  # tokens of the last forward
+        self._lib = _load_calls()
+        self._out = (self.topk_ids.data_ptr(), self.topk_weights.data_ptr(),
+                     self.counts.data_ptr())
+
+    def _tokens(self, logits):
+        T = logits.shape[0]
+        if T > self.T_max:
+            raise ValueError(f"{T} tokens, but T_max is {self.T_max}")
+        _expect(logits, "logits", self.dtype, (T, self.E), self._gpu, rows=True)
+        return T
+
+    def forward(self, logits, bias=None, token_mask=None, stream=None):
+        """logits [T, E], bias fp32 [E] (for the choice alone), token_mask bool [T] (False: ids -1,
+        weights 0). Returns (topk_ids int32 [T, k], topk_weights fp32 [T, k], counts int32 [E])."""
+        T = self._tokens(logits)
+        if bias is not None:
+            _expect(bias, "bias", self.topk_weights.dtype, (self.E,), self._gpu)
+        if token_mask is not None:
+            import torch
+            if token_mask.dtype not in (torch.bool, torch.uint8):
+                raise ValueError("token_mask must be bool or uint8")
+            _expect(token_mask, "token_mask", token_mask.dtype, (T,), self._gpu)
+        _check(self._lib.moe_router_topk_fwd(
+            logits.data_ptr(), _ld(logits), self._code, _ptr(bias), _ptr(token_mask), T, self.E,
+            self.k, SCORE[self.score], *self._groups, self.renorm, self.scale, *self._out,
+            _call_stream(self._gpu, stream)))
+        self.T = T
+        return _first(self.topk_ids, T), _first(self.topk_weights, T), self.counts
+
+    def backward(self, logits, d_weights, topk_ids=None, add_to=None, stream=None):
+        """d_weights fp32 [T, k]; topk_ids: the forward's (None: those of the last forward, which had
+        as many tokens or more); add_to fp32 [T, E] is added to the result (RouterLoss.backward's,
+        say). Returns d_logits fp32 [T, E]."""
+        import torch
+        T = self._tokens(logits)
+        _expect(d_weights, "d_weights", torch.float32, (T, self.k), self._gpu)
+        if topk_ids is None:
+            if self.T is None or T > self.T:
+                raise ValueError(f"no forward of {T} tokens has left topk_ids")
+            topk_ids = self.topk_ids
+        else:
+            _expect(topk_ids, "topk_ids", torch.int32, (T, self.k), self._gpu)
+        if add_to is not None:
+            _expect(add_to, "add_to", torch.float32, (T, self.E), self._gpu, rows=True)
+        if self.d_logits is None:
+            # what the current stream has given back may still be in use there
+            with _torch_on(self._gpu, stream):
+                self.d_logits = torch.empty(self.T_max, self.E, dtype=torch.float32,
+                                            device=self.device)
+        _check(self._lib.moe_router_topk_bwd(
+            logits.data_ptr(), _ld(logits), self._code, topk_ids.data_ptr(),
+            d_weights.data_ptr(), T, self.E, self.k, SCORE[self.score], self.renorm, self.scale,
+            _ptr(add_to), 0 if add_to is None else _ld(add_to), self.d_logits.data_ptr(), self.E,
+            _call_stream(self._gpu, stream)))
+        return _first(self.d_logits, T)
+
+
 class LayerNorm:
     """Layer norm over N features of up to M_max rows (moe_layernorm_fwd / _bwd). Owns the
     results' buffers: they hold the last call's values."""
@@ -773,14 +965,144 @@ class LayerNorm:
         return _first(self.dx, M), self.dgamma, self.dbeta
 
 
-def _collide(grads, outs) -> bool:
-    """True where a tensor that is written shares memory with another one. (address, bytes) of each
-    gradient and of its out, which may be the gradient itself."""
-    spans = []
-    for g, o in zip(grads, outs):
-        spans.append((o[0], o[0] + o[1], True))
-        if o != g:
-            spans.append((g[0], g[0] + g[1], False))
+class ResidualNorm:
+    """The residual stream around a block, x_new = x + scale * gate * (post_weight * N(o)) and
+    h = weight * N(x_new) with root-mean-square norms N, over N features of up to M_max rows
+    (moe_residual_norm_fwd / _bwd). dtype: the stream's (x), branch_dtype: o's and h's; post_norm: the
+    branch is normed before it joins. Owns the results' buffers: they hold the last call's values."""
+
+    def __init__(self, N, M_max, dtype=None, branch_dtype=None, weight_dtype=None,
+                 post_norm=False, scale=1.0, eps=1e-6, device="cuda"):
+        import torch
+        dev = self.device = _gpu(device)
+        self._gpu = dev.index
+        self.dtype = torch.bfloat16 if dtype is None else dtype
+        self.branch_dtype = self.dtype if branch_dtype is None else branch_dtype
+        self.weight_dtype = self.branch_dtype if weight_dtype is None else weight_dtype
+        self._codes = tuple(_dtype_code(t) for t in
+                            (self.dtype, self.branch_dtype, self.weight_dtype))
+        self.N, self.M_max = N, M_max
+        self.post_norm, self.scale, self.eps = bool(post_norm), float(scale), float(eps)
+        self.x_new = None
+        self.h = torch.empty(M_max, N, dtype=self.branch_dtype, device=dev)
+        self.rstd = torch.empty(M_max, dtype=torch.float32, device=dev)
+        self.rstd_post = torch.empty(M_max, dtype=torch.float32, device=dev)
+        self.dx = None
+        # rows whose rstd and rstd_post the last forward left
+        self.M = self.M_post = None
+        self._lib = _load_calls()
+
+    def _rows(self, x, name, dtype, M=None):
+        if x.dim() != 2 or x.shape[0] > self.M_max:
+            raise ValueError(f"{name}: expected at most {self.M_max} rows of {self.N}")
+        if M is not None and x.shape[0] != M:
+            raise ValueError(f"{name}: expected {M} rows, got {x.shape[0]}")
+        return _expect(x, name, dtype, (x.shape[0], self.N), self._gpu, rows=True).shape[0]
+
+    def _weight(self, w, name):
+        if w is None:
+            return None
+        return _expect(w, name, self.weight_dtype, (self.N,), self._gpu)
+
+    def _branch(self, o, post_weight, gate, M):
+        """Checks what belongs to a branch; its post norm (0 or 1)."""
+        import torch
+        if o is None:
+            if post_weight is not None or gate is not None:
+                raise ValueError("post_weight and gate need a branch o")
+            return 0
+        self._rows(o, "o", self.branch_dtype, M)
+        self._weight(post_weight, "post_weight")
+        if gate is not None:
+            _expect(gate, "gate", torch.float32, (M,), self._gpu)
+        return int(self.post_norm)
+
+    def forward(self, x, o=None, weight=None, post_weight=None, gate=None, norm=True, stream=None):
+        """x [M, N] of the stream, o [M, N] the branch that joins it (None: x_new is x), gate fp32
+        [M]; norm=False: no h (the last block's sum). Returns (x_new [M, N], h [M, N] or None)."""
+        import torch
+        M = self._rows(x, "x", self.dtype)
+        post = self._branch(o, post_weight, gate, M)
+        self._weight(weight, "weight")
+        if not norm and (weight is not None or o is None):
+            raise ValueError("without a norm there is a branch and no weight")
+        if o is not None and self.x_new is None:
+            # what the current stream has given back may still be in use there
+            with _torch_on(self._gpu, stream):
+                self.x_new = torch.empty(self.M_max, self.N, dtype=self.dtype, device=self.device)
+        new = None if o is None else self.x_new
+        _check(self._lib.moe_residual_norm_fwd(
+            x.data_ptr(), _ld(x), _ptr(o), 0 if o is None else _ld(o), _ptr(post_weight),
+            _ptr(gate), _ptr(weight), _ptr(new), self.N, self.h.data_ptr() if norm else None,
+            self.N, self.rstd_post.data_ptr(), self.rstd.data_ptr(), M, self.N, self.scale, post,
+            self.eps, *self._codes, _call_stream(self._gpu, stream)))
+        self.M, self.M_post = (M if norm else None), (M if post else None)
+        return x if o is None else _first(new, M), _first(self.h, M) if norm else None
+
+    def _stats(self, given, name, own, M, rows):
+        if given is not None:
+            import torch
+            return _expect(given, name, torch.float32, (M,), self._gpu).data_ptr()
+        if rows is None or M > rows:
+            raise ValueError(f"no forward of {M} rows has left {name}")
+        return own.data_ptr()
+
+    def backward(self, dh, x_new=None, o=None, weight=None, post_weight=None, gate=None,
+                 dx_new=None, rstd=None, rstd_post=None, stream=None):
+        """dh [M, N] the gradient of h (None: forward(norm=False)), dx_new that of x_new through
+        everything else (None: 0), x_new and o the forward's; rstd, rstd_post: the forward's (None:
+        those of the last forward, which had as many rows or more). Returns (dx, do, d_weight,
+        d_post_weight, d_gate), None for what had no part."""
+        import torch
+        if dh is None and dx_new is None:
+            raise ValueError("neither dh nor dx_new")
+        M = (self._rows(dx_new, "dx_new", self.dtype) if dh is None
+             else self._rows(dh, "dh", self.branch_dtype))
+        if dx_new is not None:
+            self._rows(dx_new, "dx_new", self.dtype, M)
+        post = self._branch(o, post_weight, gate, M)
+        if dh is None:
+            if weight is not None:
+                raise ValueError("weight needs dh")
+            x_new = r = None
+        else:
+            if x_new is None:
+                raise ValueError("dh needs x_new")
+            self._rows(x_new, "x_new", self.dtype, M)
+            r = self._stats(rstd, "rstd", self.rstd, M, self.M)
+        rp = self._stats(rstd_post, "rstd_post", self.rstd_post, M, self.M_post) if post else None
+        self._weight(weight, "weight")
+        if self.dx is None:
+            self.ws_bytes = moe_residual_norm_workspace(self.M_max, self.N)
+            with _torch_on(self._gpu, stream):
+                def make(dtype, *shape):
+                    return torch.empty(*shape, dtype=dtype, device=self.device)
+                self.dx = make(self.dtype, self.M_max, self.N)
+                self.do = make(self.branch_dtype, self.M_max, self.N)
+                self.d_weight = make(self.weight_dtype, self.N)
+                self.d_post_weight = make(self.weight_dtype, self.N)
+                self.d_gate = make(torch.float32, self.M_max)
+                self.ws = make(torch.uint8, self.ws_bytes)
+        do = None if o is None else self.do
+        dw = None if weight is None else self.d_weight
+        dwp = None if post_weight is None else self.d_post_weight
+        dg = None if gate is None else self.d_gate
+
+        def rows(t):
+            return (None, 0) if t is None else (t.data_ptr(), _ld(t))
+
+        _check(self._lib.moe_residual_norm_bwd(
+            *rows(dh), *rows(dx_new), *rows(x_new), *rows(o), _ptr(post_weight), _ptr(gate),
+            _ptr(weight), rp, r, self.dx.data_ptr(), self.N, _ptr(do), self.N, _ptr(dwp),
+            _ptr(dw), _ptr(dg), M, self.N, self.scale, post, *self._codes, self.ws.data_ptr(),
+            self.ws_bytes, _call_stream(self._gpu, stream)))
+        return (_first(self.dx, M), None if do is None else _first(do, M), dw, dwp,
+                None if dg is None else _first(dg, M))
+
+
+def _overlap(spans) -> bool:
+    """True where a tensor that is written shares memory with another one. (first byte, end, written)
+    of each tensor."""
     end = end_written = 0
     for lo, hi, written in sorted(s for s in spans if s[1] > s[0]):
         if lo < (end if written else end_written):
@@ -789,6 +1111,13 @@ def _collide(grads, outs) -> bool:
         if written:
             end_written = max(end_written, hi)
     return False
+
+
+def _collide(grads, outs) -> bool:
+    """True where a tensor that is written shares memory with another one. (address, bytes) of each
+    gradient and of its out, which may be the gradient itself."""
+    return _overlap([(o[0], o[0] + o[1], True) for o in outs]
+                    + [(g[0], g[0] + g[1], False) for g, o in zip(grads, outs) if o != g])
 
 
 class GradClip:
@@ -834,6 +1163,113 @@ class GradClip:
                                        at[2], at[3], max_norm, *self._work,
                                        _call_stream(self._gpu, stream)))
         return self.norm
+
+
+class AdamW:
+    """AdamW over a fixed list of weights and their gradients (moe_adamw_step). Holds references to
+    the tensors: their memory stays where it is. Weights are fp32, or bf16 with an fp32 master
+    (masters: one for each weight, None for fp32 ones; None: made here from the weights). State m and
+    v in 32 bits, or 8: codes of m and of sqrt(v) with a scale byte for each 256 (m_exp, v_exp; see
+    moments()), rounded at random from `seed`. weight_decay: a number, or one for each weight. lr: a
+    number, or an fp32 tensor [1] on the GPU, which is read at each step (a captured one follows it).
+    steps (int64 [1] on the GPU): the steps done. To resume, copy a checkpoint's masters, m, v, m_exp,
+    v_exp and steps into those tensors."""
+
+    def __init__(self, params, grads, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01,
+                 state_bits=32, masters=None, seed=0):
+        import torch
+        self.params, self.grads = list(params), list(grads)
+        n = self.n = len(self.params)
+        decay = ([weight_decay] * n if isinstance(weight_decay, (int, float))
+                 else list(weight_decay))
+        masters = [None] * n if masters is None else list(masters)
+        if len(self.grads) != n or len(decay) != n or len(masters) != n:
+            raise ValueError("params, grads, masters and weight_decay differ in length")
+        if state_bits not in (8, 32):
+            raise ValueError(f"state_bits must be 8 or 32, not {state_bits}")
+        dev = self.device = self.params[0].device if n else _gpu("cuda")
+        for p, g, w in zip(self.params, self.grads, masters):
+            for t in (p, g) if w is None else (p, g, w):
+                if not t.is_cuda or not t.is_contiguous() or t.device != dev:
+                    raise ValueError("tensors must be contiguous, on one GPU")
+                if t.shape != p.shape:
+                    raise ValueError("a gradient or master differs from its weight in shape")
+            _dtype_code(p.dtype)
+            _dtype_code(g.dtype)
+            if w is not None and (w.dtype != torch.float32 or p.dtype == torch.float32):
+                raise ValueError("a master is fp32, of a bf16 weight")
+        self._gpu = dev.index
+        self.state_bits, self.betas, self.eps, self.seed = state_bits, betas, eps, seed
+        self.lr = lr
+        self.masters = [p.detach().float() if w is None and p.dtype != torch.float32 else w
+                        for p, w in zip(self.params, masters)]
+
+        def states(dtype, per=1):
+            return [torch.zeros(-(-p.numel() // per), dtype=dtype, device=dev)
+                    for p in self.params]
+
+        if state_bits == 32:
+            self.m, self.v = states(torch.float32), states(torch.float32)
+            self.m_exp = self.v_exp = [None] * n
+        else:
+            self.m, self.v = states(torch.uint8), states(torch.uint8)
+            self.m_exp, self.v_exp = states(torch.uint8, 256), states(torch.uint8, 256)
+        self._counters = torch.zeros(2, dtype=torch.int64, device=dev)
+        self.steps = self._counters[:1]
+        self._list = (AdamWTensor * n)(*[
+            AdamWTensor(p.data_ptr(), _ptr(w), g.data_ptr(), m.data_ptr(), v.data_ptr(), _ptr(me),
+                        _ptr(ve), p.numel(), _dtype_code(p.dtype), _dtype_code(g.dtype), d, 0)
+            for p, w, g, m, v, me, ve, d in zip(self.params, self.masters, self.grads, self.m,
+                                                self.v, self.m_exp, self.v_exp, decay)])
+        self._at = ctypes.addressof(self._list)
+
+        written = [*self.params, *self.masters, *self.m, *self.v, *self.m_exp, *self.v_exp]
+        if _overlap([(t.data_ptr(), t.data_ptr() + t.numel() * t.element_size(), w)
+                     for ts, w in ((written, True), (self.grads, False)) for t in ts
+                     if t is not None]):
+            raise ValueError("a weight shares memory with another tensor")
+        self._moments = None
+        self._lib = _load_calls()
+
+    def step(self, norm=None, max_norm=math.inf, lr=None, stream=None):
+        """One step. norm: GradClip's (fp32 [1] on the GPU): the gradients are multiplied by
+        min(1, max_norm / (norm + 1e-6)), and a norm that is not finite skips the step. lr: another
+        learning rate than the optimiser's, for this step."""
+        import torch
+        lr = self.lr if lr is None else lr
+        lr_dev = None
+        if isinstance(lr, torch.Tensor):
+            lr_dev, lr = _expect(lr, "lr", torch.float32, lr.shape, self._gpu), 0.0
+            if lr_dev.numel() != 1:
+                raise ValueError("lr must hold one value")
+        if norm is not None:
+            _expect(norm, "norm", torch.float32, norm.shape, self._gpu)
+            if norm.numel() != 1:
+                raise ValueError("norm must hold one value")
+        elif max_norm != math.inf:
+            raise ValueError("max_norm needs the gradients' norm")
+        _check(self._lib.moe_adamw_step(
+            self.n, self._at, self.state_bits, lr, _ptr(lr_dev), *self.betas, self.eps,
+            _ptr(norm), max_norm, self.seed, self._counters.data_ptr(),
+            _call_stream(self._gpu, stream)))
+
+    def moments(self, stream=None):
+        """The values that 8-bit states stand for: lists of m and of sqrt(v), bf16, in buffers that
+        hold the last call's values."""
+        import torch
+        if self.state_bits != 8:
+            raise ValueError("states in 32 bits are m and v themselves")
+        if self._moments is None:
+            with _torch_on(self._gpu, stream):
+                self._moments = tuple([torch.empty(p.numel(), dtype=torch.bfloat16,
+                                                   device=self.device) for p in self.params]
+                                      for _ in range(2))
+            self._moments_at = tuple((_P * self.n)(*[t.data_ptr() for t in ts])
+                                     for ts in self._moments)
+        _check(self._lib.moe_adamw_moments(
+            self.n, self._at, *[ctypes.addressof(a) for a in self._moments_at],
+            _call_stream(self._gpu, stream)))
+        return self._moments
 
 
 def _up(n, m) -> int:

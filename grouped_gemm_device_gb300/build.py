@@ -17,7 +17,7 @@ LIB = os.path.join(OUT_DIR, "libmoegmm.so")
 CALLS = os.path.join(OUT_DIR, "_moecalls.so")  # Python's way into the operators
 SOURCES = ["api.cu", "route.cu", "mxfp8.cu", "gemm.cu", "gemm_mx.cu", "gemm_rc.cu", "noalloc.cu",
            "nvfp4.cu", "gemm_fp4.cu", "router_loss.cu", "layernorm.cu", "grad_clip.cu",
-           "fp8_quant.cu", "gemm_fp8.cu"]
+           "fp8_quant.cu", "gemm_fp8.cu", "router_topk.cu", "residual_norm.cu", "adamw.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -495,6 +495,52 @@ moe_status_t moe_workspace_layout(const moe_layer_desc_t* desc, moe_ws_layout_t*
   return MOE_OK;
 }
 
+// The rows of a routing whose counts the stream's earlier work has left: their order, x gathered into
+// it, and the layer's quantised copies. `given`: ids that the caller chose (moe_permute).
+static moe_status_t permute_rows(const moe_layer_desc_t* d, int32_t T, const int32_t* topk_ids,
+                                 const float* topk_probs, const int32_t* counts, const void* x,
+                                 const Ws& w, bool given, cudaStream_t s) {
+  int32_t* offsets = w.at<int32_t>(w.L.offsets);
+  int32_t* row_of = w.at<int32_t>(w.L.row_of);
+  int32_t* src_of = w.at<int32_t>(w.L.src_of);
+  float* row_prob = w.at<float>(w.L.row_prob);
+  int* err = w.at<int>(w.L.err);
+  cudaError_t e;
+  launch_kernel(given ? assign_given_rows_kernel : assign_rows_kernel, d->E, 1024, 0, s, nullptr, 0,
+                topk_ids, topk_probs, counts, T, d->E, d->k, d->align, w.L.R_cap, offsets, row_of,
+                src_of, row_prob, err);
+  count_launch(s, MOE_K_ASSIGN_ROWS);
+  if (d->precision == MOE_PREC_NVFP4) {
+    // gather fused with X's amax and rotated amax, then its copies: along H for FC1 and
+    // transposed, rotated along the expert's rows, for the FC1 weight gradient
+    const Fp4Problem p = fp4_problem(d, w);
+    e = cudaMemsetAsync(p.amax + AM_X, 0, 2 * sizeof(float), s);
+    if (e != cudaSuccess) return cuda_fail(e, "memset amax");
+    launch_gather_rows_amax(x, src_of, offsets, d->E, d->k, d->H, w.L.R_cap, p.rht_mask,
+                            w.at<void>(w.L.x_perm), p.amax + AM_X, p.amax + AM_XT, device_sms(),
+                            MOE_K_GATHER_X, s);
+    if (!nv_quantize(w.at<void>(w.L.x_perm), w.L.R_cap, d->H, w.L.R_cap, w.L.R_cap, nullptr, p,
+                     AM_X, AM_XT, p.x, p.xt, 1, s))
+      return fail(MOE_ERR_CUDA, "NVFP4 quantiser: tensor map or shared-memory limit");
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return cuda_fail(e, given ? "permute launch" : "route_permute launch");
+    return MOE_OK;
+  }
+  launch_kernel(gather_rows_kernel, grid_for(w.L.R_cap, 8), 256, 0, s, nullptr, 0, 
+      static_cast<const uint4*>(x), src_of, offsets, d->E, d->k, d->H / 8, w.L.R_cap,
+      w.at<uint4>(w.L.x_perm));
+  count_launch(s, MOE_K_GATHER_X);
+  if (d->precision == MOE_PREC_MXFP8) {
+    // X along H for FC1 and column-wise (along the expert's rows) for the FC1 weight gradient
+    const MxProblem m = mx_problem(d, w);
+    mx_quantize_operands(w.at<void>(w.L.x_perm), w.L.R_cap, d->H, w.L.R_cap, w.L.R_cap, m.x,
+                         m.xt, s);
+  }
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return cuda_fail(e, given ? "permute launch" : "route_permute launch");
+  return MOE_OK;
+}
+
 moe_status_t moe_route_permute(const moe_layer_desc_t* d, int32_t T, const float* logits,
                                const void* x, int32_t* topk_ids, float* topk_probs,
                                int32_t* counts, void* ws, size_t ws_bytes, moe_stream_t stream) {
@@ -510,48 +556,39 @@ moe_status_t moe_route_permute(const moe_layer_desc_t* d, int32_t T, const float
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e = cudaMemsetAsync(counts, 0, sizeof(int32_t) * d->E, s);
   if (e != cudaSuccess) return cuda_fail(e, "memset counts");
-  int32_t* offsets = w.at<int32_t>(w.L.offsets);
-  int32_t* row_of = w.at<int32_t>(w.L.row_of);
-  int32_t* src_of = w.at<int32_t>(w.L.src_of);
-  float* row_prob = w.at<float>(w.L.row_prob);
-  int* err = w.at<int>(w.L.err);
   if (T > 0) {
     launch_kernel(route_topk_kernel, grid_for((T + 7) / 8, 8), 256, 0, s, nullptr, 0, logits, T, d->E, d->k, topk_ids,
                                                                  topk_probs, counts);
     count_launch(s, MOE_K_ROUTE_TOPK);
   }
-  launch_kernel(assign_rows_kernel, d->E, 1024, 0, s, nullptr, 0, topk_ids, topk_probs, counts, T, d->E, d->k, d->align,
-                                           w.L.R_cap, offsets, row_of, src_of, row_prob, err);
-  count_launch(s, MOE_K_ASSIGN_ROWS);
-  if (d->precision == MOE_PREC_NVFP4) {
-    // gather fused with X's amax and rotated amax, then its copies: along H for FC1 and
-    // transposed, rotated along the expert's rows, for the FC1 weight gradient
-    const Fp4Problem p = fp4_problem(d, w);
-    e = cudaMemsetAsync(p.amax + AM_X, 0, 2 * sizeof(float), s);
-    if (e != cudaSuccess) return cuda_fail(e, "memset amax");
-    launch_gather_rows_amax(x, src_of, offsets, d->E, d->k, d->H, w.L.R_cap, p.rht_mask,
-                            w.at<void>(w.L.x_perm), p.amax + AM_X, p.amax + AM_XT, device_sms(),
-                            MOE_K_GATHER_X, s);
-    if (!nv_quantize(w.at<void>(w.L.x_perm), w.L.R_cap, d->H, w.L.R_cap, w.L.R_cap, nullptr, p,
-                     AM_X, AM_XT, p.x, p.xt, 1, s))
-      return fail(MOE_ERR_CUDA, "NVFP4 quantiser: tensor map or shared-memory limit");
-    e = cudaGetLastError();
-    if (e != cudaSuccess) return cuda_fail(e, "route_permute launch");
-    return MOE_OK;
+  return permute_rows(d, T, topk_ids, topk_probs, counts, x, w, false, s);
+}
+
+moe_status_t moe_permute(const moe_layer_desc_t* d, int32_t T, const int32_t* topk_ids,
+                         const float* topk_probs, const void* x, int32_t* counts, void* ws,
+                         size_t ws_bytes, moe_stream_t stream) {
+  PdlScope pdl_scope(d);
+  moe_status_t st = validate_desc(d);
+  if (st != MOE_OK) return st;
+  if (T < 0 || T > d->T_max) return fail(MOE_ERR_INVALID_ARG, "T=%d outside [0, T_max]", T);
+  if ((T > 0 && (!x || !topk_ids || !topk_probs)) || !counts)
+    return fail(MOE_ERR_INVALID_ARG, "NULL tensor pointer");
+  if (!aligned16(x)) return fail(MOE_ERR_INVALID_ARG, "x must be 16-byte aligned");
+  if ((reinterpret_cast<uintptr_t>(topk_ids) | reinterpret_cast<uintptr_t>(topk_probs) |
+       reinterpret_cast<uintptr_t>(counts)) & 3)
+    return fail(MOE_ERR_INVALID_ARG, "topk_ids, topk_probs and counts must be 4-byte aligned");
+  Ws w;
+  if ((st = check_ws(d, ws, ws_bytes, w)) != MOE_OK) return st;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const cudaError_t e = cudaMemsetAsync(counts, 0, sizeof(int32_t) * d->E, s);
+  if (e != cudaSuccess) return cuda_fail(e, "memset counts");
+  if (T > 0) {
+    const int64_t n = (int64_t)T * d->k;
+    launch_kernel(count_ids_kernel, grid_for((n + 255) / 256, 2), 256, 0, s, nullptr, 0, topk_ids,
+                  n, d->E, counts);
+    count_launch(s, MOE_K_COUNT_IDS);
   }
-  launch_kernel(gather_rows_kernel, grid_for(w.L.R_cap, 8), 256, 0, s, nullptr, 0, 
-      static_cast<const uint4*>(x), src_of, offsets, d->E, d->k, d->H / 8, w.L.R_cap,
-      w.at<uint4>(w.L.x_perm));
-  count_launch(s, MOE_K_GATHER_X);
-  if (d->precision == MOE_PREC_MXFP8) {
-    // X along H for FC1 and column-wise (along the expert's rows) for the FC1 weight gradient
-    const MxProblem m = mx_problem(d, w);
-    mx_quantize_operands(w.at<void>(w.L.x_perm), w.L.R_cap, d->H, w.L.R_cap, w.L.R_cap, m.x,
-                         m.xt, s);
-  }
-  e = cudaGetLastError();
-  if (e != cudaSuccess) return cuda_fail(e, "route_permute launch");
-  return MOE_OK;
+  return permute_rows(d, T, topk_ids, topk_probs, counts, x, w, true, s);
 }
 
 static moe_status_t fwd_impl(const moe_layer_desc_t* d, int32_t T, const void* w1_packed,

@@ -79,6 +79,11 @@ __global__ void assign_rows_kernel(const int32_t* ids, const float* probs, const
                                    int T, int E, int k, int align, int64_t R_cap,
                                    int32_t* offsets, int32_t* row_of, int32_t* src_of,
                                    float* row_prob, int* err);
+__global__ void assign_given_rows_kernel(const int32_t* ids, const float* probs,
+                                         const int32_t* counts, int T, int E, int k, int align,
+                                         int64_t R_cap, int32_t* offsets, int32_t* row_of,
+                                         int32_t* src_of, float* row_prob, int* err);
+__global__ void count_ids_kernel(const int32_t* ids, int64_t n, int E, int32_t* counts);
 __global__ void gather_rows_kernel(const uint4* x, const int32_t* src_of, const int32_t* offsets,
                                    int E, int k, int H8, int64_t R_cap, uint4* out);
 __global__ void route_export_kernel(const int32_t* off_ws, int n_off, const int32_t* row_of_ws,

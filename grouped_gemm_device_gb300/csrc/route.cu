@@ -96,13 +96,14 @@ __global__ void __launch_bounds__(256) route_topk_kernel(const float* __restrict
 // One block per expert e. Every block recomputes the padded exclusive scan of the counts
 // (E <= 256) so no extra launch or grid sync is needed; block 0 publishes offsets[]. The
 // block then walks all (token, slot) pairs in token order and gives the pairs routed to e
-// consecutive rows (token ascending) by a block-wide prefix sum.
-__global__ void __launch_bounds__(1024) assign_rows_kernel(
-    const int32_t* __restrict__ ids, const float* __restrict__ probs,
-    const int32_t* __restrict__ counts, int T, int E, int k, int align, int64_t R_cap,
-    int32_t* __restrict__ offsets, int32_t* __restrict__ row_of, int32_t* __restrict__ src_of,
-    float* __restrict__ row_prob, int* err) {
-  MOE_GRIDDEP_ENTRY();
+// consecutive rows (token ascending) by a block-wide prefix sum. GIVEN: ids that the caller chose,
+// among them ids outside [0, E) (dropped slots, row -1) and experts that a token names twice.
+template <bool GIVEN>
+MOE_DEVICE void assign_rows(const int32_t* __restrict__ ids, const float* __restrict__ probs,
+                            const int32_t* __restrict__ counts, int T, int E, int k, int align,
+                            int64_t R_cap, int32_t* __restrict__ offsets,
+                            int32_t* __restrict__ row_of, int32_t* __restrict__ src_of,
+                            float* __restrict__ row_prob, int* err) {
   __shared__ int s_off[257];
   __shared__ int s_warp[32];
   __shared__ int s_base;
@@ -136,9 +137,15 @@ __global__ void __launch_bounds__(1024) assign_rows_kernel(
       int t = t0 + threadIdx.x * TPT + i;
       my_slot[i] = -1;
       if (t < T) {
-        for (int j = 0; j < k; ++j)
-          if (ids[(size_t)t * k + j] == e) my_slot[i] = j;
-        my_cnt += my_slot[i] >= 0;
+        for (int j = 0; j < k; ++j) {
+          const int id = ids[(size_t)t * k + j];
+          if (id == e) my_slot[i] = j;
+          if (GIVEN) {
+            my_cnt += id == e;
+            if (e == 0 && (id < 0 || id >= E)) row_of[(size_t)t * k + j] = -1;
+          }
+        }
+        if (!GIVEN) my_cnt += my_slot[i] >= 0;
       }
     }
     // block exclusive scan of my_cnt
@@ -166,12 +173,15 @@ __global__ void __launch_bounds__(1024) assign_rows_kernel(
     for (int i = 0; i < TPT; ++i) {
       if (my_slot[i] >= 0) {
         int t = t0 + threadIdx.x * TPT + i;
-        int src = t * k + my_slot[i];
-        int row = off_e + rank;
-        row_of[src] = row;
-        src_of[row] = src;
-        row_prob[row] = probs[src];
-        ++rank;
+        for (int j = GIVEN ? 0 : my_slot[i]; j <= my_slot[i]; ++j) {
+          int src = t * k + j;
+          if (GIVEN && ids[src] != e) continue;
+          int row = off_e + rank;
+          row_of[src] = row;
+          src_of[row] = src;
+          row_prob[row] = probs[src];
+          ++rank;
+        }
       }
     }
     __syncthreads();
@@ -185,6 +195,41 @@ __global__ void __launch_bounds__(1024) assign_rows_kernel(
     src_of[r] = -1;
     row_prob[r] = 0.f;
   }
+}
+
+__global__ void __launch_bounds__(1024) assign_rows_kernel(
+    const int32_t* __restrict__ ids, const float* __restrict__ probs,
+    const int32_t* __restrict__ counts, int T, int E, int k, int align, int64_t R_cap,
+    int32_t* __restrict__ offsets, int32_t* __restrict__ row_of, int32_t* __restrict__ src_of,
+    float* __restrict__ row_prob, int* err) {
+  MOE_GRIDDEP_ENTRY();
+  assign_rows<false>(ids, probs, counts, T, E, k, align, R_cap, offsets, row_of, src_of, row_prob,
+                     err);
+}
+__global__ void __launch_bounds__(1024) assign_given_rows_kernel(
+    const int32_t* __restrict__ ids, const float* __restrict__ probs,
+    const int32_t* __restrict__ counts, int T, int E, int k, int align, int64_t R_cap,
+    int32_t* __restrict__ offsets, int32_t* __restrict__ row_of, int32_t* __restrict__ src_of,
+    float* __restrict__ row_prob, int* err) {
+  MOE_GRIDDEP_ENTRY();
+  assign_rows<true>(ids, probs, counts, T, E, k, align, R_cap, offsets, row_of, src_of, row_prob,
+                    err);
+}
+
+// counts[e] += slots that name expert e (ids outside [0, E) count nowhere).
+__global__ void __launch_bounds__(256) count_ids_kernel(const int32_t* __restrict__ ids, int64_t n,
+                                                        int E, int32_t* __restrict__ counts) {
+  MOE_GRIDDEP_ENTRY();
+  __shared__ int hist[256];
+  hist[threadIdx.x] = 0;
+  __syncthreads();
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
+    const int e = ids[i];
+    if (e >= 0 && e < E) atomicAdd(&hist[e], 1);
+  }
+  __syncthreads();
+  const int c = hist[threadIdx.x];
+  if (c) atomicAdd(&counts[threadIdx.x], c);
 }
 
 // Copies of the routing maps into caller buffers (any destination may be null).
@@ -224,7 +269,8 @@ __global__ void __launch_bounds__(256) gather_rows_kernel(const uint4* __restric
   }
 }
 
-// out[t, :] = sum_{j<k} in[row_of[t*k+j], :], fp32 accumulation in slot order, bf16 result.
+// out[t, :] = sum_{j<k} in[row_of[t*k+j], :], fp32 accumulation in slot order, bf16 result. A
+// dropped slot has row -1.
 __global__ void __launch_bounds__(256) combine_rows_kernel(const uint4* __restrict__ in,
                                                            const int32_t* __restrict__ row_of,
                                                            int T, int k, int H8,
@@ -238,6 +284,7 @@ __global__ void __launch_bounds__(256) combine_rows_kernel(const uint4* __restri
 #pragma unroll
       for (int q = 0; q < 8; ++q) acc[q] = 0.f;
       for (int j = 0; j < k; ++j) {
+        if (rows[j] < 0) continue;
         uint4 v = in[(int64_t)rows[j] * H8 + i];
         acc[0] += bf16_lo(v.x); acc[1] += bf16_hi(v.x);
         acc[2] += bf16_lo(v.y); acc[3] += bf16_hi(v.y);
@@ -254,15 +301,17 @@ __global__ void __launch_bounds__(256) combine_rows_kernel(const uint4* __restri
   }
 }
 
-// d_probs[t*k+j] = sum_i part[row_of[t*k+j], i] (column tiles in order).
+// d_probs[t*k+j] = sum_i part[row_of[t*k+j], i] (column tiles in order), 0 for a dropped slot.
 __global__ void dprob_reduce_kernel(const float* __restrict__ part, int nparts,
                                     const int32_t* __restrict__ row_of, int n,
                                     float* __restrict__ d_probs) {
   MOE_GRIDDEP_ENTRY();
   for (int i = blockIdx.x * blockDim.x + threadIdx.x; i < n; i += gridDim.x * blockDim.x) {
-    const float* p = part + (int64_t)row_of[i] * nparts;
+    const int row = row_of[i];
+    const float* p = part + (int64_t)row * nparts;
     float s = 0.f;
-    for (int q = 0; q < nparts; ++q) s += p[q];
+    if (row >= 0)
+      for (int q = 0; q < nparts; ++q) s += p[q];
     d_probs[i] = s;
   }
 }

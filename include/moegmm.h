@@ -2,8 +2,9 @@
  * moegmm.h - C ABI of the GB300 (sm_103a) fused grouped expert MLP of a Mixture-of-Experts
  * layer: routing + permutation, fused FC1 -> GLU -> probability scale -> FC2 forward, the
  * matching backward (BF16, MXFP8 or NVFP4 GEMM operands), the standalone MXFP8 and NVFP4
- * quantisers, and the operators around the layer in a training or serving step: the router's
- * balance loss, layer norm, gradient clipping, and a dense FP8 product with block-128 scales.
+ * quantisers, and the operators around the layer in a training or serving step: the choice of
+ * experts and the router's balance loss, layer norm, the norms around a block fused with its
+ * residual sum, gradient clipping, AdamW, and a dense FP8 product with block-128 scales.
  *
  * Sources (by page title and section):
  *   [NV-blog] NVIDIA technical blog "Boosting MoE Training Throughput with Advanced Fusion
@@ -180,10 +181,22 @@ moe_status_t moe_route_permute(const moe_layer_desc_t *desc, int32_t T, const fl
                                const void *x, int32_t *topk_ids, float *topk_probs,
                                int32_t *counts, void *ws, size_t ws_bytes, moe_stream_t stream);
 
+/* Permute by a routing that is given (as moe_router_topk_fwd leaves it) in the place of the top-k
+ * that moe_route_permute takes itself; everything else is as there, and the same calls follow it.
+ *   topk_ids   int32 [T, k]  experts; an id outside [0, E) is a dropped slot: it gets no row (-1 in
+ *              row_of), adds nothing to y and has d_probs 0. A token may name an expert twice:
+ *              each slot gets a row of its own
+ *   topk_probs fp32 [T, k]   weights of the experts' outputs
+ *   counts     int32 [E]     out: rows of each expert
+ * Rows are in the order expert, token, slot. T in [0, T_max]. */
+moe_status_t moe_permute(const moe_layer_desc_t *desc, int32_t T, const int32_t *topk_ids,
+                         const float *topk_probs, const void *x, int32_t *counts, void *ws,
+                         size_t ws_bytes, moe_stream_t stream);
+
 /* The routing maps of the last moe_route_permute on ws, copied into caller buffers (device
  * memory; [NV-blog] host-sync section: the per-expert counts and offsets stay on the device):
  *   offsets  int32 [E+1]    padded segment starts; offsets[E] = rows in use
- *   row_of   int32 [T*k]    permuted row of (token t, slot j) at t*k+j
+ *   row_of   int32 [T*k]    permuted row of (token t, slot j) at t*k+j (-1: dropped by moe_permute)
  *   src_of   int32 [R_cap]  t*k+j of a permuted row, -1 for a padding row
  *   row_prob fp32  [R_cap]  routing probability of a permuted row, 0 for a padding row
  * R_cap as in moe_workspace_layout; rows at or beyond offsets[E] carry no routing (their
@@ -204,7 +217,7 @@ moe_status_t moe_route_export(const moe_layer_desc_t *desc, const void *ws, size
  *                              order of moe_pack_fc1_weight (gate/linear blocks interleaved)
  *   w2        bf16 [E, F, H]   FC2 weight (logical [F, H] per expert)
  *   y         bf16 [T, H]      out
- * Requires a preceding moe_route_permute on the same ws. Saves z and a_s in ws for the
+ * Requires a preceding moe_route_permute or moe_permute on the same ws. Saves z and a_s in ws for the
  * backward. MXFP8 layers also quantise both weights (both directions) into ws first. NVFP4
  * layers take the weights' amax and NVFP4 copies (both directions) first; their FC1 kernel
  * also writes the amax and the rotated amax of a_s into ws (nv_amax), from which a_s's NVFP4
@@ -362,13 +375,60 @@ moe_status_t moe_pack_fc1_weight(const void *w1_src, void *w1_dst, int32_t E, in
                                  moe_stream_t stream);
 
 /* ------------------------------------------------------------------------------------------
- * Operators around the expert layer: the router's balance loss, layer norm, gradient clipping
- * and a dense product in 8-bit floating point with a scale for each block of 128. They take no
+ * Operators around the expert layer: the choice of experts and the router's balance loss, layer
+ * norm and residual norm, gradient clipping, AdamW, and a dense product in 8-bit floating point
+ * with a scale for each block of 128. They take no
  * layer description; the conventions at the top of this file hold (caller-owned device memory,
  * no synchronisation, graph-capturable, checks before any launch). Results do not depend on the
  * timing of the launch: sums are taken in a fixed order.
  * ------------------------------------------------------------------------------------------ */
 typedef enum { MOE_DT_BF16 = 0, MOE_DT_FP32 = 1 } moe_dtype_t;
+
+/* Choice of experts. With l the E logits of a token (NaN is read as -inf):
+ *   score s_e   MOE_SCORE_SIGMOID: 1 / (1 + exp(-l_e)).  MOE_SCORE_SOFTMAX: exp(l_e - max l), 1
+ *               where l_e is the maximum, times the reciprocal of their sum; the sum takes
+ *               neighbours in pairs, then pairs of pairs, zeros filling up to a power of two
+ *   value v_e   s_e + bias[e] (NaN is read as -inf), or s_e without a bias
+ *   choice c_e  v_e, or without a bias l_e itself, which has the scores' order
+ *   groups      the experts in n_group groups of E / n_group neighbours; a group counts the largest
+ *               c of its experts (group_top 1) or the sum of its two largest v (group_top 2); the
+ *               topk_group largest groups stay (ties to the lower one)
+ *   topk_ids    the k experts of those groups by descending c (ties to the lower index)
+ *   weights     scale * s_j;  with renorm, sigmoid: scale * s_j / (sum of the chosen s + 1e-20),
+ *               softmax: scale * softmax over the chosen logits (those equal to their maximum
+ *               weigh 1 before normalisation)
+ * Each step up to the choice is one rounded fp32 operation (exp: CUDA's expf), so that the choice
+ * between near values does not depend on the launch. A token whose mask is 0 gets ids -1 (dropped
+ * slots to every function here) and weights 0, and is not counted.
+ *   logits       [T, E] of logits_dtype (moe_dtype_t), row stride ld_logits >= E
+ *   bias         fp32 [E] or NULL: it takes part in the choice alone
+ *   token_mask   uint8 [T] or NULL: all tokens
+ *   topk_ids     int32 [T, k] out;  topk_weights fp32 [T, k] out
+ *   counts       int32 [E] out, or NULL: (token, slot) pairs of each expert
+ * E in [1, 256], k in [1, min(E, 8)], n_group a divisor of E, topk_group in [1, n_group] with
+ * topk_group * E / n_group >= k, group_top 1 or 2 (2: at least two experts a group); T >= 0. */
+typedef enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score_t;
+moe_status_t moe_router_topk_fwd(const void *logits, int64_t ld_logits, int32_t logits_dtype,
+                                 const float *bias, const uint8_t *token_mask, int32_t T,
+                                 int32_t E, int32_t k, int32_t score, int32_t n_group,
+                                 int32_t topk_group, int32_t group_top, int32_t renorm,
+                                 float scale, int32_t *topk_ids, float *topk_weights,
+                                 int32_t *counts, moe_stream_t stream);
+/* Gradient of the logits through the weights (the choice is constant), u_j = scale * d_weights_j:
+ *   sigmoid:          ds_j = u_j, d_e = ds_j s_j (1 - s_j) at the chosen experts;
+ *   sigmoid, renorm:  ds_j = (u_j - sum_i u_i s_i / S) / S,  S = sum of the chosen s + 1e-20
+ *   softmax:          d_e = p_e (u_e - sum_j u_j p_j), u_e = 0 for experts that are not chosen
+ *   softmax, renorm:  d_e = w_j (u_j - sum_i w_i u_i) at the chosen experts, w their softmax
+ * Dropped slots (ids outside [0, E)) take no part; slots that name the same expert add up.
+ *   topk_ids    int32 [T, k], d_weights fp32 [T, k] (moe_grouped_mlp_bwd's d_probs)
+ *   add_to      fp32 [T, E], row stride ld_add >= E, or NULL: added to the result (the balance
+ *               loss's gradient from moe_router_loss_bwd, say); may be d_logits
+ *   d_logits    fp32 [T, E] out, row stride ld_d >= E, written whole */
+moe_status_t moe_router_topk_bwd(const void *logits, int64_t ld_logits, int32_t logits_dtype,
+                                 const int32_t *topk_ids, const float *d_weights, int32_t T,
+                                 int32_t E, int32_t k, int32_t score, int32_t renorm, float scale,
+                                 const float *add_to, int64_t ld_add, float *d_logits,
+                                 int64_t ld_d, moe_stream_t stream);
 
 /* Load-balance loss of a top-k router and the counts it is made of. With p[t] the softmax of
  * token t's E logits, over the n tokens whose mask is set:
@@ -429,6 +489,53 @@ moe_status_t moe_layernorm_bwd(const void *dy, int64_t lddy, const void *x, int6
                                int32_t x_dtype, int32_t w_dtype, void *ws, size_t ws_bytes,
                                moe_stream_t stream);
 
+/* The residual stream around a block, with root-mean-square norms N(a) = a / sqrt(mean(a^2) + eps)
+ * (over a row) after the block and before the next one:
+ *   u     = post_weight * N(o) (post_norm 1), or post_weight * o (post_norm 0: a gate a feature)
+ *   x_new = x + scale * gate[m] * u
+ *   h     = weight * N(x_new), of x_new as it is stored
+ *   x, x_new     [M, N] of x_dtype, row strides ldx, ldxn >= N; x_new may be x. Without a branch
+ *                (o NULL) x_new is x: x_new must be NULL, and h alone is made
+ *   o, h         [M, N] of o_dtype, row strides ldo, ldh >= N; o may be NULL (no branch), h may be
+ *                NULL (no norm: the last block's sum); h may be o
+ *   post_weight, weight  [N] of w_dtype, each may be NULL (1)
+ *   gate         fp32 [M] or NULL (1)
+ *   rstd_post, rstd  fp32 [M] out, each may be NULL: 1 / sqrt(mean + eps) of the two norms (rstd_post
+ *                is not written without a post norm), which a backward pass needs
+ * x_dtype, o_dtype: both BF16, both FP32, or FP32 and BF16. w_dtype BF16 or FP32 with o_dtype BF16,
+ * FP32 otherwise. eps >= 0, M >= 0, N >= 1. The sums of squares are fp32 ones. */
+moe_status_t moe_residual_norm_fwd(const void *x, int64_t ldx, const void *o, int64_t ldo,
+                                   const void *post_weight, const float *gate,
+                                   const void *weight, void *x_new, int64_t ldxn, void *h,
+                                   int64_t ldh, float *rstd_post, float *rstd, int64_t M,
+                                   int64_t N, float scale, int32_t post_norm, float eps,
+                                   int32_t x_dtype, int32_t o_dtype, int32_t w_dtype,
+                                   moe_stream_t stream);
+/* Its backward pass, from x_new and o as the forward left them, with y = x_new * rstd,
+ * z = o * rstd_post (post_norm 0: o) and q = scale * gate:
+ *   dx  = dx_new + rstd (dh weight - y mean_n(dh weight y))     (the gradient of x, and of x_new)
+ *   do  = q rstd_post (e - z mean_n(e z)),  e = dx post_weight  (post_norm 0: q e)
+ *   d_weight = sum_m dh y;  d_post_weight = sum_m q dx z;  d_gate[m] = scale sum_n e z
+ *   dh, o, do    [M, N] of o_dtype, dx_new, x_new, dx of x_dtype, row strides >= N. dh NULL: no norm
+ *                follows; dx_new NULL: nothing else reads x_new; not both. o NULL: no branch (do,
+ *                d_post_weight, d_gate, post_weight, gate and rstd_post are NULL too). x_new and
+ *                rstd may be NULL without dh
+ *   dx may be dx_new, do may be dh or o; dx NULL: not written (it is dx_new when there is no dh)
+ *   d_weight, d_post_weight [N] of w_dtype out, each may be NULL; summed in fp32 in a fixed order
+ *                (zeros for M = 0).  d_gate fp32 [M] out or NULL
+ * ws: moe_residual_norm_workspace(M, N) bytes, 16-byte aligned (may be NULL when both weight
+ * gradients are). */
+size_t moe_residual_norm_workspace(int64_t M, int64_t N);
+moe_status_t moe_residual_norm_bwd(const void *dh, int64_t lddh, const void *dx_new,
+                                   int64_t lddxn, const void *x_new, int64_t ldxn, const void *o,
+                                   int64_t ldo, const void *post_weight, const float *gate,
+                                   const void *weight, const float *rstd_post, const float *rstd,
+                                   void *dx, int64_t lddx, void *d_o, int64_t lddo,
+                                   void *d_post_weight, void *d_weight, float *d_gate, int64_t M,
+                                   int64_t N, float scale, int32_t post_norm, int32_t x_dtype,
+                                   int32_t o_dtype, int32_t w_dtype, void *ws, size_t ws_bytes,
+                                   moe_stream_t stream);
+
 /* Global gradient norm over n tensors, and clipping:
  *   norm = sqrt(sum over all elements of g^2),  c = min(1, max_norm / (norm + 1e-6)),  out = c*g
  * A NaN anywhere makes norm and c NaN; an infinite element makes c 0 (and itself NaN). Finite
@@ -448,6 +555,54 @@ size_t moe_grad_clip_workspace(void);
 moe_status_t moe_grad_clip(int32_t n, const void *const *grads, void *const *outs,
                            const int64_t *numel, const int32_t *dtypes, float max_norm,
                            float *norm, void *ws, size_t ws_bytes, moe_stream_t stream);
+
+/* One AdamW step over n tensors. With t the steps done before plus 1, g the gradient times the clip
+ * factor, p the fp32 value of a weight (its master where it has one):
+ *   m <- beta1 m + (1 - beta1) g;  v <- beta2 v + ((1 - beta2) g) g
+ *   p <- (p - lr decay p) - lr / (1 - beta1^t) * m / (sqrt(v) / sqrt(1 - beta2^t) + eps)
+ * each product, sum and root of m and v one rounded fp32 operation.
+ * States in 8 bits hold m and r = sqrt(v) (v = r r when read). 256 values in a row share a scale byte
+ * b; a code's magnitude c (1..127 for m, under a sign bit; 1..255 for r) stands for the fp32 number
+ * whose bits are (c + 8 b + 7 - C) << 20, C = 127 or 255: eight values a power of two, 16 or 32 powers
+ * of two down from 2^(b - 127) * 1.875; c = 0 is 0. b is the smallest that holds the block's largest
+ * value rounded up (at least 32), 255 for a block with a NaN or an infinity, whose values are NaN.
+ * Values are rounded to one of their two neighbours at random, in proportion to their distance
+ * (sixteen random bits: the low half of a 32-bit word for m, the high half for r), so that small
+ * changes are not lost. The word of element e of tensor i in step t is
+ *   mix(low32(e) ^ mix(high32(e) ^ mix(i + mix(low32(t) ^ mix(low32(seed) ^ mix(high32(seed)))))))
+ * with mix(x): x ^= x >> 16; x *= 0xf75341d5; x ^= x >> 15; x *= 0x99d5d0a1; x ^= x >> 16. The same
+ * seed and inputs give the same result.
+ *   tensors    HOST array, read before the call returns. Pointers are aligned to their elements;
+ *              tensors that are written share no memory with others
+ *   state_bits 32: m and v are fp32. 8: codes, with the scale bytes in m_scale and v_scale
+ *   lr_device  fp32 [1] device, or NULL: the learning rate is lr
+ *   grad_norm  fp32 [1] device (moe_grad_clip's norm), or NULL. With it the gradients are multiplied
+ *              by min(1, max_norm / (norm + 1e-6)) (max_norm +inf: by 1), and a norm that is not
+ *              finite skips the step: nothing is written
+ *   counters   int64 [2] device, zeroed by the caller before the first step: the steps done, and a
+ *              count of the kernel's own. Calls that share them must not overlap
+ * lr, decay and eps finite and >= 0, beta1 and beta2 in [0, 1), max_norm > 0. n in [0, 65536]. */
+typedef struct {
+  void *param;         /* param_dtype [numel], written                                        */
+  float *master;       /* fp32 [numel] behind bf16 weights, written; NULL for fp32 weights    */
+  const void *grad;    /* grad_dtype [numel]                                                  */
+  void *m, *v;         /* [numel] states: fp32, or uint8 codes of m and of sqrt(v)            */
+  uint8_t *m_scale;    /* [ceil(numel / 256)] scale bytes of 8-bit states, NULL otherwise     */
+  uint8_t *v_scale;
+  int64_t numel;       /* >= 0                                                                */
+  int32_t param_dtype; /* moe_dtype_t; MOE_DT_BF16 needs a master                             */
+  int32_t grad_dtype;  /* moe_dtype_t                                                         */
+  float decay;         /* weight decay                                                        */
+  int32_t reserved;    /* 0                                                                   */
+} moe_adamw_tensor_t;
+moe_status_t moe_adamw_step(int32_t n, const moe_adamw_tensor_t *tensors, int32_t state_bits,
+                            double lr, const float *lr_device, double beta1, double beta2,
+                            double eps, const float *grad_norm, float max_norm, uint64_t seed,
+                            int64_t *counters, moe_stream_t stream);
+/* The values that 8-bit states stand for: m and sqrt(v), bf16 [numel] each (four significant bits:
+ * exact). m_out, v_out: HOST arrays of n device pointers, element-aligned. */
+moe_status_t moe_adamw_moments(int32_t n, const moe_adamw_tensor_t *tensors, void *const *m_out,
+                               void *const *v_out, moe_stream_t stream);
 
 /* E4M3 with one fp32 scale for each block of 128 (the layout of block-scaled FP8 checkpoints):
  *   a = max(amax of the block, 2^-100),  s = a / 448,  code = E4M3(v * (448 / a)),
@@ -556,7 +711,15 @@ typedef enum {
   MOE_K_GRAD_SCALE = 25,
   MOE_K_FP8_QUANTIZE = 26,
   MOE_K_FP8_GEMM = 27,
-  MOE_K_COUNT = 28
+  MOE_K_COUNT_IDS = 28,
+  MOE_K_ROUTER_TOPK = 29,
+  MOE_K_ROUTER_TOPK_GRAD = 30,
+  MOE_K_RESIDUAL_NORM_FWD = 31,
+  MOE_K_RESIDUAL_NORM_BWD = 32,
+  MOE_K_RESIDUAL_NORM_REDUCE = 33,
+  MOE_K_ADAMW = 34,
+  MOE_K_ADAMW_MOMENTS = 35,
+  MOE_K_COUNT = 36
 } moe_kernel_id_t;
 
 /* Launch timeline, for measurement. Between moe_timeline_begin and moe_timeline_end the
