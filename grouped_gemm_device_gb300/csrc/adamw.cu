@@ -31,7 +31,9 @@ struct Tensor {
   int64_t first;  // its first block of 256 among the launch's
   float decay;
   int32_t index;  // in the caller's list
-  int16_t p_bf16, g_bf16, vec, unused;
+  int16_t p_bf16, g_bf16;
+  int16_t wide;   // its arrays lie on boundaries of eight elements (16 bytes at least)
+  int16_t unused;
 };
 struct Batch {
   Tensor t[kCap];
@@ -118,7 +120,7 @@ MOE_DEVICE Now step_now(const Step& s) {
   return n;
 }
 
-// m, v and the weight after the step; v2 the second moment before it.
+// m, v and sqrt(v) after the step; v2 the second moment before it.
 struct Moments {
   float m, v, r;
 };
@@ -129,12 +131,175 @@ MOE_DEVICE Moments advance(float g, float m, float v2, const Step& s) {
   o.r = __fsqrt_rn(o.v);
   return o;
 }
+// The quotient within two steps: r rb + eps is 0 or between 2^-75 and 2^126.
 MOE_DEVICE float update(float p, const Moments& o, float lr_decay, const Now& n, const Step& s) {
-  return (p - p * lr_decay) - n.a * (o.m / (o.r * n.rb + s.eps));
+  return (p - p * lr_decay) - n.a * __fdividef(o.m, o.r * n.rb + s.eps);
 }
 
+// 8 fp32 or 16 bytes in one access; streamed data is not kept in L1.
+MOE_DEVICE void load8(const void* p, float (&x)[8]) {
+  asm volatile("ld.global.L1::no_allocate.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3]), "=f"(x[4]), "=f"(x[5]),
+                 "=f"(x[6]), "=f"(x[7])
+               : "l"(p));
+}
+MOE_DEVICE void store8(void* p, const float (&x)[8]) {
+  asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(x[0]),
+               "f"(x[1]), "f"(x[2]), "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7])
+               : "memory");
+}
+MOE_DEVICE uint4 load4(const void* p) {
+  uint4 q;
+  asm volatile("ld.global.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(q.x), "=r"(q.y), "=r"(q.z), "=r"(q.w)
+               : "l"(p));
+  return q;
+}
+MOE_DEVICE uint2 load2(const void* p) {
+  uint2 q;
+  asm volatile("ld.global.L1::no_allocate.v2.b32 {%0, %1}, [%2];" : "=r"(q.x), "=r"(q.y) : "l"(p));
+  return q;
+}
+MOE_DEVICE uint32_t byte_of(const uint2& q, int j) {  // j is a constant after unrolling
+  return ((j < 4 ? q.x : q.y) >> (8 * (j & 3))) & 255u;
+}
+
+// A block of 256: lane i has elements 8 i .. 8 i + 7 (WIDE: a full block whose arrays allow whole
+// vectors), or every 32nd element from i on.
+template <int BITS, bool WIDE>
+MOE_DEVICE void adamw_block(const Tensor& t, int64_t blk, int lane, const Now& n, const Step& s) {
+  const int64_t e0 = blk * kBlock + (WIDE ? lane * 8 : lane);
+  auto at = [&](int j) { return WIDE ? e0 + j : e0 + j * 32; };
+  auto in = [&](int j) { return WIDE || at(j) < t.numel; };
+  float* weights = t.p_bf16 ? t.master : static_cast<float*>(t.p);
+  float g[8], p[8], m[8], v[8];
+  uint32_t sm = 0, sv = 0;
+  if constexpr (BITS == 8) {
+    sm = t.m_scale[blk];
+    sv = t.v_scale[blk];
+  }
+  if constexpr (WIDE) {
+    uint4 gq;
+    uint2 mc, vc;
+    if (t.g_bf16) gq = load4(static_cast<const __nv_bfloat16*>(t.g) + e0);
+    else load8(static_cast<const float*>(t.g) + e0, g);
+    load8(weights + e0, p);
+    if constexpr (BITS == 8) {
+      mc = load2(static_cast<const uint8_t*>(t.m) + e0);
+      vc = load2(static_cast<const uint8_t*>(t.v) + e0);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        m[j] = decode_m(byte_of(mc, j), sm);
+        v[j] = decode_r(byte_of(vc, j), sv);
+      }
+    } else {
+      load8(static_cast<const float*>(t.m) + e0, m);
+      load8(static_cast<const float*>(t.v) + e0, v);
+    }
+    if (t.g_bf16) {
+      const uint32_t w[4] = {gq.x, gq.y, gq.z, gq.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        g[2 * j] = bf16_lo(w[j]);
+        g[2 * j + 1] = bf16_hi(w[j]);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      g[j] = p[j] = m[j] = v[j] = 0.f;
+      if (!in(j)) continue;
+      const int64_t e = at(j);
+      g[j] = t.g_bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(t.g)[e])
+                      : static_cast<const float*>(t.g)[e];
+      p[j] = weights[e];
+      if constexpr (BITS == 8) {
+        m[j] = decode_m(static_cast<const uint8_t*>(t.m)[e], sm);
+        v[j] = decode_r(static_cast<const uint8_t*>(t.v)[e], sv);
+      } else {
+        m[j] = static_cast<const float*>(t.m)[e];
+        v[j] = static_cast<const float*>(t.v)[e];
+      }
+    }
+  }
+  const float lr_decay = n.lr * t.decay;
+  uint32_t most_m = 0, most_r = 0;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    if constexpr (BITS == 8) v[j] = __fmul_rn(v[j], v[j]);
+    const Moments o = advance(__fmul_rn(g[j], n.factor), m[j], v[j], s);
+    p[j] = update(p[j], o, lr_decay, n, s);
+    m[j] = o.m;
+    v[j] = BITS == 8 ? o.r : o.v;
+    if constexpr (BITS == 8) {  // elements past the end are 0
+      most_m = max(most_m, __float_as_uint(fabsf(o.m)));
+      most_r = max(most_r, __float_as_uint(fabsf(o.r)));
+    }
+  }
+  if constexpr (WIDE) {
+    store8(weights + e0, p);
+    if (t.p_bf16)
+      *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(t.p) + e0) =
+          make_uint4(pack_bf16x2(p[0], p[1]), pack_bf16x2(p[2], p[3]), pack_bf16x2(p[4], p[5]),
+                     pack_bf16x2(p[6], p[7]));
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (in(j)) {
+        weights[at(j)] = p[j];
+        if (t.p_bf16) static_cast<__nv_bfloat16*>(t.p)[at(j)] = __float2bfloat16_rn(p[j]);
+      }
+  }
+  if constexpr (BITS == 32) {
+    if constexpr (WIDE) {
+      store8(static_cast<float*>(t.m) + e0, m);
+      store8(static_cast<float*>(t.v) + e0, v);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (in(j)) {
+          static_cast<float*>(t.m)[at(j)] = m[j];
+          static_cast<float*>(t.v)[at(j)] = v[j];
+        }
+    }
+  } else {
+    sm = block_scale(__reduce_max_sync(0xFFFFFFFFu, most_m));
+    sv = block_scale(__reduce_max_sync(0xFFFFFFFFu, most_r));
+    const uint32_t key = mix((uint32_t)(e0 >> 32) ^ mix((uint32_t)t.index + n.key));
+    uint32_t cm[8], cv[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const uint32_t w = mix((uint32_t)at(j) ^ key);
+      cm[j] = encode(fabsf(m[j]), w & 0xFFFFu, sm, 127);
+      if (m[j] < 0.f && cm[j]) cm[j] |= 128u;
+      cv[j] = encode(v[j], w >> 16, sv, 255);
+    }
+    if constexpr (WIDE) {
+      auto bytes = [](const uint32_t(&c)[8]) {
+        return make_uint2(c[0] | c[1] << 8 | c[2] << 16 | c[3] << 24,
+                          c[4] | c[5] << 8 | c[6] << 16 | c[7] << 24);
+      };
+      *reinterpret_cast<uint2*>(static_cast<uint8_t*>(t.m) + e0) = bytes(cm);
+      *reinterpret_cast<uint2*>(static_cast<uint8_t*>(t.v) + e0) = bytes(cv);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (in(j)) {
+          static_cast<uint8_t*>(t.m)[at(j)] = (uint8_t)cm[j];
+          static_cast<uint8_t*>(t.v)[at(j)] = (uint8_t)cv[j];
+        }
+    }
+    if (lane == 0) {
+      t.m_scale[blk] = (uint8_t)sm;
+      t.v_scale[blk] = (uint8_t)sv;
+    }
+  }
+}
+
+// Four blocks an SM: 403 M elements with 32-bit states 1740 us, with three 1826, with five (registers
+// for one) 1903.
 template <int BITS>
-__global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__ Batch b,
+__global__ void __launch_bounds__(kThreads, 4) adamw_kernel(const __grid_constant__ Batch b,
                                                          const __grid_constant__ Step s) {
   MOE_GRIDDEP_ENTRY();
   __shared__ Now sn;
@@ -146,63 +311,9 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
   for (int64_t c = (int64_t)blockIdx.x * kWarps + warp; c < b.blocks;
        c += (int64_t)gridDim.x * kWarps) {
     const Tensor& t = b.t[find_tensor(b, c)];
-    const int64_t blk = c - t.first, e0 = blk * kBlock;
-    const float lr_decay = n.lr * t.decay;
-    const uint32_t key = mix((uint32_t)(e0 >> 32) ^ mix((uint32_t)t.index + n.key));
-    uint32_t sm = 0, sv = 0;
-    if constexpr (BITS == 8) {
-      sm = t.m_scale[blk];
-      sv = t.v_scale[blk];
-    }
-    Moments o[8];
-    uint32_t most_m = 0, most_r = 0;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int64_t e = e0 + j * 32 + lane;
-      o[j] = {0.f, 0.f, 0.f};
-      if (e >= t.numel) continue;
-      float g = t.g_bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(t.g)[e])
-                         : static_cast<const float*>(t.g)[e];
-      g = __fmul_rn(g, n.factor);
-      float m, v;
-      if constexpr (BITS == 8) {
-        m = decode_m(static_cast<const uint8_t*>(t.m)[e], sm);
-        const float r = decode_r(static_cast<const uint8_t*>(t.v)[e], sv);
-        v = __fmul_rn(r, r);
-      } else {
-        m = static_cast<const float*>(t.m)[e];
-        v = static_cast<const float*>(t.v)[e];
-      }
-      o[j] = advance(g, m, v, s);
-      float* pm = t.p_bf16 ? t.master : static_cast<float*>(t.p);
-      const float p = update(pm[e], o[j], lr_decay, n, s);
-      pm[e] = p;
-      if (t.p_bf16) static_cast<__nv_bfloat16*>(t.p)[e] = __float2bfloat16_rn(p);
-      if constexpr (BITS == 8) {
-        most_m = max(most_m, __float_as_uint(fabsf(o[j].m)));
-        most_r = max(most_r, __float_as_uint(fabsf(o[j].r)));
-      } else {
-        static_cast<float*>(t.m)[e] = o[j].m;
-        static_cast<float*>(t.v)[e] = o[j].v;
-      }
-    }
-    if constexpr (BITS == 8) {
-      sm = block_scale(__reduce_max_sync(0xFFFFFFFFu, most_m));
-      sv = block_scale(__reduce_max_sync(0xFFFFFFFFu, most_r));
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int64_t e = e0 + j * 32 + lane;
-        if (e >= t.numel) continue;
-        const uint32_t w = mix((uint32_t)e ^ key);
-        const uint32_t cm = encode(fabsf(o[j].m), w & 0xFFFFu, sm, 127);
-        static_cast<uint8_t*>(t.m)[e] = (uint8_t)(cm | (cm && o[j].m < 0.f ? 128u : 0u));
-        static_cast<uint8_t*>(t.v)[e] = (uint8_t)encode(o[j].r, w >> 16, sv, 255);
-      }
-      if (lane == 0) {
-        t.m_scale[blk] = (uint8_t)sm;
-        t.v_scale[blk] = (uint8_t)sv;
-      }
-    }
+    const int64_t blk = c - t.first;
+    if (t.wide && (blk + 1) * kBlock <= t.numel) adamw_block<BITS, true>(t, blk, lane, n, s);
+    else adamw_block<BITS, false>(t, blk, lane, n, s);
   }
   if (!s.last) return;
   if (threadIdx.x == 0) {  // this block's read of the count lies before its ticket
@@ -227,6 +338,24 @@ __global__ void __launch_bounds__(kThreads) adamw_moments_kernel(const __grid_co
     const Tensor& t = b.t[i];
     const int64_t blk = c - t.first, e0 = blk * kBlock;
     const uint32_t sm = t.m_scale[blk], sv = t.v_scale[blk];
+    if (t.wide && e0 + kBlock <= t.numel) {
+      const int64_t e = e0 + lane * 8;
+      const uint2 mc = load2(static_cast<const uint8_t*>(t.m) + e);
+      const uint2 vc = load2(static_cast<const uint8_t*>(t.v) + e);
+      float m[8], v[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        m[j] = decode_m(byte_of(mc, j), sm);
+        v[j] = decode_r(byte_of(vc, j), sv);
+      }
+      *reinterpret_cast<uint4*>(out.m[i] + e) = make_uint4(
+          pack_bf16x2(m[0], m[1]), pack_bf16x2(m[2], m[3]), pack_bf16x2(m[4], m[5]),
+          pack_bf16x2(m[6], m[7]));
+      *reinterpret_cast<uint4*>(out.v[i] + e) = make_uint4(
+          pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+          pack_bf16x2(v[6], v[7]));
+      continue;
+    }
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const int64_t e = e0 + j * 32 + lane;
@@ -240,16 +369,18 @@ __global__ void __launch_bounds__(kThreads) adamw_moments_kernel(const __grid_co
 bool on(const void* p, int bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
 
 // Tensors [i, ..) of the list that hold elements, up to kCap; returns the next index.
-int fill_batch(Batch& b, int i, int n, const moe_adamw_tensor_t* list, int* from) {
+int fill_batch(Batch& b, int i, int n, const moe_adamw_tensor_t* list, int bits) {
   b.n = 0;
   b.blocks = 0;
+  const int state = bits == 8 ? 8 : 32;  // bytes of eight values
   for (; i < n && b.n < kCap; ++i) {
     const moe_adamw_tensor_t& l = list[i];
     if (l.numel == 0) continue;
-    if (from) from[b.n] = i;
-    Tensor& t = b.t[b.n++];
-    t = {l.param, l.master, l.grad, l.m, l.v, l.m_scale, l.v_scale, l.numel, b.blocks, l.decay, i,
-         l.param_dtype == MOE_DT_BF16, l.grad_dtype == MOE_DT_BF16, 0, 0};
+    const int pb = l.param_dtype == MOE_DT_BF16, gb = l.grad_dtype == MOE_DT_BF16;
+    const bool wide = on(l.param, pb ? 16 : 32) && on(l.master, 32) && on(l.grad, gb ? 16 : 32) &&
+                      on(l.m, state) && on(l.v, state);
+    b.t[b.n++] = {l.param, l.master, l.grad, l.m, l.v, l.m_scale, l.v_scale, l.numel, b.blocks,
+                  l.decay, i, (int16_t)pb, (int16_t)gb, (int16_t)wide, 0};
     b.blocks += (l.numel + kBlock - 1) / kBlock;
   }
   return i;
@@ -325,7 +456,7 @@ moe_status_t moe_adamw_step(int32_t n, const moe_adamw_tensor_t* tensors, int32_
   Batch b;
   int i = 0;
   do {
-    i = fill_batch(b, i, n, tensors, nullptr);
+    i = fill_batch(b, i, n, tensors, state_bits);
     int left = i;
     while (left < n && tensors[left].numel == 0) ++left;
     step.last = left == n;
@@ -350,13 +481,13 @@ moe_status_t moe_adamw_moments(int32_t n, const moe_adamw_tensor_t* tensors, voi
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   Batch b;
   MomentsOut out;
-  int from[kCap];
   for (int i = 0; i < n;) {
-    i = fill_batch(b, i, n, tensors, from);
+    i = fill_batch(b, i, n, tensors, 8);
     if (b.n == 0) break;
     for (int j = 0; j < b.n; ++j) {
-      out.m[j] = static_cast<__nv_bfloat16*>(m_out[from[j]]);
-      out.v[j] = static_cast<__nv_bfloat16*>(v_out[from[j]]);
+      out.m[j] = static_cast<__nv_bfloat16*>(m_out[b.t[j].index]);
+      out.v[j] = static_cast<__nv_bfloat16*>(v_out[b.t[j].index]);
+      b.t[j].wide = on(b.t[j].m, 8) && on(b.t[j].v, 8) && on(out.m[j], 16) && on(out.v[j], 16);
     }
     const cudaError_t e = launch_pdl(adamw_moments_kernel, adamw_blocks<adamw_moments_kernel>(b.blocks),
                                      kThreads, 0, s, 1, b, out);
