@@ -191,6 +191,54 @@ def test_gradients_that_are_not_finite_without_a_norm(lib):
             assert bad[hit].all() and int(bad.sum()) == hit.stop - hit.start
 
 
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("eps", [1e-8, 0.0])
+@pytest.mark.parametrize("scale", [1e-16, 1e-19, 1e-30, 1e-4, 1e8, 1e15])
+def test_far_magnitudes(lib, bits, eps, scale):
+    """Gradients whose squares are subnormal, 0 or near fp32's end, and elements far below their
+    block's largest: the codes are the oracle's, the weights move by lr where eps is 0."""
+    gen = torch.Generator().manual_seed(2)
+    params = [torch.zeros(5000, device="cuda")]
+    grads = [torch.randn(5000, generator=gen).mul_(scale).cuda()]
+    grads[0][::3] *= 1e-4
+    grads[0][1000:1600] = 0
+    grads[0][2048:2300] *= 2.0 ** -20
+    opt = g.AdamW(params, grads, lr=LR, betas=(B1, B2), eps=eps, weight_decay=0.0, state_bits=bits)
+    m = v = np.zeros(5000)
+    codes = None
+    for t in range(1, 4):
+        gr = f64(grads[0])
+        r = None
+        if bits == 8 and codes is not None:
+            m, r = so.decode(*codes[0], True), so.decode(*codes[1], False)
+        m32 = m.astype(np.float32)
+        v32 = v.astype(np.float32) if r is None else r.astype(np.float32) * r.astype(np.float32)
+        with np.errstate(under="ignore"):
+            m1, v1, r1 = so.moments(gr.astype(np.float32), m32, v32, B1, B2)
+        before = f64(params[0])
+        opt.step()
+        if bits == 8:
+            w = so.words(0, t, 0, 5000)
+            codes = (so.encode(m1, (w & np.uint64(0xFFFF)).astype(np.int64), True),
+                     so.encode(r1, (w >> np.uint64(16)).astype(np.int64), False))
+            for (c, s), own, scales in zip(codes, (opt.m, opt.v), (opt.m_exp, opt.v_exp)):
+                assert (own[0].cpu().numpy() == c).all() and (scales[0].cpu().numpy() == s).all()
+        else:
+            # the same roundings, whatever the path
+            assert (f64(opt.m[0]) == m1).all() and (f64(opt.v[0]) == v1).all()
+            m, v = m1.astype(np.float64), v1.astype(np.float64)
+        # r32 is the rounded root; the move is off by a few roundings of itself and of the weight
+        with np.errstate(invalid="ignore", divide="ignore"):
+            c1, c2 = 1 - B1 ** t, 1 - B2 ** t
+            move = LR / c1 * m1.astype(np.float64) / (r1.astype(np.float64) / c2 ** 0.5 + eps)
+        after = f64(params[0])
+        ok = np.isfinite(move)
+        assert (~ok == ((r1 == 0) & (eps == 0))).all()
+        assert (np.abs(after - (before - move))[ok] <= 40 * U * np.abs(move)[ok]
+                + 2 * U * np.abs(before)[ok]).all()
+        params[0].zero_()   # 0 / 0 where nothing has been seen and eps is 0
+
+
 def test_moments(lib):
     """Every code under several scales, the smallest and the largest among them."""
     params, grads, _ = make([2000, 5], [(F32, F32)] * 2)
