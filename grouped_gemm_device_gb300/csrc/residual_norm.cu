@@ -8,44 +8,10 @@
 // Bound by HBM: the forward reads x and o and writes x' and h, the backward reads dh, dx', x' and o
 // and writes dx and do.
 #include "kernels.cuh"
+#include "row8.cuh"
 
 namespace moe {
 namespace {
-
-template <typename T>
-MOE_DEVICE float to_f(T v) {
-  if constexpr (sizeof(T) == 2) return __bfloat162float(v);
-  else return v;
-}
-template <typename T>
-MOE_DEVICE T from_f(float v) {
-  if constexpr (sizeof(T) == 2) return __float2bfloat16_rn(v);
-  else return v;
-}
-// A norm's weight: bf16, fp32 or none (1).
-struct Weight {
-  const void* p;
-  int fp32;
-};
-MOE_DEVICE float weight_at(const Weight& w, int64_t c) {
-  if (!w.p) return 1.0f;
-  return w.fp32 ? static_cast<const float*>(w.p)[c]
-                : __bfloat162float(static_cast<const __nv_bfloat16*>(w.p)[c]);
-}
-
-// Sum over a block of 1024 threads, the same in each. `sm` must not be in use by a call less than
-// one barrier ago.
-MOE_DEVICE float block_sum(float a, float (&sm)[32]) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) a += __shfl_xor_sync(0xFFFFFFFFu, a, o);
-  const int lane = threadIdx.x & 31;
-  if (lane == 0) sm[threadIdx.x >> 5] = a;
-  __syncthreads();
-  a = sm[lane];
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) a += __shfl_xor_sync(0xFFFFFFFFu, a, o);
-  return a;
-}
 
 struct FwdArgs {
   const void *x, *o;
@@ -72,10 +38,10 @@ __global__ void __launch_bounds__(1024) rn_fwd_any_kernel(const FwdArgs a) {
     if (a.post) {
       float s = 0.f;
       for (int64_t c = threadIdx.x; c < a.N; c += 1024) {
-        const float v = to_f(o[c]);
+        const float v = to_float(o[c]);
         s += v * v;
       }
-      rp = 1.0f / sqrtf(block_sum(s, sm[0]) / (float)a.N + a.eps);
+      rp = 1.0f / sqrtf(group_sum<1024>(s, sm[0]) / (float)a.N + a.eps);
       if (threadIdx.x == 0 && a.rstd_post) a.rstd_post[row] = rp;
     }
     const float q = a.gate ? a.scale * a.gate[row] : a.scale;
@@ -83,23 +49,105 @@ __global__ void __launch_bounds__(1024) rn_fwd_any_kernel(const FwdArgs a) {
     for (int64_t c = threadIdx.x; c < a.N; c += 1024) {
       XT v = x[c];
       if (a.o) {
-        const float z = a.post ? to_f(o[c]) * rp : to_f(o[c]);
-        v = from_f<XT>(to_f(v) + q * (z * weight_at(a.wp, c)));
+        const float z = a.post ? to_float(o[c]) * rp : to_float(o[c]);
+        v = from_float<XT>(to_float(v) + q * (z * weight_at(a.wp, c)));
         xn[c] = v;
       }
-      s += to_f(v) * to_f(v);
+      s += to_float(v) * to_float(v);
     }
     if (a.h) {
-      const float r = 1.0f / sqrtf(block_sum(s, sm[1]) / (float)a.N + a.eps);
+      const float r = 1.0f / sqrtf(group_sum<1024>(s, sm[1]) / (float)a.N + a.eps);
       if (threadIdx.x == 0 && a.rstd) a.rstd[row] = r;
       const XT* y = a.o ? xn : x;
       for (int64_t c = threadIdx.x; c < a.N; c += 1024)
-        static_cast<OT*>(a.h)[row * a.ldh + c] = from_f<OT>(to_f(y[c]) * r * weight_at(a.w, c));
+        static_cast<OT*>(a.h)[row * a.ldh + c] = from_float<OT>(to_float(y[c]) * r * weight_at(a.w, c));
     }
     __syncthreads();  // the sums' places are used again
   }
 }
 
+// A row of up to 8 G PER columns (ANY: 7 less) in the registers of G threads, a warp of four in a block
+// or a whole block: read once, both sums taken, written once.
+template <typename XT, typename OT, int G, int PER, bool ANY>
+__global__ void __launch_bounds__(G < 128 ? 128 : G) rn_fwd_kernel(const FwdArgs a) {
+  MOE_GRIDDEP_ENTRY();
+  __shared__ float sm[2][32];
+  constexpr int R = G < 128 ? 128 / G : 1;
+  const int t = threadIdx.x % G, N = (int)a.N;
+  const int64_t row = (int64_t)blockIdx.x * R + threadIdx.x / G;
+  if (G == 32 && row >= a.M) return;  // a block's groups are its warps; otherwise R = 1
+  const XT* x = static_cast<const XT*>(a.x) + row * a.ldx;
+  const OT* o = static_cast<const OT*>(a.o) + row * a.ldo;
+  const int lead = ANY ? lead8(x) : 0;
+  Raw8<XT> xr[PER];
+  Raw8<OT> br[PER];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int c = (i * G + t) * 8 - lead;
+    zero8(xr[i]);
+    zero8(br[i]);
+    if (c < N) {
+      if (a.o) load8(o + c, br[i]);
+      load8(x + c, xr[i]);
+      if (ANY && (c < 0 || c + 8 > N)) {
+        clear8(br[i], -c, N - c);
+        clear8(xr[i], -c, N - c);
+      }
+    }
+  }
+  float s = 0.f;
+  if (a.o) {
+    float rp = 1.0f;
+    if (a.post) {
+#pragma unroll
+      for (int i = 0; i < PER; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) s += at8(br[i], j) * at8(br[i], j);
+      rp = 1.0f / sqrtf(group_sum<G>(s, sm[0]) / (float)N + a.eps);
+      if (t == 0 && a.rstd_post) a.rstd_post[row] = rp;
+    }
+    const float q = (a.gate ? a.scale * a.gate[row] : a.scale) * rp;
+    s = 0.f;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int c = (i * G + t) * 8 - lead;
+      if (c < N) {
+        float wp[8], v[8];
+        weights8<ANY>(a.wp, c, N, wp);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = at8(xr[i], j) + q * (at8(br[i], j) * wp[j]);
+        round8(v, xr[i]);
+        store8<ANY>(static_cast<XT*>(a.xn) + row * a.ldxn + c, xr[i], -c, N - c);
+      }
+    }
+  }
+  if (!a.h) return;
+#pragma unroll
+  for (int i = 0; i < PER; ++i)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) s += at8(xr[i], j) * at8(xr[i], j);
+  const float r = 1.0f / sqrtf(group_sum<G>(s, sm[1]) / (float)N + a.eps);
+  if (t == 0 && a.rstd) a.rstd[row] = r;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int c = (i * G + t) * 8 - lead;
+    if (c < N) {
+      float w[8];
+      weights8<ANY>(a.w, c, N, w);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) w[j] *= at8(xr[i], j) * r;
+      Raw8<OT> hr;
+      round8(w, hr);
+      store8<ANY>(static_cast<OT*>(a.h) + row * a.ldh + c, hr, -c, N - c);
+    }
+  }
+}
+
+// A row of partial sums: whole vectors, and the place of a row's first element in its first one.
+template <typename I>
+__host__ __device__ constexpr I part_pitch(I N) {
+  return (N + 7) / 8 * 8 + 8;
+}
 struct BwdArgs {
   const void *dh, *dxn, *xn, *o;
   void *dx, *d_o;
@@ -109,14 +157,17 @@ struct BwdArgs {
   float* d_gate;
   float scale;
   int post;
-  float* part;  // [blocks][2][N]: dw, dwp
+  float* part;  // [blocks][2][part_pitch(N)]: dw, dwp
+  void *dw, *dwp;
+  int w_fp32;
 };
 
 template <typename XT, typename OT>
 __global__ void __launch_bounds__(1024) rn_bwd_any_kernel(const BwdArgs a) {
   MOE_GRIDDEP_ENTRY();
   __shared__ float sm[2][32];
-  float* part = a.part ? a.part + (int64_t)blockIdx.x * 2 * a.N : nullptr;
+  const int64_t NP = part_pitch(a.N);
+  float* part = a.part ? a.part + (int64_t)blockIdx.x * 2 * NP : nullptr;
   bool first = true;
   for (int64_t row = blockIdx.x; row < a.M; row += gridDim.x) {
     const OT* dh = static_cast<const OT*>(a.dh) + row * a.lddh;
@@ -128,53 +179,319 @@ __global__ void __launch_bounds__(1024) rn_bwd_any_kernel(const BwdArgs a) {
     float c1 = 0.f;
     if (a.dh) {
       for (int64_t c = threadIdx.x; c < a.N; c += 1024)
-        c1 += to_f(dh[c]) * weight_at(a.w, c) * (to_f(xn[c]) * r);
-      c1 = block_sum(c1, sm[0]) / (float)a.N;
+        c1 += to_float(dh[c]) * weight_at(a.w, c) * (to_float(xn[c]) * r);
+      c1 = group_sum<1024>(c1, sm[0]) / (float)a.N;
     }
     auto grad = [&](int64_t c) {
-      float d = a.dxn ? to_f(dxn[c]) : 0.f;
-      if (a.dh) d += r * (to_f(dh[c]) * weight_at(a.w, c) - to_f(xn[c]) * r * c1);
+      float d = a.dxn ? to_float(dxn[c]) : 0.f;
+      if (a.dh) d += r * (to_float(dh[c]) * weight_at(a.w, c) - to_float(xn[c]) * r * c1);
       return d;
     };
     float dot = 0.f;
     if (a.o && (a.post || a.d_gate)) {
       for (int64_t c = threadIdx.x; c < a.N; c += 1024)
-        dot += grad(c) * weight_at(a.wp, c) * (to_f(o[c]) * rp);
-      dot = block_sum(dot, sm[1]);
+        dot += grad(c) * weight_at(a.wp, c) * (to_float(o[c]) * rp);
+      dot = group_sum<1024>(dot, sm[1]);
       if (threadIdx.x == 0 && a.d_gate) a.d_gate[row] = a.scale * dot;
     }
     const float c2 = a.post ? dot / (float)a.N : 0.f;
     for (int64_t c = threadIdx.x; c < a.N; c += 1024) {
       const float d = grad(c);
-      const float y = a.dh ? to_f(xn[c]) * r : 0.f, dw = a.dh ? to_f(dh[c]) * y : 0.f;
-      const float z = a.o ? to_f(o[c]) * rp : 0.f, dwp = q * d * z;
+      const float y = a.dh ? to_float(xn[c]) * r : 0.f, dw = a.dh ? to_float(dh[c]) * y : 0.f;
+      const float z = a.o ? to_float(o[c]) * rp : 0.f, dwp = q * d * z;
       if (part) {  // column c belongs to this thread in every row
         part[c] = first ? dw : part[c] + dw;
-        part[a.N + c] = first ? dwp : part[a.N + c] + dwp;
+        part[NP + c] = first ? dwp : part[NP + c] + dwp;
       }
-      if (a.dx) static_cast<XT*>(a.dx)[row * a.lddx + c] = from_f<XT>(d);
+      if (a.dx) static_cast<XT*>(a.dx)[row * a.lddx + c] = from_float<XT>(d);
       if (a.d_o)
         static_cast<OT*>(a.d_o)[row * a.lddo + c] =
-            from_f<OT>(q * rp * (d * weight_at(a.wp, c) - z * c2));
+            from_float<OT>(q * rp * (d * weight_at(a.wp, c) - z * c2));
     }
     first = false;
     __syncthreads();
   }
 }
 
-// dw (columns [0, N)) and dwp (columns [N, 2 N)) = sum of the blocks' partials in a fixed order.
+
+// Threads a block of the kernel that walks rows: eight warps with a row each, or one row.
+constexpr int block_of(int G) { return G == 32 ? 256 : G; }
+template <int N>
+MOE_DEVICE void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+MOE_DEVICE void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+// 16-byte units of a vector of the four tensors that are read: x_new, dx_new, o, dh.
+template <typename XT, typename OT>
+constexpr int units() {
+  return (int)(sizeof(XT) + sizeof(OT));
+}
+
+// A group of G threads walks rows that lie alike in their vectors; a thread owns the same 8 PER columns
+// of every row and keeps their sums of the weights' gradients in registers until the end. Each thread
+// copies its own columns of the next S - 1 rows into a ring in shared memory (cp.async), so that no
+// barrier is spent on the copies. N (ANY: N + 7) <= 8 G PER, and the groups' number a multiple of 8 where
+// ANY and a group takes more than one row.
+template <typename XT, typename OT, int G, int PER, int S, bool ANY>
+__global__ void __launch_bounds__(block_of(G), G == 288 ? 2 : 1) rn_bwd_kernel(const BwdArgs a) {
+  MOE_GRIDDEP_ENTRY();
+  constexpr int B = block_of(G), GROUPS = B / G, U = units<XT, OT>();
+  constexpr int UX = sizeof(XT) / 2, UO = sizeof(OT) / 2;
+  // few enough columns a thread to hold both weights beside the sums
+  constexpr bool kKeep = PER <= 2 && G <= 512;
+  __shared__ float sm[2][2][32];
+  extern __shared__ uint4 ring[];  // [S][PER][U][B]
+  const int t = threadIdx.x % G, N = (int)a.N;
+  const int64_t row0 = (int64_t)blockIdx.x * GROUPS + threadIdx.x / G;
+  const int64_t step = (int64_t)gridDim.x * GROUPS;
+  const XT* xn = static_cast<const XT*>(a.xn);
+  const XT* dxn = static_cast<const XT*>(a.dxn);
+  const OT* o = static_cast<const OT*>(a.o);
+  const OT* dh = static_cast<const OT*>(a.dh);
+  const int lead = !ANY ? 0
+                   : dh ? lead8(dh + row0 * a.lddh)
+                        : lead8(dxn + row0 * a.lddxn);
+  auto fetch = [&](int64_t row, int slot) {
+    if (row < a.M) {
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        const int c = (i * G + t) * 8 - lead;
+        if (c >= N) continue;
+        const uint32_t at = smem_u32(ring) + (((slot * PER + i) * U) * B + threadIdx.x) * 16;
+#pragma unroll
+        for (int u = 0; u < UX; ++u) {
+          if (dh) cp_async16(at + u * B * 16, reinterpret_cast<const uint4*>(xn + row * a.ldxn + c) + u);
+          if (dxn)
+            cp_async16(at + (UX + u) * B * 16,
+                       reinterpret_cast<const uint4*>(dxn + row * a.lddxn + c) + u);
+        }
+#pragma unroll
+        for (int u = 0; u < UO; ++u) {
+          if (o)
+            cp_async16(at + (2 * UX + u) * B * 16,
+                       reinterpret_cast<const uint4*>(o + row * a.ldo + c) + u);
+          if (dh)
+            cp_async16(at + (2 * UX + UO + u) * B * 16,
+                       reinterpret_cast<const uint4*>(dh + row * a.lddh + c) + u);
+        }
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  // vector i of a row's tensor that begins at unit `first`; zeros where there is none
+  auto take = [&](auto& r, bool there, int slot, int i, int first) {
+    constexpr int W = sizeof(r.w) / 16;
+    zero8(r);
+    if (!there) return;
+#pragma unroll
+    for (int u = 0; u < W; ++u) {
+      const uint4 q = ring[((slot * PER + i) * U + first + u) * B + threadIdx.x];
+      r.w[4 * u] = q.x;
+      r.w[4 * u + 1] = q.y;
+      r.w[4 * u + 2] = q.z;
+      r.w[4 * u + 3] = q.w;
+    }
+  };
+  // What a row's first and last vector hold of other rows is cleared in the ring, once a row.
+  auto clear = [&](auto r, int slot, int i, int first, int c) {
+    take(r, true, slot, i, first);
+    clear8(r, -c, N - c);
+#pragma unroll
+    for (int u = 0; u < (int)sizeof(r.w) / 16; ++u)
+      ring[((slot * PER + i) * U + first + u) * B + threadIdx.x] =
+          make_uint4(r.w[4 * u], r.w[4 * u + 1], r.w[4 * u + 2], r.w[4 * u + 3]);
+  };
+  auto clear_edges = [&](int slot) {
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int c = (i * G + t) * 8 - lead;
+      if (c >= N || (c >= 0 && c + 8 <= N)) continue;
+      clear(Raw8<XT>(), slot, i, 0, c);
+      clear(Raw8<XT>(), slot, i, UX, c);
+      clear(Raw8<OT>(), slot, i, 2 * UX, c);
+      clear(Raw8<OT>(), slot, i, 2 * UX + UO, c);
+    }
+  };
+  float dw[PER][8], dwp[PER][8], w_[kKeep ? PER : 1][8], wp_[kKeep ? PER : 1][8];
+#pragma unroll
+  for (int i = 0; i < PER; ++i)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) dw[i][j] = dwp[i][j] = 0.f;
+#pragma unroll
+  for (int k = 0; k < S - 1; ++k) fetch(row0 + k * step, k);
+  if constexpr (kKeep) {
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int c = (i * G + t) * 8 - lead;
+      if (c < N) {
+        weights8<ANY>(a.w, c, N, w_[i]);
+        weights8<ANY>(a.wp, c, N, wp_[i]);
+      }
+    }
+  }
+  auto weight = [&](const Weight& w, float (&kept)[kKeep ? PER : 1][8], int i, float (&v)[8]) {
+    if constexpr (kKeep) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = kept[i][j];
+    } else {
+      weights8<ANY>(w, (i * G + t) * 8 - lead, N, v);
+    }
+  };
+  int slot = 0, turn = 0;
+  for (int64_t row = row0; row < a.M; row += step) {
+    const float r = dh ? a.rstd[row] : 0.f, rp = a.post ? a.rstd_post[row] : 1.0f;
+    const float q = a.gate ? a.scale * a.gate[row] : a.scale;
+    fetch(row + (S - 1) * step, slot == 0 ? S - 1 : slot - 1);
+    cp_async_wait<S - 1>();
+    if (ANY) clear_edges(slot);
+    float c1 = 0.f;
+    if (dh) {
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        if ((i * G + t) * 8 - lead >= N) continue;
+        Raw8<XT> xr;
+        Raw8<OT> hr;
+        float w[8];
+        take(xr, true, slot, i, 0);
+        take(hr, true, slot, i, 2 * UX + UO);
+        weight(a.w, w_, i, w);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float y = at8(xr, j) * r, g = at8(hr, j);
+          dw[i][j] += g * y;
+          c1 += (g * w[j]) * y;
+        }
+      }
+      c1 = group_sum<G>(c1, sm[turn][0]) / (float)N;
+    }
+    float d[PER][8], dot = 0.f;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int c = (i * G + t) * 8 - lead;
+      if (c >= N) continue;
+      Raw8<XT> xr, dr;
+      Raw8<OT> hr, br;
+      float w[8], wp[8];
+      take(xr, dh != nullptr, slot, i, 0);
+      take(dr, dxn != nullptr, slot, i, UX);
+      take(br, o != nullptr, slot, i, 2 * UX);
+      take(hr, dh != nullptr, slot, i, 2 * UX + UO);
+      weight(a.w, w_, i, w);
+      weight(a.wp, wp_, i, wp);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        d[i][j] = at8(dr, j) + r * (at8(hr, j) * w[j] - (at8(xr, j) * r) * c1);
+        const float z = at8(br, j) * rp;
+        dwp[i][j] += (q * d[i][j]) * z;
+        dot += (d[i][j] * wp[j]) * z;
+      }
+      if (a.dx) {
+        round8(d[i], dr);
+        store8<ANY>(static_cast<XT*>(a.dx) + row * a.lddx + c, dr, -c, N - c);
+      }
+    }
+    if (o) {
+      if (a.post || a.d_gate) {
+        dot = group_sum<G>(dot, sm[turn][1]);
+        if (t == 0 && a.d_gate) a.d_gate[row] = a.scale * dot;
+      }
+      if (a.d_o) {
+        const float c2 = a.post ? dot / (float)N : 0.f, qr = q * rp;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+          const int c = (i * G + t) * 8 - lead;
+          if (c >= N) continue;
+          Raw8<OT> br;
+          float wp[8];
+          take(br, true, slot, i, 2 * UX);
+          weight(a.wp, wp_, i, wp);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) wp[j] = qr * (d[i][j] * wp[j] - (at8(br, j) * rp) * c2);
+          round8(wp, br);
+          store8<ANY>(static_cast<OT*>(a.d_o) + row * a.lddo + c, br, -c, N - c);
+        }
+      }
+    }
+    turn ^= 1;
+    if (++slot == S) slot = 0;
+  }
+  cp_async_wait<0>();
+  if (!a.part) return;
+  // a block's sums to its partials, or (a single block) the results
+  float* part = a.part + (int64_t)blockIdx.x * 2 * part_pitch(N);
+  auto put = [&](int c, float x, float y) {
+    if (gridDim.x > 1) {
+      part[c] = x;
+      part[part_pitch(N) + c] = y;
+    } else if (a.w_fp32) {
+      if (a.dw) static_cast<float*>(a.dw)[c] = x;
+      if (a.dwp) static_cast<float*>(a.dwp)[c] = y;
+    } else {
+      if (a.dw) static_cast<__nv_bfloat16*>(a.dw)[c] = __float2bfloat16_rn(x);
+      if (a.dwp) static_cast<__nv_bfloat16*>(a.dwp)[c] = __float2bfloat16_rn(y);
+    }
+  };
+  if constexpr (GROUPS > 1) {
+    // the block's groups, in order, through the columns of one shared row at a time
+    __shared__ float cols[2][G * PER * 8];
+    for (int g = 0; g < GROUPS; ++g) {
+      __syncthreads();
+      if ((int)threadIdx.x / G == g) {
+#pragma unroll
+        for (int i = 0; i < PER; ++i)
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const int c = (i * G + t) * 8 - lead + j;
+            if (c < 0 || c >= N) continue;
+            cols[0][c] = g == 0 ? dw[i][j] : cols[0][c] + dw[i][j];
+            cols[1][c] = g == 0 ? dwp[i][j] : cols[1][c] + dwp[i][j];
+          }
+      }
+    }
+    __syncthreads();
+    for (int c = threadIdx.x; c < N; c += B) put(c, cols[0][c], cols[1][c]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int at = (i * G + t) * 8;
+      if (at - lead >= N) continue;
+      if (gridDim.x > 1) {  // column c at c + lead: whole vectors
+        Raw8<float> r;
+        round8(dw[i], r);
+        store8<false>(part + at, r, 0, 8);
+        round8(dwp[i], r);
+        store8<false>(part + part_pitch(N) + at, r, 0, 8);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (at - lead + j >= 0 && at - lead + j < N) put(at - lead + j, dw[i][j], dwp[i][j]);
+      }
+    }
+  }
+}
+
+// dw (columns [0, N)) and dwp (columns [N, 2 N)) = sum of the blocks' partials in a fixed order; block
+// b's column c lies at c + (place + b pitch) % 8. Each of a block's 32 warps sums every 32nd partial of
+// 32 columns; the warps' sums are added as a tree.
 template <typename WT>
 __global__ void __launch_bounds__(1024) rn_colsum_kernel(const float* __restrict__ part,
                                                          int nparts, int64_t N,
                                                          WT* __restrict__ dw,
-                                                         WT* __restrict__ dwp) {
+                                                         WT* __restrict__ dwp, uint32_t place,
+                                                         uint32_t pitch) {
   MOE_GRIDDEP_ENTRY();
   __shared__ float sm[32][33];
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  const int64_t c = (int64_t)blockIdx.x * 32 + lane;
+  const int64_t c = (int64_t)blockIdx.x * 32 + lane, NP = part_pitch(N);
   float s = 0.f;
-  if (c < 2 * N)
-    for (int b = w; b < nparts; b += 32) s += part[(int64_t)b * 2 * N + c];
+  if (c < 2 * N) {
+    const float* at = part + (c < N ? c : c - N + NP);
+#pragma unroll 5
+    for (int b = w; b < nparts; b += 32)
+      s += at[(int64_t)b * 2 * NP + ((place + (uint32_t)b * pitch) & 7u)];
+  }
   sm[w][lane] = s;
   __syncthreads();
   s = sm[lane][w];
@@ -183,14 +500,119 @@ __global__ void __launch_bounds__(1024) rn_colsum_kernel(const float* __restrict
   const int64_t col = (int64_t)blockIdx.x * 32 + w;
   if (lane == 0 && col < 2 * N) {
     if (col < N) {
-      if (dw) dw[col] = from_f<WT>(s);
+      if (dw) dw[col] = from_float<WT>(s);
     } else if (dwp) {
-      dwp[col - N] = from_f<WT>(s);
+      dwp[col - N] = from_float<WT>(s);
     }
   }
 }
 
 constexpr int64_t kMaxParts = 480;  // rows of partial weight gradients
+
+// Whether every row of a tensor lies in its vectors as those of the first one given do.
+struct Places {
+  bool first = true, same = true, aligned = true;
+  int64_t place = 0, pitch = 0;
+  void add(const void* p, int64_t ld, int bytes) {
+    if (!p) return;
+    const int64_t at = (int64_t)(reinterpret_cast<uintptr_t>(p) / bytes & 7u);
+    if (first) {
+      place = at;
+      pitch = ld & 7;
+      first = false;
+    }
+    same = same && at == place && (ld & 7) == pitch;
+    aligned = aligned && at == 0 && (ld & 7) == 0;
+  }
+};
+
+template <typename XT, typename OT, bool ANY, int G, int PER>
+cudaError_t fwd_launch(const FwdArgs& a, cudaStream_t s) {
+  constexpr int B = G < 128 ? 128 : G, rows = B / G;
+  return launch_pdl(rn_fwd_kernel<XT, OT, G, PER, ANY>, (unsigned)((a.M + rows - 1) / rows), B, 0,
+                    s, 1, a);
+}
+template <typename XT, typename OT, bool ANY>
+cudaError_t fwd_typed(const FwdArgs& a, bool rows, cudaStream_t s) {
+  const int64_t C = rows ? a.N + (ANY ? 7 : 0) : INT64_MAX;
+  const bool many = a.M >= (int64_t)std::max(device_sms(), 1) * 2;
+  if (C <= 32 * 8) return fwd_launch<XT, OT, ANY, 32, 1>(a, s);
+  if (many) {
+    if (C <= 32 * 16) return fwd_launch<XT, OT, ANY, 32, 2>(a, s);
+    if (C <= 128 * 8) return fwd_launch<XT, OT, ANY, 128, 1>(a, s);
+    if (C <= 128 * 16) return fwd_launch<XT, OT, ANY, 128, 2>(a, s);
+    // a row just below a power of two needs seven columns more off the boundaries
+    if constexpr (ANY)
+      if (C <= 160 * 16) return fwd_launch<XT, OT, ANY, 160, 2>(a, s);
+    if (C <= 128 * 24) return fwd_launch<XT, OT, ANY, 128, 3>(a, s);
+    if (C <= 128 * 32) return fwd_launch<XT, OT, ANY, 128, 4>(a, s);
+    if constexpr (ANY)
+      if (C <= 160 * 32) return fwd_launch<XT, OT, ANY, 160, 4>(a, s);
+    if (C <= 256 * 32) return fwd_launch<XT, OT, ANY, 256, 4>(a, s);
+  }
+  if (C <= 256 * 8) return fwd_launch<XT, OT, ANY, 256, 1>(a, s);
+  if (C <= 512 * 8) return fwd_launch<XT, OT, ANY, 512, 1>(a, s);
+  if (C <= 1024 * 8) return fwd_launch<XT, OT, ANY, 1024, 1>(a, s);
+  if (C <= 1024 * 16) return fwd_launch<XT, OT, ANY, 1024, 2>(a, s);
+  const int grid = (int)std::min<int64_t>(a.M, (int64_t)std::max(device_sms(), 1) * 2);
+  return launch_pdl(rn_fwd_any_kernel<XT, OT>, grid, 1024, 0, s, 1, a);
+}
+
+// The partial sums that a backward kernel leaves.
+struct Parts {
+  int n = 0;
+  bool done = false;     // a single block has written the weights' gradients
+  bool shifted = false;  // block b's lie like row b in its vectors
+};
+// Rows of the ring: as many as leave room for two blocks an SM (where the registers hold only one: for
+// that one), up to four; at least one.
+template <typename XT, typename OT, int G, int PER>
+constexpr int ring_rows() {
+  constexpr int bytes = units<XT, OT>() * PER * block_of(G) * 16;
+  constexpr int n = (G >= 512 ? 200 : 112) * 1024 / bytes;
+  return n > 4 ? 4 : n < 1 ? 1 : n;
+}
+template <typename XT, typename OT, bool ANY, int G, int PER>
+cudaError_t bwd_launch(const BwdArgs& a, Parts& parts, cudaStream_t s) {
+  constexpr int B = block_of(G), GROUPS = B / G, S = ring_rows<XT, OT, G, PER>();
+  constexpr int smem = S * units<XT, OT>() * PER * B * 16;
+  static_assert(smem <= 200 * 1024, "shared memory of a block");
+  auto kern = rn_bwd_kernel<XT, OT, G, PER, S, ANY>;
+  cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kern), smem);
+  if (e != cudaSuccess) return e;
+  // as many blocks as fit at once, each a row of partials
+  static DeviceCache cache;
+  const int per_sm = std::max(1, cache.get(current_device(), [&] {
+    return blocks_per_sm(reinterpret_cast<const void*>(kern), B, smem);
+  }));
+  const int64_t fit = std::min<int64_t>((int64_t)std::max(device_sms(), 1) * per_sm, kMaxParts);
+  parts.n = (int)std::max<int64_t>(1, std::min<int64_t>((a.M + GROUPS - 1) / GROUPS, fit));
+  if (ANY && (int64_t)parts.n * GROUPS < a.M)  // rows of a group lie alike
+    parts.n = std::max(parts.n * GROUPS / 8 * 8, 8) / GROUPS;
+  parts.done = parts.n == 1;
+  parts.shifted = ANY && GROUPS == 1;
+  return launch_pdl(kern, parts.n, B, smem, s, 1, a);
+}
+template <typename XT, typename OT, bool ANY>
+cudaError_t bwd_typed(const BwdArgs& a, bool rows, Parts& parts, cudaStream_t s) {
+  const int64_t C = rows ? a.N + (ANY ? 7 : 0) : INT64_MAX;
+  if (C <= 32 * 8) return bwd_launch<XT, OT, ANY, 32, 1>(a, parts, s);
+  if (C <= 32 * 16) return bwd_launch<XT, OT, ANY, 32, 2>(a, parts, s);
+  if (C <= 128 * 8) return bwd_launch<XT, OT, ANY, 128, 1>(a, parts, s);
+  if (C <= 256 * 8) return bwd_launch<XT, OT, ANY, 256, 1>(a, parts, s);
+  // a row just below a power of two needs seven columns more off the boundaries
+  if constexpr (ANY)
+    if (C <= 288 * 8) return bwd_launch<XT, OT, ANY, 288, 1>(a, parts, s);
+  if (C <= 256 * 16) return bwd_launch<XT, OT, ANY, 256, 2>(a, parts, s);
+  if constexpr (ANY)
+    if (C <= 288 * 16) return bwd_launch<XT, OT, ANY, 288, 2>(a, parts, s);
+  if (C <= 512 * 16) return bwd_launch<XT, OT, ANY, 512, 2>(a, parts, s);
+  if constexpr (sizeof(OT) == 2)
+    if (C <= 512 * 32) return bwd_launch<XT, OT, ANY, 512, 4>(a, parts, s);
+  parts.n = (int)std::min<int64_t>(
+      a.M, std::min<int64_t>((int64_t)std::max(device_sms(), 1) * 2, kMaxParts));
+  return launch_pdl(rn_bwd_any_kernel<XT, OT>, parts.n, 1024, 0, s, 1, a);
+}
 
 bool on(const void* p, int bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
 int size_of(int32_t dtype) { return dtype == MOE_DT_FP32 ? 4 : 2; }
@@ -251,12 +673,21 @@ moe_status_t moe_residual_norm_fwd(const void* x, int64_t ldx, const void* o, in
     return fail(MOE_ERR_INVALID_ARG, "tensors must be aligned to their elements");
   if (!x) return fail(MOE_ERR_INVALID_ARG, "NULL tensor pointer");
   const int w32 = w_dtype == MOE_DT_FP32;
-  const FwdArgs a = {x, o, x_new, h, ldx, ldo, ldxn, ldh, M, N, {post_weight, w32}, {weight, w32},
-                     gate, rstd_post, rstd, scale, eps, post_norm != 0};
+  const FwdArgs a = {x, o, x_new, h, ldx, ldo, ldxn, ldh, M, N,
+                     {post_weight, (int16_t)w32, on(post_weight, 16)},
+                     {weight, (int16_t)w32, on(weight, 16)}, gate, rstd_post, rstd, scale, eps,
+                     post_norm != 0};
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const int grid = (int)std::min<int64_t>(M, (int64_t)std::max(device_sms(), 1) * 2);
+  Places at;
+  at.add(x, ldx, xb);
+  at.add(x_new, ldxn, xb);
+  at.add(o, ldo, ob);
+  at.add(h, ldh, ob);
+  const bool any = !(at.aligned && N % 8 == 0 && a.wp.vec && a.w.vec);
   const cudaError_t e = typed(x_dtype, o_dtype, [&](auto xt, auto ot) {
-    return launch_pdl(rn_fwd_any_kernel<decltype(xt), decltype(ot)>, grid, 1024, 0, s, 1, a);
+    using XT = decltype(xt);
+    using OT = decltype(ot);
+    return any ? fwd_typed<XT, OT, true>(a, at.same, s) : fwd_typed<XT, OT, false>(a, true, s);
   });
   count_launch(s, MOE_K_RESIDUAL_NORM_FWD);
   if (e != cudaSuccess) return cuda_fail(e, "residual norm forward launch");
@@ -268,7 +699,7 @@ size_t moe_residual_norm_workspace(int64_t M, int64_t N) {
     fail(MOE_ERR_INVALID_ARG, "M must be in [0, 2^31) and N in [1, 2^31)");
     return 0;
   }
-  return (size_t)std::max<int64_t>(1, std::min<int64_t>(M, kMaxParts)) * 2 * (N + 8) *
+  return (size_t)std::max<int64_t>(1, std::min<int64_t>(M, kMaxParts)) * 2 * part_pitch(N) *
          sizeof(float);
 }
 
@@ -319,28 +750,44 @@ moe_status_t moe_residual_norm_bwd(const void* dh, int64_t lddh, const void* dx_
   const int w32 = w_dtype == MOE_DT_FP32;
   float* part = weights ? static_cast<float*>(ws) : nullptr;
   const BwdArgs a = {dh, dx_new, x_new, o, dx, d_o, lddh, lddxn, ldxn, ldo, lddx, lddo, M, N,
-                     {post_weight, w32}, {weight, w32}, gate, rstd_post, rstd, d_gate, scale,
-                     post_norm != 0, part};
+                     {post_weight, (int16_t)w32, on(post_weight, 16)},
+                     {weight, (int16_t)w32, on(weight, 16)}, gate, rstd_post, rstd, d_gate, scale,
+                     post_norm != 0, part, d_weight, d_post_weight, w32};
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e = cudaSuccess;
-  const int nparts = (int)std::min<int64_t>(
-      M, std::min<int64_t>((int64_t)std::max(device_sms(), 1) * 2, kMaxParts));
+  Parts parts;
+  Places at;
   if (M > 0) {
+    if (dh) {
+      at.add(dh, lddh, ob);
+      at.add(x_new, ldxn, xb);
+    }
+    at.add(dx_new, lddxn, xb);
+    at.add(dx, lddx, xb);
+    at.add(o, ldo, ob);
+    at.add(d_o, lddo, ob);
+    const bool any = !(at.aligned && N % 8 == 0 && a.wp.vec && a.w.vec);
     e = typed(x_dtype, o_dtype, [&](auto xt, auto ot) {
-      return launch_pdl(rn_bwd_any_kernel<decltype(xt), decltype(ot)>, nparts, 1024, 0, s, 1, a);
+      using XT = decltype(xt);
+      using OT = decltype(ot);
+      return any ? bwd_typed<XT, OT, true>(a, at.same, parts, s)
+                 : bwd_typed<XT, OT, false>(a, true, parts, s);
     });
     count_launch(s, MOE_K_RESIDUAL_NORM_BWD);
     if (e != cudaSuccess) return cuda_fail(e, "residual norm backward launch");
   }  // no rows: no partials, the sums are zero
-  if (weights) {
+  if (weights && !parts.done) {
     const unsigned grid = (unsigned)((2 * N + 31) / 32);
+    const uint32_t place = parts.shifted ? (uint32_t)at.place : 0u;
+    const uint32_t pitch = parts.shifted ? (uint32_t)at.pitch : 0u;
     if (w32)
-      e = launch_pdl(rn_colsum_kernel<float>, grid, 1024, 0, s, 1, (const float*)part, nparts, N,
-                     static_cast<float*>(d_weight), static_cast<float*>(d_post_weight));
+      e = launch_pdl(rn_colsum_kernel<float>, grid, 1024, 0, s, 1, (const float*)part, parts.n, N,
+                     static_cast<float*>(d_weight), static_cast<float*>(d_post_weight), place,
+                     pitch);
     else
       e = launch_pdl(rn_colsum_kernel<__nv_bfloat16>, grid, 1024, 0, s, 1, (const float*)part,
-                     nparts, N, static_cast<__nv_bfloat16*>(d_weight),
-                     static_cast<__nv_bfloat16*>(d_post_weight));
+                     parts.n, N, static_cast<__nv_bfloat16*>(d_weight),
+                     static_cast<__nv_bfloat16*>(d_post_weight), place, pitch);
     count_launch(s, MOE_K_RESIDUAL_NORM_REDUCE);
     if (e != cudaSuccess) return cuda_fail(e, "residual norm reduction launch");
   }
