@@ -112,6 +112,55 @@ def test_logits_that_are_not_finite(lib, score, renorm):
     assert ids.cpu().tolist() == [[2, 1, 0, 3]] * 6
 
 
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("E,groups,of", [(256, 8, 4), (256, 1, 1), (64, 4, 2), (40, 1, 1)])
+def test_biases_of_any_size(lib, score, E, groups, of):
+    """Biases far beyond the scores, infinite ones among them, and logits so near to one another that
+    most choices are close: fp32 sums, of which many are equal, and the lower index then."""
+    gen = torch.Generator().manual_seed(E)
+    x = torch.randn(200, E, generator=gen).cuda()
+    x[50:100] *= 1e-6
+    x[100:150] *= 30
+    x[150:] = x[150:].round()
+    inf = float("inf")
+    for scale in (1e-7, 1.0, 100.0, 1e6):
+        bias = (torch.randn(E, generator=gen) * scale).cuda()
+        for special in (False, True):
+            if special:
+                bias[3], bias[7], bias[8], bias[20] = inf, -inf, inf, float("nan")
+            for top in ((1, 2) if groups > 1 else (1,)):
+                plan = g.RouterTopK(E, 8, 200, score=score, n_group=groups, topk_group=of,
+                                    group_top=top)
+                ids = plan.forward(x, bias)[0]
+                assert torch.equal(ids.long(), by_steps(x, bias, score, 8, groups, of, top))
+
+
+def by_steps(x, bias, score, k, groups, of, top):
+    """The definition in single fp32 operations of torch, on the GPU."""
+    T, E = x.shape
+    if score == "sigmoid":
+        s = torch.reciprocal(1.0 + torch.exp(-x))
+    else:
+        e = torch.exp(x - x.amax(1, keepdim=True))
+        total = torch.nn.functional.pad(e, (0, (1 << (E - 1).bit_length()) - E))
+        while total.shape[1] > 1:
+            total = total[:, 0::2] + total[:, 1::2]
+        s = e * torch.reciprocal(total)
+    v = s + torch.where(bias.isnan(), -torch.inf, bias)
+    if groups > 1:
+        best = v.view(T, groups, -1).sort(dim=2, descending=True).values[:, :, :top].sum(2)
+        best = torch.where(best.isnan(), -torch.inf, best)
+        kept = best.sort(dim=1, descending=True, stable=True).indices[:, :of]
+        keep = torch.zeros(T, groups, dtype=torch.bool, device="cuda").scatter_(1, kept, True)
+        keep = keep.repeat_interleave(E // groups, 1)
+        # an expert of a kept group at -inf comes before those of other groups
+        order = torch.where(keep, v, -torch.inf).sort(dim=1, descending=True, stable=True).indices
+        inside = keep.gather(1, order)
+        order = order.gather(1, (~inside).int().sort(dim=1, stable=True).indices)
+        return order[:, :k]
+    return v.sort(dim=1, descending=True, stable=True).indices[:, :k]
+
+
 @pytest.mark.parametrize("shape", SHAPES)
 @pytest.mark.parametrize("score", ["sigmoid", "softmax"])
 @pytest.mark.parametrize("renorm", [True, False])
