@@ -270,8 +270,9 @@ MOE_DEVICE void sort4(float& a, float& b, float& c, float& d) {
   order_pair(b, d);
   order_pair(b, c);
 }
-constexpr int list_of(int VPL) { return VPL < 4 ? VPL : 4; }
-// A lane's largest values, descending: all of them, or the first four of eight.
+constexpr int list_of(int VPL) { return VPL < 5 ? VPL : 5; }
+// A lane's largest values, descending: all of them, or the first five of eight (odd-even merge, Batcher
+// 1968).
 template <int VPL>
 MOE_DEVICE void top_values(const float (&v)[VPL], float (&l)[list_of(VPL)]) {
   if constexpr (VPL <= 4) {
@@ -280,15 +281,20 @@ MOE_DEVICE void top_values(const float (&v)[VPL], float (&l)[list_of(VPL)]) {
     if constexpr (VPL == 2) order_pair(l[0], l[1]);
     if constexpr (VPL == 4) sort4(l[0], l[1], l[2], l[3]);
   } else {
-    float a[4] = {v[0], v[1], v[2], v[3]}, b[4] = {v[4], v[5], v[6], v[7]};
-    sort4(a[0], a[1], a[2], a[3]);
-    sort4(b[0], b[1], b[2], b[3]);
+    float a[8];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) l[j] = fmaxf(a[j], b[3 - j]);  // rises, then falls
-    order_pair(l[0], l[2]);
-    order_pair(l[1], l[3]);
-    order_pair(l[0], l[1]);
-    order_pair(l[2], l[3]);
+    for (int j = 0; j < 8; ++j) a[j] = v[j];
+    sort4(a[0], a[1], a[2], a[3]);
+    sort4(a[4], a[5], a[6], a[7]);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) order_pair(a[j], a[j + 4]);
+    order_pair(a[2], a[4]);
+    order_pair(a[3], a[5]);
+    order_pair(a[1], a[2]);
+    order_pair(a[3], a[4]);
+    order_pair(a[5], a[6]);
+#pragma unroll
+    for (int j = 0; j < list_of(VPL); ++j) l[j] = a[j];
   }
 }
 
@@ -307,12 +313,12 @@ MOE_DEVICE float weight_of(float l, float s, bool live, const Choice& c) {
   float w;
   if (c.score == MOE_SCORE_SIGMOID) {
     w = live ? sigmoid(l) : 0.f;
-    if (c.renorm) w = w / (sum8(w) + kWeightEps);
+    if (c.renorm) w = __fdividef(w, sum8(w) + kWeightEps);
   } else if (c.renorm) {
     if (!live) l = -INFINITY;
     const float m = max8(l);
     w = live ? (l == m ? 1.0f : expf(l - m)) : 0.f;
-    w = w / sum8(w);
+    w = __fdividef(w, sum8(w));
   } else {
     w = s;
   }
@@ -322,13 +328,14 @@ MOE_DEVICE float weight_of(float l, float s, bool live, const Choice& c) {
 // What decides the choice: the logits themselves; sigmoids (and biases), taken approximately; softmax
 // probabilities.
 enum Kind { kLogits = 0, kSigmoid = 1, kSoftmax = 2 };
+constexpr float kFar = 3e38f;  // an infinite bias, and what lies past E, among approximate values
 
-// GROUPS: the experts' groups are whole lanes, a power of two of them each. The choice goes by sorted
+// GROUPS: the experts' groups are whole lanes, a power of two of them each. k <= KMAX. The choice goes by sorted
 // lists, one a lane, whose heads the warp's maximum takes one by one. kSigmoid: 4 instructions a score
 // against some 17, and three bits of a value hold its place in the lane. A token with two deciding values
 // too near to tell, with an infinite value among its k, or with a lane that holds equal ones or more than
 // its list, is chosen anew by definition.
-template <int VPL, bool GROUPS, int KIND, typename LT>
+template <int VPL, bool GROUPS, int KIND, int KMAX, typename LT>
 __global__ void __launch_bounds__(kThreads, 4) router_topk_kernel(
     const LT* __restrict__ logits, int64_t ld, const float* __restrict__ bias,
     const uint8_t* __restrict__ mask, int T, const __grid_constant__ Choice c, int vec,
@@ -352,6 +359,7 @@ __global__ void __launch_bounds__(kThreads, 4) router_topk_kernel(
     const int e = lane * VPL + j;
     b[j] = e >= E ? -INFINITY : KIND != kLogits && bias ? fmaxf(bias[e], -INFINITY) : 0.f;
     if (fabsf(b[j]) < INFINITY) most = fmaxf(most, fabsf(b[j]));
+    if (KIND == kSigmoid) b[j] = fmaxf(fminf(b[j], kFar), -kFar);  // finite, for the place's bits
   }
   // kSigmoid: a value is off by 2^-21 in its score, by a step of the sum with its bias (2^-23 of it) and
   // by the place in its last three bits (2^-20 of it); a sum of two by twice that and a step of its own
@@ -381,8 +389,7 @@ __global__ void __launch_bounds__(kThreads, 4) router_topk_kernel(
 #pragma unroll
       for (int j = 0; j < VPL; ++j) {
         const float y = sigmoid_near(x[j]) + b[j];
-        v[j] = VPL == 1 || fabsf(y) == INFINITY
-                   ? y : __uint_as_float((__float_as_uint(y) & ~(uint32_t)(VPL - 1)) | j);
+        v[j] = __uint_as_float((__float_as_uint(y) & ~(uint32_t)(VPL - 1)) | j);
       }
     } else {
 #pragma unroll
@@ -421,7 +428,8 @@ __global__ void __launch_bounds__(kThreads, 4) router_topk_kernel(
 #pragma unroll 4
       for (int i = 0; i < c.n_group; ++i) {
         const float other = __shfl_sync(kAll, best, i * group_lanes);
-        before += other > best || (other == best && i < group);
+        // equal approximate values are too near to tell
+        before += other > best || (KIND != kSigmoid && other == best && i < group);
       }
       keep = before < c.topk_group && group < c.n_group;
       if (KIND == kSigmoid) {
@@ -440,37 +448,36 @@ __global__ void __launch_bounds__(kThreads, 4) router_topk_kernel(
 #pragma unroll
       for (int j = 0; j < LIST; ++j) list[j] = -INFINITY;
     }
-    float taken = -INFINITY;  // lane j: the j-th largest value, and the lane that held it
-    uint32_t holder = 1u;
+    // round j's holder leaves the value and its lane
+    float2* found = reinterpret_cast<float2*>(room[warp][0]);
     int pops = 0;
 #pragma unroll
-    for (int j = 0; j < 9; ++j) {
-      if (j >= (KIND == kSigmoid ? k + 1 : k)) break;
+    for (int j = 0; j < KMAX + (KIND == kSigmoid); ++j) {
       const float m = warp_max(list[0]);
       const uint32_t who = __ballot_sync(kAll, list[0] == m);
-      const uint32_t first = who & (0u - who);
-      if (lane == j) {
-        taken = m;
-        holder = first;
-      }
-      if (first == lane_bit) {
+      if ((who & (0u - who)) == lane_bit) {
+        found[j] = make_float2(m, __int_as_float(lane));
 #pragma unroll
         for (int i = 0; i + 1 < LIST; ++i) list[i] = list[i + 1];
         list[LIST - 1] = -INFINITY;
         if (VPL > LIST) ++pops;
       }
     }
-    const int from = __ffs(holder) - 1;
+    __syncwarp();
+    const float2 mine_found = found[lane <= KMAX ? lane : 0];  // lane j: round j's
+    const float taken = mine_found.x;
+    const int from = __float_as_int(mine_found.y) & 31;
+    __syncwarp();
     const float after = __shfl_down_sync(kAll, taken, 1);
-    const uint32_t after_holder = __shfl_down_sync(kAll, holder, 1);
+    const int after_from = __shfl_down_sync(kAll, from, 1);
     again |= VPL > LIST && pops >= LIST;
-    again |= lane < k && (KIND == kSigmoid ? fabsf(taken) == INFINITY : taken == -INFINITY);
+    again |= lane < k && (KIND == kSigmoid ? !(fabsf(taken) < 0.9f * kFar) : taken == -INFINITY);
     int mine = 0;
     if constexpr (KIND == kSigmoid) {
       again |= lane < k && near(taken, after, eps);
       mine = from * VPL + (int)(__float_as_uint(taken) & (uint32_t)(VPL - 1));
     } else {
-      again |= lane + 1 < k && taken == after && holder == after_holder;
+      again |= lane + 1 < k && taken == after && from == after_from;
 #pragma unroll
       for (int j = VPL - 1; j >= 0; --j) {
         const float other = __shfl_sync(kAll, v[j], from);
@@ -862,6 +869,11 @@ __global__ void __launch_bounds__(kThreads) router_topk_grad_small_kernel(
   }
 }
 
+__global__ void __launch_bounds__(256) zero_counts_kernel(int32_t* counts, int E) {
+  MOE_GRIDDEP_ENTRY();
+  if ((int)threadIdx.x < E) counts[threadIdx.x] = 0;
+}
+
 template <int N>
 using I = std::integral_constant<int, N>;
 // Calls fn with the experts a lane and a value of the logits' type.
@@ -943,11 +955,14 @@ moe_status_t moe_router_topk_fwd(const void* logits, int64_t ld_logits, int32_t 
     return fail(MOE_ERR_INVALID_ARG, "tensors must be aligned to their elements");
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const bool small = E <= kSmall && n_group == 1;
-  const int grid = topk_blocks(T, small ? kThreads : kWarps, 8);
+  const int grid = topk_blocks(T, small ? kThreads : kWarps, 4);  // as many as fit at once
   cudaError_t e = cudaSuccess;
   if (T == 0 || grid > 1) {  // a single block writes the counts, several add to them
-    if (counts) e = cudaMemsetAsync(counts, 0, sizeof(int32_t) * E, s);
-    if (e != cudaSuccess) return cuda_fail(e, "memset counts");
+    if (counts) {
+      e = launch_pdl(zero_counts_kernel, 1, 256, 0, s, 1, counts, E);
+      count_launch(s, MOE_K_ROUTER_TOPK);
+      if (e != cudaSuccess) return cuda_fail(e, "router counts launch");
+    }
     if (T == 0) return MOE_OK;
   }
   const Choice c = {E, k, score, n_group, topk_group, group_top, renorm != 0, scale};
@@ -972,15 +987,17 @@ moe_status_t moe_router_topk_fwd(const void* logits, int64_t ld_logits, int32_t 
     with_shape(E, logits_dtype, [&](auto v, auto lt) {
       using LT = decltype(lt);
       constexpr int V = v.value;
-      auto kind = [&](auto g) {
+      auto kind = [&](auto g, auto kmax) {
         constexpr bool G = g.value;
+        constexpr int K = kmax.value;
         if (score == MOE_SCORE_SOFTMAX && (by_score || !renorm))
-          launch(router_topk_kernel<V, G, kSoftmax, LT>, lt);
-        else if (by_score) launch(router_topk_kernel<V, G, kSigmoid, LT>, lt);
-        else launch(router_topk_kernel<V, G, kLogits, LT>, lt);
+          launch(router_topk_kernel<V, G, kSoftmax, K, LT>, lt);
+        else if (by_score) launch(router_topk_kernel<V, G, kSigmoid, K, LT>, lt);
+        else launch(router_topk_kernel<V, G, kLogits, K, LT>, lt);
       };
-      if (n_group > 1) kind(std::true_type());
-      else kind(std::false_type());
+      if (n_group > 1) kind(std::true_type(), I<8>());
+      else if (k <= 4) kind(std::false_type(), I<4>());
+      else kind(std::false_type(), I<8>());
     });
   }
   count_launch(s, MOE_K_ROUTER_TOPK);
