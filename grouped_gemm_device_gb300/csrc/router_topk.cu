@@ -305,7 +305,7 @@ MOE_DEVICE float sigmoid_near(float x) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
   return r;
 }
-// Whether a and b, a >= b, may be in another order than they seem, each being off by less than eps / 2.
+// Whether a and b, a >= b, may be in another order than they seem, each being off by eps / 2 at most.
 MOE_DEVICE bool near(float a, float b, float eps) { return !(a - b > eps) && b != -INFINITY; }
 
 // A token's weights, one a lane below k (live): l the expert's logit, s its score (softmax alone).
@@ -361,9 +361,10 @@ __global__ void __launch_bounds__(kThreads, 4) router_topk_kernel(
     if (fabsf(b[j]) < INFINITY) most = fmaxf(most, fabsf(b[j]));
     if (KIND == kSigmoid) b[j] = fmaxf(fminf(b[j], kFar), -kFar);  // finite, for the place's bits
   }
-  // kSigmoid: a value is off by 2^-21 in its score, by a step of the sum with its bias (2^-23 of it) and
-  // by the place in its last three bits (2^-20 of it); a sum of two by twice that and a step of its own
-  const float eps = 0x1p-18f * (2.0f + warp_max(most));
+  // kSigmoid: a value is off by 2^-21 in its score, by a step in the sum with its bias and by up to seven
+  // in its last three bits, 2^-20 of it together; a sum of two (of up to 1 + the largest bias) by twice
+  // that and a step of its own
+  const float eps_group = 0x1p-19f + 0x1.2p-18f * (1.0f + warp_max(most));
   const uint32_t lane_bit = 1u << lane;
   const int64_t step = (int64_t)gridDim.x * kWarps;
   int64_t t = (int64_t)blockIdx.x * kWarps + warp;
@@ -435,7 +436,7 @@ __global__ void __launch_bounds__(kThreads, 4) router_topk_kernel(
       if (KIND == kSigmoid) {
         const float in = -warp_max(keep ? -best : -INFINITY);
         const float out = warp_max(keep || group >= c.n_group ? -INFINITY : best);
-        again = near(in, out, 2 * eps);
+        again = near(in, out, eps_group);
       }
     }
     if (KIND == kSoftmax && !bias) {  // the logits' order
@@ -474,7 +475,8 @@ __global__ void __launch_bounds__(kThreads, 4) router_topk_kernel(
     again |= lane < k && (KIND == kSigmoid ? !(fabsf(taken) < 0.9f * kFar) : taken == -INFINITY);
     int mine = 0;
     if constexpr (KIND == kSigmoid) {
-      again |= lane < k && near(taken, after, eps);
+      again |= lane < k &&
+               near(taken, after, 0x1p-20f + 0x1p-19f * fmaxf(fabsf(taken), fabsf(after)));
       mine = from * VPL + (int)(__float_as_uint(taken) & (uint32_t)(VPL - 1));
     } else {
       again |= lane + 1 < k && taken == after && from == after_from;
