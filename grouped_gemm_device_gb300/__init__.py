@@ -983,6 +983,7 @@ class ResidualNorm:
                             (self.dtype, self.branch_dtype, self.weight_dtype))
         self.N, self.M_max = N, M_max
         self.post_norm, self.scale, self.eps = bool(post_norm), float(scale), float(eps)
+        self._post = int(self.post_norm)
         self.x_new = None
         self.h = torch.empty(M_max, N, dtype=self.branch_dtype, device=dev)
         self.rstd = torch.empty(M_max, dtype=torch.float32, device=dev)
@@ -991,6 +992,7 @@ class ResidualNorm:
         # rows whose rstd and rstd_post the last forward left
         self.M = self.M_post = None
         self._lib = _load_calls()
+        self._out = self.h.data_ptr(), self.rstd_post.data_ptr(), self.rstd.data_ptr()
 
     def _rows(self, x, name, dtype, M=None):
         if x.dim() != 2 or x.shape[0] > self.M_max:
@@ -1006,7 +1008,6 @@ class ResidualNorm:
 
     def _branch(self, o, post_weight, gate, M):
         """Checks what belongs to a branch; its post norm (0 or 1)."""
-        import torch
         if o is None:
             if post_weight is not None or gate is not None:
                 raise ValueError("post_weight and gate need a branch o")
@@ -1014,30 +1015,36 @@ class ResidualNorm:
         self._rows(o, "o", self.branch_dtype, M)
         self._weight(post_weight, "post_weight")
         if gate is not None:
-            _expect(gate, "gate", torch.float32, (M,), self._gpu)
-        return int(self.post_norm)
+            _expect(gate, "gate", self.rstd.dtype, (M,), self._gpu)
+        return self._post
 
     def forward(self, x, o=None, weight=None, post_weight=None, gate=None, norm=True, stream=None):
         """x [M, N] of the stream, o [M, N] the branch that joins it (None: x_new is x), gate fp32
         [M]; norm=False: no h (the last block's sum). Returns (x_new [M, N], h [M, N] or None)."""
-        import torch
         M = self._rows(x, "x", self.dtype)
         post = self._branch(o, post_weight, gate, M)
         self._weight(weight, "weight")
         if not norm and (weight is not None or o is None):
             raise ValueError("without a norm there is a branch and no weight")
-        if o is not None and self.x_new is None:
-            # what the current stream has given back may still be in use there
-            with _torch_on(self._gpu, stream):
-                self.x_new = torch.empty(self.M_max, self.N, dtype=self.dtype, device=self.device)
-        new = None if o is None else self.x_new
+        h, rstd_post, rstd = self._out
+        if o is None:
+            branch = None, 0
+            new = None
+        else:
+            branch = o.data_ptr(), _ld(o)
+            if self.x_new is None:
+                import torch
+                # what the current stream has given back may still be in use there
+                with _torch_on(self._gpu, stream):
+                    self.x_new = torch.empty(self.M_max, self.N, dtype=self.dtype,
+                                             device=self.device)
+            new = self.x_new.data_ptr()
         _check(self._lib.moe_residual_norm_fwd(
-            x.data_ptr(), _ld(x), _ptr(o), 0 if o is None else _ld(o), _ptr(post_weight),
-            _ptr(gate), _ptr(weight), _ptr(new), self.N, self.h.data_ptr() if norm else None,
-            self.N, self.rstd_post.data_ptr(), self.rstd.data_ptr(), M, self.N, self.scale, post,
+            x.data_ptr(), _ld(x), *branch, _ptr(post_weight), _ptr(gate), _ptr(weight), new,
+            self.N, h if norm else None, self.N, rstd_post, rstd, M, self.N, self.scale, post,
             self.eps, *self._codes, _call_stream(self._gpu, stream)))
         self.M, self.M_post = (M if norm else None), (M if post else None)
-        return x if o is None else _first(new, M), _first(self.h, M) if norm else None
+        return x if o is None else _first(self.x_new, M), _first(self.h, M) if norm else None
 
     def _stats(self, given, name, own, M, rows):
         if given is not None:
@@ -1216,6 +1223,7 @@ class AdamW:
             self.m_exp, self.v_exp = states(torch.uint8, 256), states(torch.uint8, 256)
         self._counters = torch.zeros(2, dtype=torch.int64, device=dev)
         self.steps = self._counters[:1]
+        self._counters_at, self._f32 = self._counters.data_ptr(), torch.float32
         self._list = (AdamWTensor * n)(*[
             AdamWTensor(p.data_ptr(), _ptr(w), g.data_ptr(), m.data_ptr(), v.data_ptr(), _ptr(me),
                         _ptr(ve), p.numel(), _dtype_code(p.dtype), _dtype_code(g.dtype), d, 0)
@@ -1235,22 +1243,21 @@ class AdamW:
         """One step. norm: GradClip's (fp32 [1] on the GPU): the gradients are multiplied by
         min(1, max_norm / (norm + 1e-6)), and a norm that is not finite skips the step. lr: another
         learning rate than the optimiser's, for this step."""
-        import torch
         lr = self.lr if lr is None else lr
         lr_dev = None
-        if isinstance(lr, torch.Tensor):
-            lr_dev, lr = _expect(lr, "lr", torch.float32, lr.shape, self._gpu), 0.0
+        if not isinstance(lr, (int, float)):
+            lr_dev, lr = _expect(lr, "lr", self._f32, lr.shape, self._gpu), 0.0
             if lr_dev.numel() != 1:
                 raise ValueError("lr must hold one value")
         if norm is not None:
-            _expect(norm, "norm", torch.float32, norm.shape, self._gpu)
+            _expect(norm, "norm", self._f32, norm.shape, self._gpu)
             if norm.numel() != 1:
                 raise ValueError("norm must hold one value")
         elif max_norm != math.inf:
             raise ValueError("max_norm needs the gradients' norm")
         _check(self._lib.moe_adamw_step(
             self.n, self._at, self.state_bits, lr, _ptr(lr_dev), *self.betas, self.eps,
-            _ptr(norm), max_norm, self.seed, self._counters.data_ptr(),
+            _ptr(norm), max_norm, self.seed, self._counters_at,
             _call_stream(self._gpu, stream)))
 
     def moments(self, stream=None):

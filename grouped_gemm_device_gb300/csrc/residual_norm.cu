@@ -229,20 +229,30 @@ constexpr int units() {
   return (int)(sizeof(XT) + sizeof(OT));
 }
 
+// The weights of the elements that wrap: those of columns c .. N - 1 come first.
+MOE_DEVICE void wrap_weights(const Weight& w, int N, int c, float (&v)[8]) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    if (c + j < N) v[j] = weight_at(w, c + j);
+}
+
 // A group of G threads walks rows that lie alike in their vectors; a thread owns the same 8 PER columns
 // of every row and keeps their sums of the weights' gradients in registers until the end. Each thread
 // copies its own columns of the next S - 1 rows into a ring in shared memory (cp.async), so that no
-// barrier is spent on the copies. N (ANY: N + 7) <= 8 G PER, and the groups' number a multiple of 8 where
-// ANY and a group takes more than one row.
+// barrier is spent on the copies. N <= 8 G PER, and the groups' number a multiple of 8 where ANY and a
+// group takes more than one row. ANY: a row may reach into one vector more than the group's; its elements
+// there are fewer than those that the first vector's `lead` leaves free, and wrap around to them.
 template <typename XT, typename OT, int G, int PER, int S, bool ANY>
-__global__ void __launch_bounds__(block_of(G), G == 288 ? 2 : 1) rn_bwd_kernel(const BwdArgs a) {
+__global__ void __launch_bounds__(block_of(G), ANY && G == 256 ? 2 : 1) rn_bwd_kernel(const BwdArgs a) {
   MOE_GRIDDEP_ENTRY();
   constexpr int B = block_of(G), GROUPS = B / G, U = units<XT, OT>();
   constexpr int UX = sizeof(XT) / 2, UO = sizeof(OT) / 2;
   // few enough columns a thread to hold both weights beside the sums
   constexpr bool kKeep = PER <= 2 && G <= 512;
   __shared__ float sm[2][2][32];
-  extern __shared__ uint4 ring[];  // [S][PER][U][B]
+  extern __shared__ uint4 ring[];  // [S][PER][U][B]; ANY: [S][GROUPS][U] for the vectors that wrap
+  constexpr int CAP = 8 * G * PER;
+  uint4* spare = ring + S * PER * U * B + threadIdx.x / G * U;
   const int t = threadIdx.x % G, N = (int)a.N;
   const int64_t row0 = (int64_t)blockIdx.x * GROUPS + threadIdx.x / G;
   const int64_t step = (int64_t)gridDim.x * GROUPS;
@@ -253,30 +263,35 @@ __global__ void __launch_bounds__(block_of(G), G == 288 ? 2 : 1) rn_bwd_kernel(c
   const int lead = !ANY ? 0
                    : dh ? lead8(dh + row0 * a.lddh)
                         : lead8(dxn + row0 * a.lddxn);
+  const bool wraps = ANY && t == 0 && CAP - lead < N;
+  // the vector of columns c .. c + 7 to units `pitch` bytes apart
+  auto copy = [&](int64_t row, int c, uint32_t at, uint32_t pitch) {
+#pragma unroll
+    for (int u = 0; u < UX; ++u) {
+      if (dh) cp_async16(at + u * pitch, reinterpret_cast<const uint4*>(xn + row * a.ldxn + c) + u);
+      if (dxn)
+        cp_async16(at + (UX + u) * pitch,
+                   reinterpret_cast<const uint4*>(dxn + row * a.lddxn + c) + u);
+    }
+#pragma unroll
+    for (int u = 0; u < UO; ++u) {
+      if (o)
+        cp_async16(at + (2 * UX + u) * pitch,
+                   reinterpret_cast<const uint4*>(o + row * a.ldo + c) + u);
+      if (dh)
+        cp_async16(at + (2 * UX + UO + u) * pitch,
+                   reinterpret_cast<const uint4*>(dh + row * a.lddh + c) + u);
+    }
+  };
   auto fetch = [&](int64_t row, int slot) {
     if (row < a.M) {
 #pragma unroll
       for (int i = 0; i < PER; ++i) {
         const int c = (i * G + t) * 8 - lead;
-        if (c >= N) continue;
-        const uint32_t at = smem_u32(ring) + (((slot * PER + i) * U) * B + threadIdx.x) * 16;
-#pragma unroll
-        for (int u = 0; u < UX; ++u) {
-          if (dh) cp_async16(at + u * B * 16, reinterpret_cast<const uint4*>(xn + row * a.ldxn + c) + u);
-          if (dxn)
-            cp_async16(at + (UX + u) * B * 16,
-                       reinterpret_cast<const uint4*>(dxn + row * a.lddxn + c) + u);
-        }
-#pragma unroll
-        for (int u = 0; u < UO; ++u) {
-          if (o)
-            cp_async16(at + (2 * UX + u) * B * 16,
-                       reinterpret_cast<const uint4*>(o + row * a.ldo + c) + u);
-          if (dh)
-            cp_async16(at + (2 * UX + UO + u) * B * 16,
-                       reinterpret_cast<const uint4*>(dh + row * a.lddh + c) + u);
-        }
+        if (c < N)
+          copy(row, c, smem_u32(ring) + (((slot * PER + i) * U) * B + threadIdx.x) * 16, B * 16);
       }
+      if (wraps) copy(row, CAP - lead, smem_u32(spare + slot * GROUPS * U), 16);
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
@@ -294,10 +309,25 @@ __global__ void __launch_bounds__(block_of(G), G == 288 ? 2 : 1) rn_bwd_kernel(c
       r.w[4 * u + 3] = q.w;
     }
   };
-  // What a row's first and last vector hold of other rows is cleared in the ring, once a row.
+  // What a row's first and last vector hold of other rows is cleared in the ring, once a row, and what
+  // wraps put there.
   auto clear = [&](auto r, int slot, int i, int first, int c) {
     take(r, true, slot, i, first);
     clear8(r, -c, N - c);
+    if (wraps && i == 0) {
+      auto more = r;
+#pragma unroll
+      for (int u = 0; u < (int)sizeof(r.w) / 16; ++u) {
+        const uint4 q = spare[slot * GROUPS * U + first + u];
+        more.w[4 * u] = q.x;
+        more.w[4 * u + 1] = q.y;
+        more.w[4 * u + 2] = q.z;
+        more.w[4 * u + 3] = q.w;
+      }
+      clear8(more, 0, N - (CAP - lead));  // fewer than lead are left
+#pragma unroll
+      for (int k = 0; k < (int)sizeof(r.w) / 4; ++k) r.w[k] |= more.w[k];
+    }
 #pragma unroll
     for (int u = 0; u < (int)sizeof(r.w) / 16; ++u)
       ring[((slot * PER + i) * U + first + u) * B + threadIdx.x] =
@@ -328,6 +358,10 @@ __global__ void __launch_bounds__(block_of(G), G == 288 ? 2 : 1) rn_bwd_kernel(c
       if (c < N) {
         weights8<ANY>(a.w, c, N, w_[i]);
         weights8<ANY>(a.wp, c, N, wp_[i]);
+        if (wraps && i == 0) {
+          wrap_weights(a.w, N, CAP - lead, w_[i]);
+          wrap_weights(a.wp, N, CAP - lead, wp_[i]);
+        }
       }
     }
   }
@@ -337,6 +371,7 @@ __global__ void __launch_bounds__(block_of(G), G == 288 ? 2 : 1) rn_bwd_kernel(c
       for (int j = 0; j < 8; ++j) v[j] = kept[i][j];
     } else {
       weights8<ANY>(w, (i * G + t) * 8 - lead, N, v);
+      if (wraps && i == 0) wrap_weights(w, N, CAP - lead, v);
     }
   };
   int slot = 0, turn = 0;
@@ -390,6 +425,8 @@ __global__ void __launch_bounds__(block_of(G), G == 288 ? 2 : 1) rn_bwd_kernel(c
       if (a.dx) {
         round8(d[i], dr);
         store8<ANY>(static_cast<XT*>(a.dx) + row * a.lddx + c, dr, -c, N - c);
+        if (wraps && i == 0)
+          store8<ANY>(static_cast<XT*>(a.dx) + row * a.lddx + CAP - lead, dr, 0, N - CAP + lead);
       }
     }
     if (o) {
@@ -411,6 +448,9 @@ __global__ void __launch_bounds__(block_of(G), G == 288 ? 2 : 1) rn_bwd_kernel(c
           for (int j = 0; j < 8; ++j) wp[j] = qr * (d[i][j] * wp[j] - (at8(br, j) * rp) * c2);
           round8(wp, br);
           store8<ANY>(static_cast<OT*>(a.d_o) + row * a.lddo + c, br, -c, N - c);
+          if (wraps && i == 0)
+            store8<ANY>(static_cast<OT*>(a.d_o) + row * a.lddo + CAP - lead, br, 0,
+                        N - CAP + lead);
         }
       }
     }
@@ -419,6 +459,12 @@ __global__ void __launch_bounds__(block_of(G), G == 288 ? 2 : 1) rn_bwd_kernel(c
   }
   cp_async_wait<0>();
   if (!a.part) return;
+  // the column of element j of vector i, -1 past the row's ends
+  auto column = [&](int i, int j) {
+    int c = (i * G + t) * 8 - lead + j;
+    if (ANY && c < 0) c += CAP;
+    return c < N && (c >= 0) ? c : -1;
+  };
   // a block's sums to its partials, or (a single block) the results
   float* part = a.part + (int64_t)blockIdx.x * 2 * part_pitch(N);
   auto put = [&](int c, float x, float y) {
@@ -443,8 +489,8 @@ __global__ void __launch_bounds__(block_of(G), G == 288 ? 2 : 1) rn_bwd_kernel(c
         for (int i = 0; i < PER; ++i)
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
-            const int c = (i * G + t) * 8 - lead + j;
-            if (c < 0 || c >= N) continue;
+            const int c = column(i, j);
+            if (c < 0) continue;
             cols[0][c] = g == 0 ? dw[i][j] : cols[0][c] + dw[i][j];
             cols[1][c] = g == 0 ? dwp[i][j] : cols[1][c] + dwp[i][j];
           }
@@ -463,10 +509,15 @@ __global__ void __launch_bounds__(block_of(G), G == 288 ? 2 : 1) rn_bwd_kernel(c
         store8<false>(part + at, r, 0, 8);
         round8(dwp[i], r);
         store8<false>(part + part_pitch(N) + at, r, 0, 8);
+        if (wraps && i == 0) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            if (j < lead && column(i, j) >= 0) put(CAP + j, dw[i][j], dwp[i][j]);
+        }
       } else {
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-          if (at - lead + j >= 0 && at - lead + j < N) put(at - lead + j, dw[i][j], dwp[i][j]);
+          if (column(i, j) >= 0) put(column(i, j), dw[i][j], dwp[i][j]);
       }
     }
   }
@@ -575,8 +626,8 @@ constexpr int ring_rows() {
 template <typename XT, typename OT, bool ANY, int G, int PER>
 cudaError_t bwd_launch(const BwdArgs& a, Parts& parts, cudaStream_t s) {
   constexpr int B = block_of(G), GROUPS = B / G, S = ring_rows<XT, OT, G, PER>();
-  constexpr int smem = S * units<XT, OT>() * PER * B * 16;
-  static_assert(smem <= 200 * 1024, "shared memory of a block");
+  constexpr int smem = (S * PER * B + (ANY ? S * GROUPS : 0)) * units<XT, OT>() * 16;
+  static_assert(smem <= 208 * 1024, "shared memory of a block");
   auto kern = rn_bwd_kernel<XT, OT, G, PER, S, ANY>;
   cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kern), smem);
   if (e != cudaSuccess) return e;
@@ -595,17 +646,12 @@ cudaError_t bwd_launch(const BwdArgs& a, Parts& parts, cudaStream_t s) {
 }
 template <typename XT, typename OT, bool ANY>
 cudaError_t bwd_typed(const BwdArgs& a, bool rows, Parts& parts, cudaStream_t s) {
-  const int64_t C = rows ? a.N + (ANY ? 7 : 0) : INT64_MAX;
+  const int64_t C = rows ? a.N : INT64_MAX;
   if (C <= 32 * 8) return bwd_launch<XT, OT, ANY, 32, 1>(a, parts, s);
   if (C <= 32 * 16) return bwd_launch<XT, OT, ANY, 32, 2>(a, parts, s);
   if (C <= 128 * 8) return bwd_launch<XT, OT, ANY, 128, 1>(a, parts, s);
   if (C <= 256 * 8) return bwd_launch<XT, OT, ANY, 256, 1>(a, parts, s);
-  // a row just below a power of two needs seven columns more off the boundaries
-  if constexpr (ANY)
-    if (C <= 288 * 8) return bwd_launch<XT, OT, ANY, 288, 1>(a, parts, s);
   if (C <= 256 * 16) return bwd_launch<XT, OT, ANY, 256, 2>(a, parts, s);
-  if constexpr (ANY)
-    if (C <= 288 * 16) return bwd_launch<XT, OT, ANY, 288, 2>(a, parts, s);
   if (C <= 512 * 16) return bwd_launch<XT, OT, ANY, 512, 2>(a, parts, s);
   if constexpr (sizeof(OT) == 2)
     if (C <= 512 * 32) return bwd_launch<XT, OT, ANY, 512, 4>(a, parts, s);

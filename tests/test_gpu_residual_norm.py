@@ -130,6 +130,14 @@ def test_many_rows(lib, types, N):
     Case(2500, N, types).check()
 
 
+@pytest.mark.parametrize("types", [(BF, BF, BF), (F32, BF, F32), (F32, F32, F32)])
+@pytest.mark.parametrize("N", [249, 255, 505, 511, 1019, 1023, 2041, 2047, 4089, 4093, 4095, 8191])
+def test_rows_that_wrap(lib, types, N):
+    """Rows just below a group's columns, many (whose groups walk rows) and few, at every place."""
+    Case(700, N, types).check()
+    Case(11, N, types, post=False, gate=False).check()
+
+
 def test_rows_of_zeros_and_far_magnitudes(lib):
     c = Case(6, 512, (F32, F32, F32))
     c.x[0] = 0
