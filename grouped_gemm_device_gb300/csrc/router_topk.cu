@@ -429,8 +429,7 @@ __global__ void __launch_bounds__(kThreads, 4) router_topk_kernel(
 #pragma unroll 4
       for (int i = 0; i < c.n_group; ++i) {
         const float other = __shfl_sync(kAll, best, i * group_lanes);
-        // equal approximate values are too near to tell
-        before += other > best || (KIND != kSigmoid && other == best && i < group);
+        before += other > best || (other == best && i < group);
       }
       keep = before < c.topk_group && group < c.n_group;
       if (KIND == kSigmoid) {

@@ -135,6 +135,34 @@ def test_biases_of_any_size(lib, score, E, groups, of):
                 assert torch.equal(ids.long(), by_steps(x, bias, score, 8, groups, of, top))
 
 
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("top", [1, 2])
+def test_groups_that_nearly_tie(lib, score, top):
+    """Two groups of the same values but for a few steps of fp32, elsewhere nothing near: as many groups
+    stay as should, and the right one of the two."""
+    gen = torch.Generator().manual_seed(top)
+    T, E, groups = 3000, 64, 4
+    x = torch.randn(T, E, generator=gen)
+    x[:, 48:] = x[:, 16:32] * (1 + torch.randint(-3, 4, (T, 16), generator=gen) * 2.0 ** -23)
+    bias = torch.randn(E, generator=gen) * 0.1
+    bias[48:] = bias[16:32]
+    x, bias = x.cuda(), bias.cuda()
+    for of in (1, 2, 3):
+        plan = g.RouterTopK(E, 8, T, score=score, n_group=groups, topk_group=of, group_top=top)
+        ids = plan.forward(x, bias)[0].long()
+        assert torch.equal(ids, by_steps(x, bias, score, 8, groups, of, top))
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+def test_many_tokens(lib, score):
+    """Many tokens a warp, every choice as the definition's single steps."""
+    gen = torch.Generator().manual_seed(8)
+    x = torch.randn(40_000, 256, generator=gen).cuda()
+    bias = (0.1 * torch.randn(256, generator=gen)).cuda()
+    plan = g.RouterTopK(256, 8, 40_000, score=score, n_group=8, topk_group=4, group_top=2)
+    assert torch.equal(plan.forward(x, bias)[0].long(), by_steps(x, bias, score, 8, 8, 4, 2))
+
+
 def by_steps(x, bias, score, k, groups, of, top):
     """The definition in single fp32 operations of torch, on the GPU."""
     T, E = x.shape
