@@ -668,17 +668,20 @@ __global__ void __launch_bounds__(kThreads) router_topk_small_kernel(
   }
 }
 
+// s (1 - s) from l, q = exp(-l) and s = 1 / (1 + q), without a difference of near numbers.
+MOE_DEVICE float slope_of(float l, float q, float s) {
+  return l >= 0.f ? q * s * s : s * (1.0f - s);
+}
 // What a token's slot, one a lane below 8 (-inf and 0 in the others), adds to its expert's gradient.
 // l, u: the slot's logit and scale * d_weight, e its expert or -1.
 MOE_DEVICE float slot_grad(float l, float u, int e, int score, int renorm) {
   if (score == MOE_SCORE_SIGMOID) {
-    const float q = expf(-fabsf(l)), r = 1.0f / (1.0f + q);
-    const float s = l >= 0.f ? r : q * r;
+    const float q = expf(-l), s = __frcp_rn(1.0f + q);
     if (renorm) {
       const float sc = e >= 0 ? s : 0.f, total = sum8(sc) + kWeightEps;
-      u = (u - sum8(u * sc) / total) / total;
+      u = (u - sum8(__fmul_rn(u, sc)) / total) / total;
     }
-    u *= q * r * r;  // s (1 - s)
+    u *= slope_of(l, q, s);
   } else if (renorm) {
     const float m = max8(l);
     float w = e >= 0 ? (l == m ? 1.0f : expf(l - m)) : 0.f;
@@ -828,16 +831,16 @@ __global__ void __launch_bounds__(kThreads) router_topk_grad_small_kernel(
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         if (score == MOE_SCORE_SIGMOID) {
-          const float q = expf(-fabsf(l[j])), r = 1.0f / (1.0f + q);
-          s[j] = l[j] >= 0.f ? r : q * r;
-          slope[j] = q * r * r;
+          const float q = expf(-l[j]);
+          s[j] = __frcp_rn(1.0f + q);
+          slope[j] = slope_of(l[j], q, s[j]);
         } else {
           s[j] = l[j] == top ? 1.0f : expf(l[j] - top);
           slope[j] = 0.f;
         }
         if (id[j] < 0) s[j] = 0.f;
         total += s[j];
-        dot += u[j] * s[j];
+        dot += __fmul_rn(u[j], s[j]);
       }
       if (score == MOE_SCORE_SIGMOID) total += kWeightEps;
       else total = fmaxf(total, 1.0f);

@@ -218,6 +218,20 @@ def test_backward(lib, shape, score, renorm):
         assert torch.equal(add, keep)
 
 
+@pytest.mark.parametrize("E", [3, 16, 40, 256])
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+def test_a_single_slot_renormalised(lib, E, score):
+    """Its weight is 1 whatever the logit: what is left of the gradient is u less its rounded self, times
+    the slope over the score, for a sigmoid; 0 for a softmax."""
+    x, dw = make(300, E, spread=2.0), make(300, 1, seed=1)
+    ids = torch.randint(0, E, (300, 1), generator=torch.Generator().manual_seed(2)).int().cuda()
+    plan = g.RouterTopK(E, 1, 300, score=score, scale=2.5)
+    d = f64(plan.backward(x, dw, ids))
+    # u s / S and u are a rounding of each apart at most, divided by s; the slope over s is at most 1
+    most = 2 * U * 2.5 * np.abs(f64(dw)) if score == "sigmoid" else 0.0
+    assert (np.abs(d) <= most * 1.01).all()
+
+
 def test_backward_in_place_and_strides(lib):
     x = make(50, 40)
     wide = torch.full((50, 64), 7.0, device="cuda")
