@@ -1194,6 +1194,8 @@ class AdamW:
             raise ValueError("params, grads, masters and weight_decay differ in length")
         if state_bits not in (8, 32):
             raise ValueError(f"state_bits must be 8 or 32, not {state_bits}")
+        if not 0 <= seed < 1 << 64:
+            raise ValueError("seed must be in [0, 2^64)")
         dev = self.device = self.params[0].device if n else _gpu("cuda")
         for p, g, w in zip(self.params, self.grads, masters):
             for t in (p, g) if w is None else (p, g, w):

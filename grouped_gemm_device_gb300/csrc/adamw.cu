@@ -547,6 +547,7 @@ __global__ void __launch_bounds__(kThreads, BITS == 8 ? 3 : 4) adamw_kernel(cons
   }
 }
 
+constexpr int kReadChunk = 2 * kChunk;  // elements a block reads back at a time: sixteen a thread
 struct MomentsOut {
   __nv_bfloat16 *m[kCap], *v[kCap];
 };
@@ -557,24 +558,34 @@ __global__ void __launch_bounds__(kThreads) adamw_moments_kernel(const __grid_co
   for (int64_t c = blockIdx.x; c < b.chunks; c += gridDim.x) {
     const int i = find_tensor(b, c);
     const Tensor& t = b.t[i];
-    const int64_t blk = (c - t.first) * kWarps + warp, e0 = blk * kBlock;
-    if (e0 >= t.numel) continue;
-    const uint32_t sm = t.m_scale[blk], sv = t.v_scale[blk];
-    if (t.wide && e0 + kBlock <= t.numel) {
-      const int64_t e = e0 + lane * 8;
-      uint32_t m[4], v[4];
-      decode8<true>(load2(static_cast<const uint8_t*>(t.m) + e), sm, m);
-      decode8<false>(load2(static_cast<const uint8_t*>(t.v) + e), sv, v);
-      *reinterpret_cast<uint4*>(out.m[i] + e) = make_uint4(m[0], m[1], m[2], m[3]);
-      *reinterpret_cast<uint4*>(out.v[i] + e) = make_uint4(v[0], v[1], v[2], v[3]);
+    const int64_t c0 = (c - t.first) * kReadChunk;
+    if (t.wide && c0 + kReadChunk <= t.numel) {
+      const int64_t e = c0 + threadIdx.x * 16;
+      const uint32_t sm = t.m_scale[e / kBlock], sv = t.v_scale[e / kBlock];
+      const uint4 cm = load4(static_cast<const uint8_t*>(t.m) + e);
+      const uint4 cv = load4(static_cast<const uint8_t*>(t.v) + e);
+      auto put = [&](__nv_bfloat16* to, auto sign, const uint4& q, uint32_t scale) {
+        uint32_t lo[4], hi[4];
+        decode8<sign.value>(make_uint2(q.x, q.y), scale, lo);
+        decode8<sign.value>(make_uint2(q.z, q.w), scale, hi);
+        const uint32_t w[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+        st_global_v8(to + e, w);
+      };
+      put(out.m[i], std::true_type(), cm, sm);
+      put(out.v[i], std::false_type(), cv, sv);
       continue;
     }
+    for (int h = 0; h < kReadChunk / kChunk; ++h) {
+      const int64_t e0 = c0 + h * kChunk + warp * kBlock;
+      if (e0 >= t.numel) break;
+      const uint32_t sm = t.m_scale[e0 / kBlock], sv = t.v_scale[e0 / kBlock];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int64_t e = e0 + j * 32 + lane;
-      if (e >= t.numel) continue;
-      out.m[i][e] = __float2bfloat16_rn(decode_m(static_cast<const uint8_t*>(t.m)[e], sm));
-      out.v[i][e] = __float2bfloat16_rn(decode_r(static_cast<const uint8_t*>(t.v)[e], sv));
+      for (int j = 0; j < 8; ++j) {
+        const int64_t e = e0 + j * 32 + lane;
+        if (e >= t.numel) continue;
+        out.m[i][e] = __float2bfloat16_rn(decode_m(static_cast<const uint8_t*>(t.m)[e], sm));
+        out.v[i][e] = __float2bfloat16_rn(decode_r(static_cast<const uint8_t*>(t.v)[e], sv));
+      }
     }
   }
 }
@@ -583,7 +594,8 @@ bool on(const void* p, int bytes) { return (reinterpret_cast<uintptr_t>(p) & (by
 
 // Tensors [i, ..) of the list that hold elements, up to kCap; returns the next index. vectors: whole
 // ones where the arrays allow.
-int fill_batch(Batch& b, int i, int n, const moe_adamw_tensor_t* list, int bits, bool vectors) {
+int fill_batch(Batch& b, int i, int n, const moe_adamw_tensor_t* list, int bits, bool vectors,
+               int chunk = kChunk) {
   b.n = 0;
   b.chunks = 0;
   const int state = bits == 8 ? 8 : 32;  // bytes of eight values
@@ -595,7 +607,7 @@ int fill_batch(Batch& b, int i, int n, const moe_adamw_tensor_t* list, int bits,
                       on(l.m, state) && on(l.v, state);
     b.t[b.n++] = {l.param, l.master, l.grad, l.m, l.v, l.m_scale, l.v_scale, l.numel, b.chunks,
                   l.decay, i, (int16_t)pb, (int16_t)gb, (int16_t)wide, 0};
-    b.chunks += (l.numel + kChunk - 1) / kChunk;
+    b.chunks += (l.numel + chunk - 1) / chunk;
   }
   return i;
 }
@@ -704,12 +716,12 @@ moe_status_t moe_adamw_moments(int32_t n, const moe_adamw_tensor_t* tensors, voi
   Batch b;
   MomentsOut out;
   for (int i = 0; i < n;) {
-    i = fill_batch(b, i, n, tensors, 8, true);
+    i = fill_batch(b, i, n, tensors, 8, true, kReadChunk);
     if (b.n == 0) break;
     for (int j = 0; j < b.n; ++j) {
       out.m[j] = static_cast<__nv_bfloat16*>(m_out[b.t[j].index]);
       out.v[j] = static_cast<__nv_bfloat16*>(v_out[b.t[j].index]);
-      b.t[j].wide = on(b.t[j].m, 8) && on(b.t[j].v, 8) && on(out.m[j], 16) && on(out.v[j], 16);
+      b.t[j].wide = on(b.t[j].m, 16) && on(b.t[j].v, 16) && on(out.m[j], 32) && on(out.v[j], 32);
     }
     const cudaError_t e = launch_pdl(adamw_moments_kernel, adamw_blocks<adamw_moments_kernel, 0, 4096>(b.chunks),
                                      kThreads, 0, s, 1, b, out);

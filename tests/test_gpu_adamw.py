@@ -228,14 +228,14 @@ def test_far_magnitudes(lib, bits, eps, scale):
             assert (f64(opt.m[0]) == m1).all() and (f64(opt.v[0]) == v1).all()
             m, v = m1.astype(np.float64), v1.astype(np.float64)
         # r32 is the rounded root; the move is off by a few roundings of itself and of the weight
-        with np.errstate(invalid="ignore", divide="ignore"):
+        with np.errstate(invalid="ignore", divide="ignore"):  # 0 / 0 where nothing has been seen
             c1, c2 = 1 - B1 ** t, 1 - B2 ** t
             move = LR / c1 * m1.astype(np.float64) / (r1.astype(np.float64) / c2 ** 0.5 + eps)
         after = f64(params[0])
         ok = np.isfinite(move)
         assert (~ok == ((r1 == 0) & (eps == 0))).all()
-        assert (np.abs(after - (before - move))[ok] <= 40 * U * np.abs(move)[ok]
-                + 2 * U * np.abs(before)[ok]).all()
+        assert (np.abs(after[ok] - (before[ok] - move[ok])) <= 40 * U * np.abs(move[ok])
+                + 2 * U * np.abs(before[ok])).all()
         params[0].zero_()   # 0 / 0 where nothing has been seen and eps is 0
 
 
@@ -337,7 +337,7 @@ def test_argument_checks(lib):
     for f in (lambda: g.AdamW([p], []), lambda: g.AdamW([p], [gr.t()]),
               lambda: g.AdamW([p.cpu()], [gr]), lambda: g.AdamW([p], [gr[:4]]),
               lambda: g.AdamW([p.half()], [gr]), lambda: g.AdamW([p], [gr.half()]),
-              lambda: g.AdamW([p], [gr], state_bits=4), lambda: g.AdamW([p], [gr], masters=[gr]),
+              lambda: g.AdamW([p], [gr], state_bits=4), lambda: g.AdamW([p], [gr], seed=-1), lambda: g.AdamW([p], [gr], masters=[gr]),
               lambda: g.AdamW([p.to(BF)], [gr], masters=[p.to(BF)]),
               lambda: g.AdamW([p], [gr], weight_decay=[0.1, 0.2]), lambda: g.AdamW([p], [p]),
               lambda: g.AdamW([p, p], [gr, gr]), lambda: g.AdamW([p, p[:4]], [gr, gr[:4]])):
