@@ -1,13 +1,17 @@
 // AdamW over a list of tensors, states in 32 or 8 bits (moe_adamw_step and moe_adamw_moments in
 // include/moegmm.h, which defines the step, the 8-bit format and its rounding).
 //
-// Bound by HBM: an element's weight, gradient and states are read once and written once. A block of
-// threads takes 2048 elements of one tensor at a time, a warp of it the 256 that share a scale in an
-// 8-bit state. The step's scalars (bias
-// corrections, clip factor, learning rate) come from device memory and are formed once a block, so
-// that a captured step replays as the next one. The steps are counted by the last block to finish.
-// m, v and r = sqrt(v) are formed by single rounded fp32 operations (no contraction): which code a
-// value gets does not depend on how the compiler joins them.
+// Bound by HBM with 32-bit states: an element's weight, gradient and states are read once and
+// written once, 28 bytes (bf16 weights with masters). 403 M elements 1600 us, 7.0 TB/s, 105% of
+// the measured copy. 8-bit states move 16 bytes an element and are bound by instructions (some 75
+// an element: decoding, the step, a hash, rounding): 101 M elements about 300 us, 5.4 TB/s; their
+// moments read back, 6 bytes an element, about 95 us. 12 tensors of 60,001 fp32 together: 4.5 us,
+// the host's. A block of threads takes 2048 elements of one tensor at a time, a warp of it the 256
+// that share a scale in an 8-bit state. The step's scalars (bias corrections, clip factor,
+// learning rate) come from device memory and are formed once a block, so that a captured step
+// replays as the next one. The steps are counted by the last block to finish. m, v and r = sqrt(v)
+// are formed by single rounded fp32 operations (no contraction): which code a value gets does not
+// depend on the path.
 #include <cmath>
 
 #include "kernels.cuh"
@@ -216,10 +220,10 @@ MOE_DEVICE uint32_t max_all(float x) { return __reduce_max_sync(0xFFFFFFFFu, __f
 
 // Writes the codes of a lane's eight m and r = sqrt(v), of elements e .. e + 7 (low 32 bits), and
 // returns the block's scales. A code is the top of the value's bits plus the random ones, less the
-// scale's base; with all of them shifted left by four it is a word's top byte, which drops the sign
-// and what lies above a code. The root is taken approximately first (2 instructions against some 12):
-// its code is the rounded one's unless two steps of r would change it, which few values in 10^5 need;
-// those, and values below the least one, go a way of their own.
+// scale's base; with all of them shifted left by four it is a word's top byte, which drops the
+// sign and what lies above a code. The root is taken approximately first (2 instructions against
+// some 12): its code is the rounded one's unless two steps of r would change it, which few values
+// in 10^5 need; those, and values below the least one, go a way of their own.
 MOE_DEVICE uint2 hold8(const float (&m)[8], const float (&v)[8], float most_m, float most_r,
                        uint32_t e, uint32_t key, uint2* to_m, uint2* to_r) {
   const uint32_t top_m = max_all(most_m);
@@ -280,9 +284,9 @@ MOE_DEVICE uint2 hold8(const float (&m)[8], const float (&v)[8], float most_m, f
 }
 
 // 8-bit states: a block's next chunk is on its way to shared memory (cp.async, each thread its own
-// bytes, so that no barrier is spent) while it works on this one: the work on 64 to 80 bytes a thread
-// is long, and registers for more warps are not there. A slot holds sixteen bytes of each thread, four
-// times (the gradients take one or two), then the codes' eights.
+// bytes, so that no barrier is spent) while it works on this one: the work on 64 to 80 bytes a
+// thread is long, and registers for more warps are not there. A slot holds sixteen bytes of each
+// thread, four times (the gradients take one or two), then the codes' eights.
 constexpr int kSlotBytes = 80 * kThreads;
 constexpr int kRingBytes = 2 * kSlotBytes;
 MOE_DEVICE void cp_async16(uint32_t dst, const void* src) {
@@ -473,11 +477,11 @@ MOE_DEVICE void adamw_any(const Tensor& t, int64_t chunk, const Now& n, const St
   }
 }
 
-// Four blocks an SM: 403 M elements with 32-bit states 1740 us, with three 1826, with five (registers
-// for one) 1903.
+// 32-bit states: four blocks an SM (403 M elements, blocks that fit alone: 1740 us; three 1826,
+// five 1903). 8-bit ones: three, as a fourth spills (101 M: 470 us against 502).
 template <int BITS>
-__global__ void __launch_bounds__(kThreads, BITS == 8 ? 3 : 4) adamw_kernel(const __grid_constant__ Batch b,
-                                                         const __grid_constant__ Step s) {
+__global__ void __launch_bounds__(kThreads, BITS == 8 ? 3 : 4)
+    adamw_kernel(const __grid_constant__ Batch b, const __grid_constant__ Step s) {
   MOE_GRIDDEP_ENTRY();
   int64_t c = blockIdx.x;
   int i = c < b.chunks ? find_tensor(b, c) : 0;
@@ -547,12 +551,14 @@ __global__ void __launch_bounds__(kThreads, BITS == 8 ? 3 : 4) adamw_kernel(cons
   }
 }
 
-constexpr int kReadChunk = 2 * kChunk;  // elements a block reads back at a time: sixteen a thread
+// Elements a block reads back at a time: sixteen a thread, so that it writes whole 32-byte sectors
+// (33.6 M elements 33 us; by sixteen bytes 43).
+constexpr int kReadChunk = 2 * kChunk;
 struct MomentsOut {
   __nv_bfloat16 *m[kCap], *v[kCap];
 };
-__global__ void __launch_bounds__(kThreads) adamw_moments_kernel(const __grid_constant__ Batch b,
-                                                                 const __grid_constant__ MomentsOut out) {
+__global__ void __launch_bounds__(kThreads)
+    adamw_moments_kernel(const __grid_constant__ Batch b, const __grid_constant__ MomentsOut out) {
   MOE_GRIDDEP_ENTRY();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   for (int64_t c = blockIdx.x; c < b.chunks; c += gridDim.x) {
@@ -592,8 +598,8 @@ __global__ void __launch_bounds__(kThreads) adamw_moments_kernel(const __grid_co
 
 bool on(const void* p, int bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
 
-// Tensors [i, ..) of the list that hold elements, up to kCap; returns the next index. vectors: whole
-// ones where the arrays allow.
+// Tensors [i, ..) of the list that hold elements, up to kCap; returns the next index. vectors:
+// whole ones where the arrays allow.
 int fill_batch(Batch& b, int i, int n, const moe_adamw_tensor_t* list, int bits, bool vectors,
                int chunk = kChunk) {
   b.n = 0;
@@ -612,10 +618,11 @@ int fill_batch(Batch& b, int i, int n, const moe_adamw_tensor_t* list, int bits,
   return i;
 }
 
-// At most kTurns times the blocks that fit at once. Short blocks start at other times and so spread
-// their reads, work and writes: 403 M elements with 32-bit states 1600 us at a chunk a block, 1752 with
-// the blocks that fit alone; 101 M with 8-bit states, whose blocks fetch ahead and pay for their first
-// chunk, 423 us at 16 turns, 455 at 4, 442 at 32, 592 at a chunk a block (92 of them the moments).
+// At most kTurns times the blocks that fit at once. Short blocks start at other times and so
+// spread their reads, work and writes: 403 M elements with 32-bit states 1600 us at a chunk a
+// block, 1752 with the blocks that fit alone; 101 M with 8-bit states, whose blocks fetch ahead
+// and pay for their first chunk, 423 us with their moments at 16 turns, 455 at 4, 442 at 32, 592
+// at a chunk a block (before the moments' last step, which took 28 us from each).
 template <auto Kernel, int kSmem, int kTurns>
 int adamw_blocks(int64_t chunks) {
   static DeviceCache cache;
@@ -683,8 +690,9 @@ moe_status_t moe_adamw_step(int32_t n, const moe_adamw_tensor_t* tensors, int32_
                mix((uint32_t)seed ^ mix((uint32_t)(seed >> 32))),
                reinterpret_cast<unsigned long long*>(counters), 0};
   auto kernel = state_bits == 8 ? adamw_kernel<8> : adamw_kernel<32>;
-  // The vectors' approximate root of a v below 2^-126 is 0 in the place of up to 2^-63. An eps that loses
-  // that in its rounding hides it; under a smaller one every element takes the rounded root.
+  // The vectors' approximate root of a v below 2^-126 is 0 in the place of up to 2^-63. An eps
+  // that loses that in its rounding hides it; under a smaller one every element takes the rounded
+  // root.
   const bool vectors = eps * 0x1p-24 >= 0x1p-63 / std::sqrt(1 - beta2);
   Batch b;
   int i = 0;
@@ -723,8 +731,8 @@ moe_status_t moe_adamw_moments(int32_t n, const moe_adamw_tensor_t* tensors, voi
       out.v[j] = static_cast<__nv_bfloat16*>(v_out[b.t[j].index]);
       b.t[j].wide = on(b.t[j].m, 16) && on(b.t[j].v, 16) && on(out.m[j], 32) && on(out.v[j], 32);
     }
-    const cudaError_t e = launch_pdl(adamw_moments_kernel, adamw_blocks<adamw_moments_kernel, 0, 4096>(b.chunks),
-                                     kThreads, 0, s, 1, b, out);
+    const int grid = adamw_blocks<adamw_moments_kernel, 0, 4096>(b.chunks);
+    const cudaError_t e = launch_pdl(adamw_moments_kernel, grid, kThreads, 0, s, 1, b, out);
     count_launch(s, MOE_K_ADAMW_MOMENTS);
     if (e != cudaSuccess) return cuda_fail(e, "AdamW moments launch");
   }

@@ -495,8 +495,8 @@ moe_status_t moe_workspace_layout(const moe_layer_desc_t* desc, moe_ws_layout_t*
   return MOE_OK;
 }
 
-// The rows of a routing whose counts the stream's earlier work has left: their order, x gathered into
-// it, and the layer's quantised copies. `given`: ids that the caller chose (moe_permute).
+// The rows of a routing whose counts the stream's earlier work has left: their order, x gathered
+// into it, and the layer's quantised copies. `given`: ids that the caller chose (moe_permute).
 static moe_status_t permute_rows(const moe_layer_desc_t* d, int32_t T, const int32_t* topk_ids,
                                  const float* topk_probs, const int32_t* counts, const void* x,
                                  const Ws& w, bool given, cudaStream_t s) {

@@ -4,9 +4,16 @@
 //   s = sigmoid(l) or softmax(l);  v = s + bias;  the best groups, their best k experts;
 //   w = scale s, or scale s / sum of the chosen s
 //
-// Rows of more than 16 experts: a warp has a token; lane i holds the VPL neighbouring experts i VPL ..,
-// so that the lowest lane that holds a maximum holds the lowest index, and a tree over lanes adds
-// neighbours first. Up to 16 experts: a thread has a token.
+// Rows of more than 16 experts: a warp has a token; lane i holds the VPL neighbouring experts i
+// VPL .., so that the lowest lane that holds a maximum holds the lowest index, and a tree over
+// lanes adds neighbours first. Up to 16 experts: a thread has a token.
+//
+// The choice is bound by instructions, about 600 a token of 256 experts in 8 groups: a round for
+// each of the k largest takes some 20, scores 30, sorted lists 35, groups 60, weights 60. 65536 x
+// 256, top 8 of 4 of 8 groups, sigmoid and bias: 56 us (1.3 TB/s; 231 us with exact scores and a
+// search over eight values a round, 63 when twice as many tokens as need be were chosen anew);
+// 16384 x 128 bf16, top 4: 7.1 us; one token 4.4 us, the host's. The gradient writes a row a
+// token, and reads one where it adds: 65536 x 256 32 us, 4.4 TB/s.
 #include "kernels.cuh"
 
 namespace moe {
@@ -26,8 +33,8 @@ MOE_DEVICE uint32_t ordered(float x) {
   return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
 }
 
-// The VPL logits of a lane; NaN and what lies past E read as -inf. vec: rows lie on boundaries of VPL
-// logits and E is a multiple of VPL.
+// The VPL logits of a lane; NaN and what lies past E read as -inf. vec: rows lie on boundaries of
+// VPL logits and E is a multiple of VPL.
 template <int VPL, typename LT>
 MOE_DEVICE void load_logits(const LT* row, int E, int lane, bool vec, float (&v)[VPL]) {
   const int e0 = lane * VPL;
@@ -181,9 +188,9 @@ MOE_DEVICE int take_best(uint32_t (&key)[VPL], int lane) {
   return owner * VPL + __shfl_sync(kAll, at, owner);
 }
 
-// The k experts of one token in lanes 0 .. k - 1, by definition: exact values, a round for each expert
-// and group. `room`: two rows of 256 of the warp's shared memory. A call of its own: few tokens need it,
-// and the others' registers and instructions stay few.
+// The k experts of one token in lanes 0 .. k - 1, by definition: exact values, a round for each
+// expert and group. `room`: two rows of 256 of the warp's shared memory. A call of its own: few
+// tokens need it, and the others' registers and instructions stay few.
 template <int VPL, typename LT>
 __device__ __noinline__ int choose(const LT* row, const float* bias, const Choice& c,
                                    float (*room)[256]) {
@@ -271,8 +278,8 @@ MOE_DEVICE void sort4(float& a, float& b, float& c, float& d) {
   order_pair(b, c);
 }
 constexpr int list_of(int VPL) { return VPL < 5 ? VPL : 5; }
-// A lane's largest values, descending: all of them, or the first five of eight (odd-even merge, Batcher
-// 1968).
+// A lane's largest values, descending: all of them, or the first five of eight (odd-even merge,
+// Batcher 1968).
 template <int VPL>
 MOE_DEVICE void top_values(const float (&v)[VPL], float (&l)[list_of(VPL)]) {
   if constexpr (VPL <= 4) {
@@ -305,7 +312,8 @@ MOE_DEVICE float sigmoid_near(float x) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
   return r;
 }
-// Whether a and b, a >= b, may be in another order than they seem, each being off by eps / 2 at most.
+// Whether a and b, a >= b, may be in another order than they seem, each being off by eps / 2 at
+// most.
 MOE_DEVICE bool near(float a, float b, float eps) { return !(a - b > eps) && b != -INFINITY; }
 
 // A token's weights, one a lane below k (live): l the expert's logit, s its score (softmax alone).
@@ -325,16 +333,16 @@ MOE_DEVICE float weight_of(float l, float s, bool live, const Choice& c) {
   return w * c.scale;
 }
 
-// What decides the choice: the logits themselves; sigmoids (and biases), taken approximately; softmax
-// probabilities.
+// What decides the choice: the logits themselves; sigmoids (and biases), taken approximately;
+// softmax probabilities.
 enum Kind { kLogits = 0, kSigmoid = 1, kSoftmax = 2 };
 constexpr float kFar = 3e38f;  // an infinite bias, and what lies past E, among approximate values
 
-// GROUPS: the experts' groups are whole lanes, a power of two of them each. k <= KMAX. The choice goes by sorted
-// lists, one a lane, whose heads the warp's maximum takes one by one. kSigmoid: 4 instructions a score
-// against some 17, and three bits of a value hold its place in the lane. A token with two deciding values
-// too near to tell, with an infinite value among its k, or with a lane that holds equal ones or more than
-// its list, is chosen anew by definition.
+// GROUPS: the experts' groups are whole lanes, a power of two of them each. k <= KMAX. The choice
+// goes by sorted lists, one a lane, whose heads the warp's maximum takes one by one. kSigmoid: 4
+// instructions a score against some 17, and three bits of a value hold its place in the lane. A
+// token with two deciding values too near to tell, with an infinite value among its k, or with a
+// lane that holds equal ones or more than its list, is chosen anew by definition.
 template <int VPL, bool GROUPS, int KIND, int KMAX, typename LT>
 __global__ void __launch_bounds__(kThreads, 4) router_topk_kernel(
     const LT* __restrict__ logits, int64_t ld, const float* __restrict__ bias,
@@ -361,9 +369,9 @@ __global__ void __launch_bounds__(kThreads, 4) router_topk_kernel(
     if (fabsf(b[j]) < INFINITY) most = fmaxf(most, fabsf(b[j]));
     if (KIND == kSigmoid) b[j] = fmaxf(fminf(b[j], kFar), -kFar);  // finite, for the place's bits
   }
-  // kSigmoid: a value is off by 2^-21 in its score, by a step in the sum with its bias and by up to seven
-  // in its last three bits, 2^-20 of it together; a sum of two (of up to 1 + the largest bias) by twice
-  // that and a step of its own
+  // kSigmoid: a value is off by 2^-21 in its score, by a step in the sum with its bias and by up
+  // to seven in its last three bits, 2^-20 of it together; a sum of two (of up to 1 + the largest
+  // bias) by twice that and a step of its own
   const float eps_group = 0x1p-19f + 0x1.2p-18f * (1.0f + warp_max(most));
   const uint32_t lane_bit = 1u << lane;
   const int64_t step = (int64_t)gridDim.x * kWarps;
@@ -672,8 +680,8 @@ __global__ void __launch_bounds__(kThreads) router_topk_small_kernel(
 MOE_DEVICE float slope_of(float l, float q, float s) {
   return l >= 0.f ? q * s * s : s * (1.0f - s);
 }
-// What a token's slot, one a lane below 8 (-inf and 0 in the others), adds to its expert's gradient.
-// l, u: the slot's logit and scale * d_weight, e its expert or -1.
+// What a token's slot, one a lane below 8 (-inf and 0 in the others), adds to its expert's
+// gradient. l, u: the slot's logit and scale * d_weight, e its expert or -1.
 MOE_DEVICE float slot_grad(float l, float u, int e, int score, int renorm) {
   if (score == MOE_SCORE_SIGMOID) {
     const float q = expf(-l), s = __frcp_rn(1.0f + q);
@@ -691,8 +699,9 @@ MOE_DEVICE float slot_grad(float l, float u, int e, int score, int renorm) {
   return e < 0 ? 0.f : u;
 }
 
-// A warp has a token: its lanes 0 .. k - 1 the slots' parts, which reach the experts through a row of
-// shared memory; each lane then has the VPL experts it owns. WHOLE: every probability has a gradient.
+// A warp has a token: its lanes 0 .. k - 1 the slots' parts, which reach the experts through a row
+// of shared memory; each lane then has the VPL experts it owns. WHOLE: every probability has a
+// gradient.
 template <int VPL, bool VEC, bool WHOLE, typename LT>
 __global__ void __launch_bounds__(kThreads) router_topk_grad_kernel(
     const LT* __restrict__ logits, int64_t ld, const int32_t* __restrict__ ids,

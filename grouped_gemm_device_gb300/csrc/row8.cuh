@@ -1,10 +1,10 @@
 // Rows of bf16 or fp32 elements in vectors of eight, on or off the vectors' boundaries.
 //
-// A vector is 16 bytes of bf16 or 32 of fp32. Rows off the boundaries (ANY) are read and written in the
-// aligned vectors that they straddle: with `lead` the place of a row's first element in its first
-// vector, element j of vector b is column 8 b - lead + j. What a row's first and last vector hold of
-// other rows is cleared when read and left alone when written. An aligned vector that holds a wanted
-// element lies in the same allocation as that element.
+// A vector is 16 bytes of bf16 or 32 of fp32. Rows off the boundaries (ANY) are read and written
+// in the aligned vectors that they straddle: with `lead` the place of a row's first element in its
+// first vector, element j of vector b is column 8 b - lead + j. What a row's first and last vector
+// hold of other rows is cleared when read and left alone when written. An aligned vector that
+// holds a wanted element lies in the same allocation as that element.
 #pragma once
 
 #include "realign.cuh"

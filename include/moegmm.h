@@ -391,8 +391,8 @@ typedef enum { MOE_DT_BF16 = 0, MOE_DT_FP32 = 1 } moe_dtype_t;
  *   value v_e   s_e + bias[e] (NaN is read as -inf), or s_e without a bias
  *   choice c_e  v_e, or without a bias l_e itself, which has the scores' order
  *   groups      the experts in n_group groups of E / n_group neighbours; a group counts the largest
- *               c of its experts (group_top 1) or the sum of its two largest v (group_top 2); the
- *               topk_group largest groups stay (ties to the lower one)
+ *               c of its experts (group_top 1) or the sum of its two largest v (group_top 2; NaN is
+ *               read as -inf); the topk_group largest groups stay (ties to the lower one)
  *   topk_ids    the k experts of those groups by descending c (ties to the lower index)
  *   weights     scale * s_j;  with renorm, sigmoid: scale * s_j / (sum of the chosen s + 1e-20),
  *               softmax: scale * softmax over the chosen logits (those equal to their maximum
