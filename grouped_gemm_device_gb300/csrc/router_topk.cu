@@ -443,7 +443,8 @@ __global__ void __launch_bounds__(kThreads, 4) router_topk_kernel(
       if (KIND == kSigmoid) {
         const float in = -warp_max(keep ? -best : -INFINITY);
         const float out = warp_max(keep || group >= c.n_group ? -INFINITY : best);
-        again = near(in, out, eps_group);
+        // sums with an infinite value are infinite, whatever else is in them
+        again = near(in, out, eps_group) || !(fabsf(in) < 0.9f * kFar);
       }
     }
     if (KIND == kSoftmax && !bias) {  // the logits' order

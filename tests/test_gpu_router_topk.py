@@ -154,6 +154,28 @@ def test_groups_that_nearly_tie(lib, score, top):
 
 
 @pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("top", [1, 2])
+def test_groups_with_infinite_biases(lib, score, top):
+    """Experts shut out or forced in: groups of one open expert, of none, of several forced ones."""
+    gen = torch.Generator().manual_seed(top)
+    T, E, groups, inf = 64, 64, 8, float("inf")
+    x = torch.randn(T, E, generator=gen).cuda()
+    biases = []
+    for fill in (-inf, 0.0):
+        for n in (3, 20):
+            b = torch.full((E,), fill)
+            b[torch.randperm(E, generator=gen)[:n]] = torch.randn(n, generator=gen)
+            b[torch.randperm(E, generator=gen)[:n]] = -inf if fill == 0.0 else 0.5
+            biases += [b, torch.where(torch.rand(E, generator=gen) < 0.1, inf, b)]
+    for b in biases:
+        b = b.cuda()
+        for of in (1, 3, 7):
+            plan = g.RouterTopK(E, 8, T, score=score, n_group=groups, topk_group=of, group_top=top)
+            ids = plan.forward(x, b)[0].long()
+            assert torch.equal(ids, by_steps(x, b, score, 8, groups, of, top))
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
 def test_many_tokens(lib, score):
     """Many tokens a warp, every choice as the definition's single steps."""
     gen = torch.Generator().manual_seed(8)
