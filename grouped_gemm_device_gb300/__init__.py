@@ -736,6 +736,18 @@ def _ld(t) -> int:
     return t.stride(0) if t.shape[0] > 1 else t.shape[1]
 
 
+def _matrix(t, name, dtype, N, most, index):
+    """Checks a matrix argument of N columns and up to `most` rows; its rows and row stride. One look at
+    each of the tensor's attributes: a small call's time is the host's."""
+    shape = t.shape
+    if len(shape) != 2 or shape[0] > most:
+        raise ValueError(f"{name}: expected at most {most} rows of {N}")
+    if (t.get_device() != index or t.dtype != dtype or shape[1] != N or not t.is_contiguous()):
+        _expect(t, name, dtype, (shape[0], N), index, rows=True)
+        return shape[0], _ld(t)
+    return shape[0], N
+
+
 def _first(buf, n):
     """The first n rows of a buffer (the buffer itself when that is all of them)."""
     return buf if buf.shape[0] == n else buf[:n]
@@ -829,6 +841,7 @@ class RouterTopK:
         self.dtype = torch.float32 if dtype is None else dtype
         self._code = _dtype_code(self.dtype)
         self.score, self.renorm, self.scale = score, bool(renorm), float(scale)
+        self._score = SCORE[score]
         self._groups = n_group, topk_group, group_top
         self.topk_ids = torch.empty(T_max, k, dtype=torch.int32, device=dev)
         self.topk_weights = torch.empty(T_max, k, dtype=torch.float32, device=dev)
@@ -839,17 +852,10 @@ class RouterTopK:
         self._out = (self.topk_ids.data_ptr(), self.topk_weights.data_ptr(),
                      self.counts.data_ptr())
 
-    def _tokens(self, logits):
-        T = logits.shape[0]
-        if T > self.T_max:
-            raise ValueError(f"{T} tokens, but T_max is {self.T_max}")
-        _expect(logits, "logits", self.dtype, (T, self.E), self._gpu, rows=True)
-        return T
-
     def forward(self, logits, bias=None, token_mask=None, stream=None):
         """logits [T, E], bias fp32 [E] (for the choice alone), token_mask bool [T] (False: ids -1,
         weights 0). Returns (topk_ids int32 [T, k], topk_weights fp32 [T, k], counts int32 [E])."""
-        T = self._tokens(logits)
+        T, ld = _matrix(logits, "logits", self.dtype, self.E, self.T_max, self._gpu)
         if bias is not None:
             _expect(bias, "bias", self.topk_weights.dtype, (self.E,), self._gpu)
         if token_mask is not None:
@@ -858,38 +864,41 @@ class RouterTopK:
                 raise ValueError("token_mask must be bool or uint8")
             _expect(token_mask, "token_mask", token_mask.dtype, (T,), self._gpu)
         _check(self._lib.moe_router_topk_fwd(
-            logits.data_ptr(), _ld(logits), self._code, _ptr(bias), _ptr(token_mask), T, self.E,
-            self.k, SCORE[self.score], *self._groups, self.renorm, self.scale, *self._out,
-            _call_stream(self._gpu, stream)))
+            logits.data_ptr(), ld, self._code, None if bias is None else bias.data_ptr(),
+            _ptr(token_mask), T, self.E, self.k, self._score, *self._groups, self.renorm, self.scale,
+            *self._out, _call_stream(self._gpu, stream)))
         self.T = T
-        return _first(self.topk_ids, T), _first(self.topk_weights, T), self.counts
+        if T == self.T_max:
+            return self.topk_ids, self.topk_weights, self.counts
+        return self.topk_ids[:T], self.topk_weights[:T], self.counts
 
     def backward(self, logits, d_weights, topk_ids=None, add_to=None, stream=None):
         """d_weights fp32 [T, k]; topk_ids: the forward's (None: those of the last forward, which had
         as many tokens or more); add_to fp32 [T, E] is added to the result (RouterLoss.backward's,
         say). Returns d_logits fp32 [T, E]."""
-        import torch
-        T = self._tokens(logits)
-        _expect(d_weights, "d_weights", torch.float32, (T, self.k), self._gpu)
+        T, ld = _matrix(logits, "logits", self.dtype, self.E, self.T_max, self._gpu)
+        _expect(d_weights, "d_weights", self.topk_weights.dtype, (T, self.k), self._gpu)
         if topk_ids is None:
             if self.T is None or T > self.T:
                 raise ValueError(f"no forward of {T} tokens has left topk_ids")
             topk_ids = self.topk_ids
         else:
-            _expect(topk_ids, "topk_ids", torch.int32, (T, self.k), self._gpu)
+            _expect(topk_ids, "topk_ids", self.topk_ids.dtype, (T, self.k), self._gpu)
+        add = None, 0
         if add_to is not None:
-            _expect(add_to, "add_to", torch.float32, (T, self.E), self._gpu, rows=True)
+            _expect(add_to, "add_to", d_weights.dtype, (T, self.E), self._gpu, rows=True)
+            add = add_to.data_ptr(), _ld(add_to)
         if self.d_logits is None:
+            import torch
             # what the current stream has given back may still be in use there
             with _torch_on(self._gpu, stream):
                 self.d_logits = torch.empty(self.T_max, self.E, dtype=torch.float32,
                                             device=self.device)
         _check(self._lib.moe_router_topk_bwd(
-            logits.data_ptr(), _ld(logits), self._code, topk_ids.data_ptr(),
-            d_weights.data_ptr(), T, self.E, self.k, SCORE[self.score], self.renorm, self.scale,
-            _ptr(add_to), 0 if add_to is None else _ld(add_to), self.d_logits.data_ptr(), self.E,
+            logits.data_ptr(), ld, self._code, topk_ids.data_ptr(), d_weights.data_ptr(), T, self.E,
+            self.k, self._score, self.renorm, self.scale, *add, self.d_logits.data_ptr(), self.E,
             _call_stream(self._gpu, stream)))
-        return _first(self.d_logits, T)
+        return self.d_logits if T == self.T_max else self.d_logits[:T]
 
 
 class LayerNorm:
@@ -995,11 +1004,11 @@ class ResidualNorm:
         self._out = self.h.data_ptr(), self.rstd_post.data_ptr(), self.rstd.data_ptr()
 
     def _rows(self, x, name, dtype, M=None):
-        if x.dim() != 2 or x.shape[0] > self.M_max:
-            raise ValueError(f"{name}: expected at most {self.M_max} rows of {self.N}")
-        if M is not None and x.shape[0] != M:
-            raise ValueError(f"{name}: expected {M} rows, got {x.shape[0]}")
-        return _expect(x, name, dtype, (x.shape[0], self.N), self._gpu, rows=True).shape[0]
+        """A matrix argument's rows, address and row stride."""
+        rows, ld = _matrix(x, name, dtype, self.N, self.M_max, self._gpu)
+        if M is not None and rows != M:
+            raise ValueError(f"{name}: expected {M} rows, got {rows}")
+        return rows, x.data_ptr(), ld
 
     def _weight(self, w, name):
         if w is None:
@@ -1007,31 +1016,30 @@ class ResidualNorm:
         return _expect(w, name, self.weight_dtype, (self.N,), self._gpu)
 
     def _branch(self, o, post_weight, gate, M):
-        """Checks what belongs to a branch; its post norm (0 or 1)."""
+        """Checks what belongs to a branch; its post norm (0 or 1), address and row stride."""
         if o is None:
             if post_weight is not None or gate is not None:
                 raise ValueError("post_weight and gate need a branch o")
-            return 0
-        self._rows(o, "o", self.branch_dtype, M)
-        self._weight(post_weight, "post_weight")
+            return 0, None, 0
+        _, at, ld = self._rows(o, "o", self.branch_dtype, M)
+        if post_weight is not None:
+            self._weight(post_weight, "post_weight")
         if gate is not None:
             _expect(gate, "gate", self.rstd.dtype, (M,), self._gpu)
-        return self._post
+        return self._post, at, ld
 
     def forward(self, x, o=None, weight=None, post_weight=None, gate=None, norm=True, stream=None):
         """x [M, N] of the stream, o [M, N] the branch that joins it (None: x_new is x), gate fp32
         [M]; norm=False: no h (the last block's sum). Returns (x_new [M, N], h [M, N] or None)."""
-        M = self._rows(x, "x", self.dtype)
-        post = self._branch(o, post_weight, gate, M)
-        self._weight(weight, "weight")
+        M, at, ld = self._rows(x, "x", self.dtype)
+        post, *branch = self._branch(o, post_weight, gate, M)
+        if weight is not None:
+            self._weight(weight, "weight")
         if not norm and (weight is not None or o is None):
             raise ValueError("without a norm there is a branch and no weight")
         h, rstd_post, rstd = self._out
-        if o is None:
-            branch = None, 0
-            new = None
-        else:
-            branch = o.data_ptr(), _ld(o)
+        new = None
+        if o is not None:
             if self.x_new is None:
                 import torch
                 # what the current stream has given back may still be in use there
@@ -1040,11 +1048,17 @@ class ResidualNorm:
                                              device=self.device)
             new = self.x_new.data_ptr()
         _check(self._lib.moe_residual_norm_fwd(
-            x.data_ptr(), _ld(x), *branch, _ptr(post_weight), _ptr(gate), _ptr(weight), new,
-            self.N, h if norm else None, self.N, rstd_post, rstd, M, self.N, self.scale, post,
-            self.eps, *self._codes, _call_stream(self._gpu, stream)))
+            at, ld, *branch, None if post_weight is None else post_weight.data_ptr(),
+            None if gate is None else gate.data_ptr(),
+            None if weight is None else weight.data_ptr(), new, self.N, h if norm else None, self.N,
+            rstd_post, rstd, M, self.N, self.scale, post, self.eps, *self._codes,
+            _call_stream(self._gpu, stream)))
         self.M, self.M_post = (M if norm else None), (M if post else None)
-        return x if o is None else _first(self.x_new, M), _first(self.h, M) if norm else None
+        if o is not None:
+            x = self.x_new if M == self.M_max else self.x_new[:M]
+        if not norm:
+            return x, None
+        return x, self.h if M == self.M_max else self.h[:M]
 
     def _stats(self, given, name, own, M, rows):
         if given is not None:
@@ -1063,19 +1077,22 @@ class ResidualNorm:
         import torch
         if dh is None and dx_new is None:
             raise ValueError("neither dh nor dx_new")
-        M = (self._rows(dx_new, "dx_new", self.dtype) if dh is None
-             else self._rows(dh, "dh", self.branch_dtype))
-        if dx_new is not None:
-            self._rows(dx_new, "dx_new", self.dtype, M)
-        post = self._branch(o, post_weight, gate, M)
+        none = None, 0
+        if dh is None:
+            M, *dxn = self._rows(dx_new, "dx_new", self.dtype)
+            grad = none
+        else:
+            M, *grad = self._rows(dh, "dh", self.branch_dtype)
+            dxn = none if dx_new is None else self._rows(dx_new, "dx_new", self.dtype, M)[1:]
+        post, *branch = self._branch(o, post_weight, gate, M)
         if dh is None:
             if weight is not None:
                 raise ValueError("weight needs dh")
-            x_new = r = None
+            new, r = none, None
         else:
             if x_new is None:
                 raise ValueError("dh needs x_new")
-            self._rows(x_new, "x_new", self.dtype, M)
+            new = self._rows(x_new, "x_new", self.dtype, M)[1:]
             r = self._stats(rstd, "rstd", self.rstd, M, self.M)
         rp = self._stats(rstd_post, "rstd_post", self.rstd_post, M, self.M_post) if post else None
         self._weight(weight, "weight")
@@ -1094,15 +1111,11 @@ class ResidualNorm:
         dw = None if weight is None else self.d_weight
         dwp = None if post_weight is None else self.d_post_weight
         dg = None if gate is None else self.d_gate
-
-        def rows(t):
-            return (None, 0) if t is None else (t.data_ptr(), _ld(t))
-
         _check(self._lib.moe_residual_norm_bwd(
-            *rows(dh), *rows(dx_new), *rows(x_new), *rows(o), _ptr(post_weight), _ptr(gate),
-            _ptr(weight), rp, r, self.dx.data_ptr(), self.N, _ptr(do), self.N, _ptr(dwp),
-            _ptr(dw), _ptr(dg), M, self.N, self.scale, post, *self._codes, self.ws.data_ptr(),
-            self.ws_bytes, _call_stream(self._gpu, stream)))
+            *grad, *dxn, *new, *branch, _ptr(post_weight), _ptr(gate), _ptr(weight), rp, r,
+            self.dx.data_ptr(), self.N, _ptr(do), self.N, _ptr(dwp), _ptr(dw), _ptr(dg), M, self.N,
+            self.scale, post, *self._codes, self.ws.data_ptr(), self.ws_bytes,
+            _call_stream(self._gpu, stream)))
         return (_first(self.dx, M), None if do is None else _first(do, M), dw, dwp,
                 None if dg is None else _first(dg, M))
 

@@ -10,9 +10,9 @@
 //
 // The choice is bound by instructions, about 600 a token of 256 experts in 8 groups: a round for
 // each of the k largest takes some 20, scores 30, sorted lists 35, groups 60, weights 60. 65536 x
-// 256, top 8 of 4 of 8 groups, sigmoid and bias: 56 us (1.3 TB/s; 231 us with exact scores and a
+// 256, top 8 of 4 of 8 groups, sigmoid and bias: 59 us (1.2 TB/s; 231 us with exact scores and a
 // search over eight values a round, 63 when twice as many tokens as need be were chosen anew);
-// 16384 x 128 bf16, top 4: 7.1 us; one token 4.4 us, the host's. The gradient writes a row a
+// 16384 x 128 bf16, top 4: 7.5 us; one token 4.0 us, the host's. The gradient writes a row a
 // token, and reads one where it adds: 65536 x 256 32 us, 4.4 TB/s.
 #include "kernels.cuh"
 
