@@ -154,6 +154,18 @@ template <typename I>
 __host__ __device__ constexpr I part_pitch(I N) {
   return (N + 7) / 8 * 8 + 8;
 }
+// Eight partial sums. The workspace lies on any 16-byte boundary; on a 32-byte one they are a single
+// store (8192 x 4096 bf16 backward 66.8 us, 68.0 with two everywhere).
+MOE_DEVICE void store_part8(float* p, const float (&v)[8]) {
+  if ((reinterpret_cast<uintptr_t>(p) & 31u) == 0) {
+    Raw8<float> r;
+    round8(v, r);
+    store8<false>(p, r, 0, 8);
+  } else {
+    reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+    reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+  }
+}
 struct BwdArgs {
   const void *dh, *dxn, *xn, *o;
   void *dx, *d_o;
@@ -513,11 +525,8 @@ __global__ void __launch_bounds__(block_of(G), ANY && G == 256 ? 2 : 1)
       const int at = (i * G + t) * 8;
       if (at - lead >= N) continue;
       if (gridDim.x > 1) {  // column c at c + lead: whole vectors
-        Raw8<float> r;
-        round8(dw[i], r);
-        store8<false>(part + at, r, 0, 8);
-        round8(dwp[i], r);
-        store8<false>(part + part_pitch(N) + at, r, 0, 8);
+        store_part8(part + at, dw[i]);
+        store_part8(part + part_pitch(N) + at, dwp[i]);
         if (wraps && i == 0) {
 #pragma unroll
           for (int j = 0; j < 8; ++j)

@@ -268,3 +268,29 @@ def test_argument_checks(lib):
             f()
     with pytest.raises(g.MoeError):
         g.ResidualNorm(64, 8, dtype=BF, branch_dtype=F32).forward(x, x.float())
+
+
+@pytest.mark.parametrize("types", [(BF, BF, BF), (F32, BF, F32), (F32, F32, F32)])
+@pytest.mark.parametrize("N", [7, 512, 513, 520, 1019, 2880, 4095, 4096, 8192, 9000])
+def test_a_workspace_on_any_16_byte_boundary(lib, types, N):
+    """The weights' gradients through partial sums in a workspace at every 16 bytes of a 64: the same
+    bits, and nothing written outside the bytes that the call asks for."""
+    xt, ot, wt = types
+    for M in (2, 40):
+        c = Case(M, N, types)
+        x_new, _ = c.forward()
+        want = [t.clone() for t in c.backward(x_new)]
+        need = g.moe_residual_norm_workspace(M, N)
+        code = {BF: 0, F32: 1}
+        outs = [torch.empty_like(t) for t in want]
+        dx, do, dw, dwp, dg = outs
+        for at in (0, 16, 32, 48):
+            buf = torch.full((need + 128,), 0x5A, dtype=torch.uint8, device="cuda")
+            assert buf.data_ptr() % 64 == 0
+            for t in outs:
+                t.fill_(7.0)
+            g.moe_residual_norm_bwd(c.dh, N, c.dx_new, N, x_new, N, c.o, N, c.wp, c.gate, c.w,
+                                    c.plan.rstd_post, c.plan.rstd, dx, N, do, N, dwp, dw, dg, M, N,
+                                    SCALE, 1, code[xt], code[ot], code[wt], buf.data_ptr() + at, need)
+            assert all(torch.equal(a, b) for a, b in zip(outs, want))
+            assert (buf[:at] == 0x5A).all() and (buf[at + need:] == 0x5A).all()
