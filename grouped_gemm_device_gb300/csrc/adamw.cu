@@ -142,9 +142,12 @@ MOE_DEVICE Moments advance(float g, float m, float v2, const Step& s) {
   o.r = __fsqrt_rn(o.v);
   return o;
 }
-// The quotient within two steps: r rb + eps is 0 or between 2^-75 and 2^126.
+// r rb + eps is 0 (with m / 0, as the formula has it) or between 2^-126 and 2^126, where the quotient is
+// within two steps; FAR: any number, and a rounded quotient.
+template <bool FAR>
 MOE_DEVICE float update(float p, const Moments& o, float lr_decay, const Now& n, const Step& s) {
-  return (p - p * lr_decay) - n.a * __fdividef(o.m, o.r * n.rb + s.eps);
+  const float d = o.r * n.rb + s.eps;
+  return (p - p * lr_decay) - n.a * (FAR ? __fdiv_rn(o.m, d) : __fdividef(o.m, d));
 }
 
 // 8 fp32 or 16 bytes in one access; streamed data is not kept in L1.
@@ -381,7 +384,7 @@ MOE_DEVICE void adamw_wide(const Tensor& t, int64_t chunk, const char* slot, uin
     if constexpr (BITS == 8) v[j] = __fmul_rn(v[j], v[j]);
     v[j] = __fadd_rn(__fmul_rn(v[j], s.b2), __fmul_rn(__fmul_rn(gs, s.c2), gs));
     const float r = sqrt_approx(v[j]);
-    // r rb + eps is 0 or between 2^-75 and 2^126
+    // r rb + eps is between 2^-39 and 2^126 (moe_adamw_step's `vectors` and `far`)
     p[j] = (p[j] - p[j] * lr_decay) - n.a * (m[j] * rcp_approx(r * n.rb + s.eps));
     if constexpr (BITS == 8) {
       most_m = most_of(most_m, m[j]);
@@ -408,7 +411,7 @@ MOE_DEVICE void adamw_wide(const Tensor& t, int64_t chunk, const char* slot, uin
 }
 
 // Any chunk: a warp's lane i has every 32nd element of its block of 256 from i on.
-template <int BITS>
+template <int BITS, bool FAR>
 MOE_DEVICE void adamw_any(const Tensor& t, int64_t chunk, const Now& n, const Step& s) {
   const int lane = threadIdx.x & 31;
   const int64_t blk = chunk * kWarps + (threadIdx.x >> 5), e0 = blk * kBlock + lane;
@@ -449,7 +452,7 @@ MOE_DEVICE void adamw_any(const Tensor& t, int64_t chunk, const Now& n, const St
       most_r = max(most_r, __float_as_uint(fabsf(o.r)));
     }
     if (e >= t.numel) continue;
-    const float w = update(p[j], o, lr_decay, n, s);
+    const float w = update<FAR>(p[j], o, lr_decay, n, s);
     weights[e] = w;
     if (t.p_bf16) static_cast<__nv_bfloat16*>(t.p)[e] = __float2bfloat16_rn(w);
     if constexpr (BITS == 32) {
@@ -478,8 +481,10 @@ MOE_DEVICE void adamw_any(const Tensor& t, int64_t chunk, const Now& n, const St
 }
 
 // 32-bit states: four blocks an SM (403 M elements, blocks that fit alone: 1740 us; three 1826,
-// five 1903). 8-bit ones: three, as a fourth spills (101 M: 470 us against 502).
-template <int BITS>
+// five 1903). 8-bit ones: three, as a fourth spills (101 M: 470 us against 502). FAR: an eps that
+// only single elements and rounded quotients are right for, which the others do not pay for (fp32
+// weights off the vectors' boundaries, 101 M: 440 us, 506 with them).
+template <int BITS, bool FAR>
 __global__ void __launch_bounds__(kThreads, BITS == 8 ? 3 : 4)
     adamw_kernel(const __grid_constant__ Batch b, const __grid_constant__ Step s) {
   MOE_GRIDDEP_ENTRY();
@@ -495,15 +500,19 @@ __global__ void __launch_bounds__(kThreads, BITS == 8 ? 3 : 4)
     return sn;
   };
   Now n;
-  if constexpr (BITS == 32) {
+  if constexpr (BITS == 32 || FAR) {
     n = step_numbers();
     if (n.skip) return;
     for (; c < b.chunks; c += gridDim.x) {
       while (i + 1 < b.n && b.t[i + 1].first <= c) ++i;
       const Tensor& t = b.t[i];
       const int64_t chunk = c - t.first;
-      if (wide(t, chunk)) adamw_wide<32>(t, chunk, nullptr, 0, 0, 0, n, s);
-      else adamw_any<32>(t, chunk, n, s);
+      if constexpr (FAR) {
+        adamw_any<BITS, true>(t, chunk, n, s);
+      } else {
+        if (wide(t, chunk)) adamw_wide<32>(t, chunk, nullptr, 0, 0, 0, n, s);
+        else adamw_any<32, false>(t, chunk, n, s);
+      }
     }
   } else {
     extern __shared__ __align__(16) char ring[];
@@ -538,7 +547,7 @@ __global__ void __launch_bounds__(kThreads, BITS == 8 ? 3 : 4)
         adamw_wide<8>(t, chunk, ring + turn * kSlotBytes, m_scale, r_scale,
                       word_key(t, chunk * kChunk, n), n, s);
       else
-        adamw_any<8>(t, chunk, n, s);
+        adamw_any<8, false>(t, chunk, n, s);
     }
   }
   if (!s.last) return;
@@ -689,11 +698,12 @@ moe_status_t moe_adamw_step(int32_t n, const moe_adamw_tensor_t* tensors, int32_
                (float)eps, max_norm, std::log(beta1), std::log(beta2), lr_device, grad_norm,
                mix((uint32_t)seed ^ mix((uint32_t)(seed >> 32))),
                reinterpret_cast<unsigned long long*>(counters), 0};
-  auto kernel = state_bits == 8 ? adamw_kernel<8> : adamw_kernel<32>;
   // The vectors' approximate root of a v below 2^-126 is 0 in the place of up to 2^-63. An eps
   // that loses that in its rounding hides it; under a smaller one every element takes the rounded
-  // root.
+  // root. r / sqrt(1 - beta2^t) is 0 or between 2^-75 and 2^91: a denominator outside the approximate
+  // quotients' range comes from eps alone.
   const bool vectors = eps * 0x1p-24 >= 0x1p-63 / std::sqrt(1 - beta2);
+  const bool far = (eps > 0 && eps < 0x1p-126) || eps > 0x1p125;
   Batch b;
   int i = 0;
   do {
@@ -701,10 +711,20 @@ moe_status_t moe_adamw_step(int32_t n, const moe_adamw_tensor_t* tensors, int32_
     int left = i;
     while (left < n && tensors[left].numel == 0) ++left;
     step.last = left == n;
-    const int grid = state_bits == 8 ? adamw_blocks<adamw_kernel<8>, kRingBytes, 16>(b.chunks)
-                                     : adamw_blocks<adamw_kernel<32>, 0, 4096>(b.chunks);
-    const cudaError_t e =
-        launch_pdl(kernel, grid, kThreads, state_bits == 8 ? kRingBytes : 0, s, 1, b, step);
+    auto launch = [&](auto bits, auto is_far) {
+      constexpr auto kernel = adamw_kernel<bits.value, is_far.value>;
+      // 8-bit states fetch their next chunk ahead
+      constexpr int smem = bits.value == 8 && !is_far.value ? kRingBytes : 0;
+      constexpr int turns = smem ? 16 : 4096;
+      return launch_pdl(kernel, adamw_blocks<kernel, smem, turns>(b.chunks), kThreads, smem, s, 1, b,
+                        step);
+    };
+    using B8 = std::integral_constant<int, 8>;
+    using B32 = std::integral_constant<int, 32>;
+    const cudaError_t e = state_bits == 8 ? (far ? launch(B8(), std::true_type())
+                                                 : launch(B8(), std::false_type()))
+                                          : (far ? launch(B32(), std::true_type())
+                                                 : launch(B32(), std::false_type()));
     count_launch(s, MOE_K_ADAMW);
     if (e != cudaSuccess) return cuda_fail(e, "AdamW launch");
     i = left;

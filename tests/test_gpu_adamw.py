@@ -353,3 +353,32 @@ def test_argument_checks(lib):
         opt.step(lr=-1.0)
     # one gradient for two weights is the caller's matter
     g.AdamW([p, torch.zeros(8, 4, device="cuda")], [gr, gr]).step()
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("eps", [1e-6, 1e-12, 1e-30, 1e-42, 1e36, 1e38, 2.9e38])
+@pytest.mark.parametrize("scale", [0.0, 1e-22, 1e-19, 1e-4, 1e15])
+def test_far_denominators(lib, bits, eps, scale):
+    """Denominators from subnormal numbers to fp32's end: elements that have seen no gradient stay, the
+    others move as the formula says, whatever path their places take."""
+    n = 5000
+    gen = torch.Generator().manual_seed(6)
+    params = [torch.zeros(n, device="cuda"), torch.zeros(n + 1, device="cuda")[1:]]
+    grads = [torch.randn(n, generator=gen).mul_(scale).cuda() for _ in params]
+    for t in grads:
+        t[::3] *= 1e-4
+        t[1000:1600] = 0
+    opt = g.AdamW(params, grads, lr=LR, betas=(B1, B2), eps=eps, weight_decay=0.0, state_bits=bits)
+    opt.step()
+    held = float(np.float32(eps))
+    zero = np.zeros(n, np.float32)
+    for p, t in zip(params, grads):
+        with np.errstate(under="ignore"):
+            m, _, r = so.moments(f64(t).astype(np.float32), zero, zero, B1, B2)
+        m, r = m.astype(np.float64), r.astype(np.float64)
+        move = LR / (1 - B1) * m / (r / (1 - B2) ** 0.5 + held)
+        # lr, its correction (a product, expm1's two steps, a quotient), the root's correction (as many
+        # and a root), the approximate root and reciprocal (2 U each), two products, a sum: 20 U; what
+        # is below 2^-126 has steps of 2^-149, in the quotient and in its product with lr
+        assert (np.abs(f64(p) + move) <= 20 * U * np.abs(move) + 2.0 ** -148).all()
+        assert not f64(p)[1000:1600].any()
