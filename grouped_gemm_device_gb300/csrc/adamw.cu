@@ -694,8 +694,10 @@ moe_status_t moe_adamw_step(int32_t n, const moe_adamw_tensor_t* tensors, int32_
   if (!on(lr_device, 4) || !on(grad_norm, 4))
     return fail(MOE_ERR_INVALID_ARG, "lr_device and grad_norm must be 4-byte aligned");
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  // an eps above 0 stays above it: a weight without gradients so far does not move (0 / eps)
+  const float eps32 = eps > 0 ? std::max((float)eps, 0x1p-149f) : 0.f;
   Step step = {(float)lr, (float)beta1, (float)(1 - beta1), (float)beta2, (float)(1 - beta2),
-               (float)eps, max_norm, std::log(beta1), std::log(beta2), lr_device, grad_norm,
+               eps32, max_norm, std::log(beta1), std::log(beta2), lr_device, grad_norm,
                mix((uint32_t)seed ^ mix((uint32_t)(seed >> 32))),
                reinterpret_cast<unsigned long long*>(counters), 0};
   // The vectors' approximate root of a v below 2^-126 is 0 in the place of up to 2^-63. An eps

@@ -581,7 +581,8 @@ moe_status_t moe_grad_clip(int32_t n, const void *const *grads, void *const *out
  *              finite skips the step: nothing is written
  *   counters   int64 [2] device, zeroed by the caller before the first step: the steps done, and a
  *              count of the kernel's own. Calls that share them must not overlap
- * lr, decay and eps finite and >= 0, beta1 and beta2 in [0, 1), max_norm > 0. n in [0, 65536]. */
+ * lr, decay and eps finite and >= 0, beta1 and beta2 in [0, 1), max_norm > 0. n in [0, 65536]. eps
+ * is held in fp32, at least 2^-149 unless it is 0; with 0, elements whose v is 0 become m / 0. */
 typedef struct {
   void *param;         /* param_dtype [numel], written                                        */
   float *master;       /* fp32 [numel] behind bf16 weights, written; NULL for fp32 weights    */

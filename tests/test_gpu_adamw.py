@@ -382,3 +382,20 @@ def test_far_denominators(lib, bits, eps, scale):
         # is below 2^-126 has steps of 2^-149, in the quotient and in its product with lr
         assert (np.abs(f64(p) + move) <= 20 * U * np.abs(move) + 2.0 ** -148).all()
         assert not f64(p)[1000:1600].any()
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("eps", [1e-44, 1e-45, 1e-50, 5e-324])
+def test_an_eps_below_fp32_is_not_0(lib, bits, eps):
+    """What has seen no gradient stays where it is; what has seen one moves by lr."""
+    params = [torch.full((3000,), 0.5, device="cuda") for _ in range(2)]
+    grads = [torch.zeros(3000, device="cuda") for _ in range(2)]
+    grads[1][::2] = 1e-3
+    opt = g.AdamW(params, grads, lr=LR, betas=(B1, B2), eps=eps, weight_decay=0.0, state_bits=bits)
+    for t in (1, 2):
+        opt.step()
+        assert (params[0] == 0.5).all() and (params[1][1::2] == 0.5).all()
+    # two moves of lr, each off by 20 U and the rounding of the sum, m and r held exactly or (8 bits) to
+    # an eighth after the first step
+    off = np.abs(f64(params[1][::2]) - (0.5 - 2 * LR))
+    assert (off <= 2 * (20 * U * LR + U * 0.5) + (0.25 * LR if bits == 8 else 0.0)).all()
