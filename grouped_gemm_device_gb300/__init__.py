@@ -567,6 +567,14 @@ class Timeline:
 
 
 # ------------------------------------------------------------------ buffer plumbing
+def _filled(index):
+    """Ends a constructor that fills memory of GPU `index` on its current stream: a first call on any other
+    stream finds it filled. Within a capture the fills are the graph's."""
+    import torch
+    if not torch.cuda.is_current_stream_capturing():
+        torch.cuda.current_stream(index).synchronize()
+
+
 class MoELayer:
     """Owns the caller-side buffers of one layer (allocated with torch) and runs the C ABI
     calls on them. Weights: w1_packed [E, N1, H] bf16 (packed rows), w2 [E, F, H] bf16."""
@@ -593,6 +601,8 @@ class MoELayer:
         self.dw2 = None
         self.d_fc1_bias = None     # extras: [E, N1] fp32, logical order
         self.d_feat_scale = None   # extras: [E, F] fp32
+        if self.ws.is_cuda:
+            _filled(self.ws.get_device())
 
     # views into the workspace -------------------------------------------------------
     def ws_view(self, name, dtype, shape):
@@ -775,6 +785,7 @@ class RouterLoss:
         self._lib = _load_calls()
         self._p = {n: getattr(self, n).data_ptr() for n in
                    ("ws", "loss", "counts", "mean_prob", "n_valid", "d_logits")}
+        _filled(self._gpu)
 
     def _tokens(self, logits, topk_ids, token_mask):
         T = logits.shape[0]
@@ -851,6 +862,7 @@ class RouterTopK:
         self._lib = _load_calls()
         self._out = (self.topk_ids.data_ptr(), self.topk_weights.data_ptr(),
                      self.counts.data_ptr())
+        _filled(self._gpu)
 
     def forward(self, logits, bias=None, token_mask=None, stream=None):
         """logits [T, E], bias fp32 [E] (for the choice alone), token_mask bool [T] (False: ids -1,
@@ -1173,6 +1185,7 @@ class GradClip:
         self.ws = torch.empty(self.ws_bytes, dtype=torch.uint8, device=dev)
         self._lib = _load_calls()
         self._work = self.norm.data_ptr(), self.ws.data_ptr(), self.ws_bytes
+        _filled(self._gpu)
 
     def clip(self, max_norm, stream=None):
         """Returns the norm [1] (on the device). max_norm = inf only takes the norm."""
@@ -1253,6 +1266,7 @@ class AdamW:
             raise ValueError("a weight shares memory with another tensor")
         self._moments = None
         self._lib = _load_calls()
+        _filled(self._gpu)
 
     def step(self, norm=None, max_norm=math.inf, lr=None, stream=None):
         """One step. norm: GradClip's (fp32 [1] on the GPU): the gradients are multiplied by
@@ -1345,6 +1359,7 @@ class Fp8Linear:
             self._xt = operand(self.xqt, self.xt_scale)
             self._dy = operand(self.dyq, self.dy_scale)
             self._dyt = operand(self.dyqt, self.dyt_scale)
+        _filled(self._gpu)
 
     def set_weight(self, w, stream=None):
         """Quantise w bf16 [N, K] (both orders for training); again whenever w has changed."""
