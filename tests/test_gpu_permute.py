@@ -164,3 +164,29 @@ def test_argument_checks(lib):
         with pytest.raises(ValueError):
             a.layer.permute(*args)
     assert np.array_equal(ids.cpu().numpy(), np.zeros((16, 3), np.int32))
+
+
+def test_first_weight_gradient_against_fp64(lib):
+    """dW1 under repeated experts, dropped slots and weights of any sign, in its logical order: bf16 stages
+    as in test_against_fp64."""
+    a = Layer(T=200, E=4, k=3, H=128, F=128)
+    gen = torch.Generator().manual_seed(3)
+    ids = torch.randint(-1, a.E + 1, (a.T, a.k), generator=gen, dtype=torch.int32).cuda()
+    ids[:50] = 2
+    ids[ids == 3] = -1                              # an expert without rows
+    probs = torch.randn(a.T, a.k, generator=gen).cuda()
+    a.layer.permute(ids, probs, a.x)
+    dw1 = a.results()[2]
+    got = torch.empty_like(a.w1)
+    g.moe_pack_fc1_weight(dw1, got, a.E, a.H, a.F, 1, 64, 1)
+    x, w1, w2, p = a.x.double(), a.w1.double().requires_grad_(), a.w2.double(), probs.double()
+    out = torch.zeros(a.T, a.H, dtype=torch.float64, device="cuda")
+    for j in range(a.k):
+        for e in range(a.E):
+            at = torch.nonzero(ids[:, j] == e)[:, 0]
+            z = x[at] @ w1[e]
+            act = torch.nn.functional.silu(z[:, :a.F]) * z[:, a.F:]
+            out = out.index_add(0, at, p[at, j:j + 1] * (act @ w2[e]))
+    (want,) = torch.autograd.grad((out * a.dy.double()).sum(), w1)
+    assert float((got.double() - want).norm() / want.norm()) <= 4 * 2.0 ** -8
+    assert not got[3].any()
