@@ -6,7 +6,9 @@
 // the measured copy. 8-bit states move 16 bytes an element and are bound by instructions (some 75
 // an element: decoding, the step, a hash, rounding): 101 M elements about 300 us, 5.4 TB/s; their
 // moments read back, 6 bytes an element, about 95 us. 12 tensors of 60,001 fp32 together: 4.5 us,
-// the host's. A block of threads takes 2048 elements of one tensor at a time, a warp of it the 256
+// the host's. Where whole vectors cannot be used, element by element: 101 M fp32 weights off their
+// boundaries 440 us with 32-bit states (floor 422), 974 to 996 with 8-bit ones. 400 equal tensors of
+// 101 M take ten launches, 458 us against 407 in one. A block of threads takes 2048 elements of one tensor at a time, a warp of it the 256
 // that share a scale in an 8-bit state. The step's scalars (bias corrections, clip factor,
 // learning rate) come from device memory and are formed once a block, so that a captured step
 // replays as the next one. The steps are counted by the last block to finish. m, v and r = sqrt(v)
@@ -64,8 +66,9 @@ MOE_DEVICE int find_tensor(const Batch& b, int64_t chunk) {
   return lo;
 }
 
-// 32-bit hash; a change of any input bit changes each output bit in half of the cases (to 0.1%,
-// measured over 2^18 words).
+// 32-bit hash; a change of any input bit changes each output bit in half of the cases, measured over
+// 2^24 random words: to 0.5% at worst (input bit 31, output bit 19), to 0.03% on average over the
+// pairs of bits.
 __host__ MOE_DEVICE uint32_t mix(uint32_t x) {
   x ^= x >> 16;
   x *= 0xf75341d5u;
@@ -702,7 +705,8 @@ moe_status_t moe_adamw_step(int32_t n, const moe_adamw_tensor_t* tensors, int32_
                reinterpret_cast<unsigned long long*>(counters), 0};
   // The vectors' approximate root of a v below 2^-126 is 0 in the place of up to 2^-63. An eps
   // that loses that in its rounding hides it; under a smaller one every element takes the rounded
-  // root. r / sqrt(1 - beta2^t) is 0 or between 2^-75 and 2^91: a denominator outside the approximate
+  // root, element by element: 101 M mixed weights at eps 1e-12 612 us against 403 at 1e-8 (8-bit
+  // states 1040 against 297). r / sqrt(1 - beta2^t) is 0 or between 2^-75 and 2^91: a denominator outside the approximate
   // quotients' range comes from eps alone.
   const bool vectors = eps * 0x1p-24 >= 0x1p-63 / std::sqrt(1 - beta2);
   const bool far = (eps > 0 && eps < 0x1p-126) || eps > 0x1p125;

@@ -9,10 +9,13 @@
 // o and writes dx and do. A row stays in registers (forward) or in shared memory (backward)
 // between its sums and their use; statistics, sums and the weights' gradients are fp32. 16384 x
 // 2880, fp32 stream and bf16 branches, both norms and a gate: forward 87 us, 6.5 TB/s, 97% of the
-// measured copy; 8192 x 4096 bf16 backward 67 us, 6.0 TB/s, 5 of them the sum of the partial
-// weight gradients; 3001 x 4095 bf16, both norms and a gate, backward 42 us, 3.5 TB/s: ten rows a
-// block, two barriers a row and the handling of partial vectors. One row of 7168: 5.3 us, the
-// host's.
+// measured copy; 8192 x 4095 bf16, both norms and a gate, forward 74 us, 3.6 TB/s (partial vectors).
+// 8192 x 4096 bf16 backward 67 us, 6.0 TB/s, 5 of them the sum of the partial
+// weight gradients; 3001 x 4095 bf16, both norms and a gate, backward 43 us, 3.5 TB/s: ten rows a
+// block, two barriers a row and the handling of partial vectors. Backward with fewer rows ahead and
+// one block an SM: 16384 x 2880 fp32 stream, bf16 branches, both norms and a gate 235 us (floor 127);
+// 4096 x 7168 of those types 122 (79), in fp32 throughout 201 (105); 2048 x 16384 bf16 123 (60). One
+// row of 7168: forward 5.3 us, backward 8.4, the host's.
 #include "kernels.cuh"
 #include "row8.cuh"
 
@@ -31,7 +34,9 @@ struct FwdArgs {
 };
 
 // Any length, stride and place: a block a row, element by element, the row once for each sum and
-// once for each result (the later ones from L2).
+// once for each result (the later ones from L2). 8192 x 4095 bf16 with branches 4104 apart: forward
+// 200 us, floor 40, and backward (rn_bwd_any_kernel) 501, floor 60; 2048 x 16384 fp32 backward 660,
+// floor 120.
 template <typename XT, typename OT>
 __global__ void __launch_bounds__(1024) rn_fwd_any_kernel(const FwdArgs a) {
   MOE_GRIDDEP_ENTRY();
@@ -257,7 +262,9 @@ MOE_DEVICE void wrap_weights(const Weight& w, int N, int c, float (&v)[8]) {
 // A group of G threads walks rows that lie alike in their vectors; a thread owns the same 8 PER
 // columns of every row and keeps their sums of the weights' gradients in registers until the end.
 // Each thread copies its own columns of the next S - 1 rows into a ring in shared memory
-// (cp.async), so that no barrier is spent on the copies. N <= 8 G PER, and the groups' number a
+// (cp.async), so that no barrier is spent on the copies. Where a row's bytes leave room for one row
+// alone (S = 1: bf16 branches above 8192 columns; fp32 ones of 257 to 512 and of 2049 to 8192) none is
+// ahead, and a row is waited for as soon as it is asked for. N <= 8 G PER, and the groups' number a
 // multiple of 8 where ANY and a group takes more than one row. ANY: a row may reach into one
 // vector more than the group's; its elements there are fewer than those that the first vector's
 // `lead` leaves free, and wrap around to them. Two blocks an SM (ANY, 256 threads): 3001 x 4095 42

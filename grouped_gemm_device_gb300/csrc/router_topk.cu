@@ -8,12 +8,18 @@
 // VPL .., so that the lowest lane that holds a maximum holds the lowest index, and a tree over
 // lanes adds neighbours first. Up to 16 experts: a thread has a token.
 //
-// The choice is bound by instructions, about 600 a token of 256 experts in 8 groups: a round for
-// each of the k largest takes some 20, scores 30, sorted lists 35, groups 60, weights 60. 65536 x
-// 256, top 8 of 4 of 8 groups, sigmoid and bias: 59 us (1.2 TB/s; 231 us with exact scores and a
-// search over eight values a round, 63 when twice as many tokens as need be were chosen anew);
-// 16384 x 128 bf16, top 4: 7.5 us; one token 4.0 us, the host's. The gradient writes a row a
-// token, and reads one where it adds: 65536 x 256 32 us, 4.4 TB/s.
+// The choice is bound by instructions and their latency, not by bytes. Some 620 instructions a token
+// of 256 experts in 8 groups were counted, two thirds of the issue slots. As written, a round for each
+// of the k + 1 largest takes some 20, scores 30, sorted lists 35, groups 60, weights 60, 365 together;
+// the rest (loads, the loop, addresses, the tests of near values, spills, tokens chosen anew) was not
+// told apart. 65536 x 256, top 8, sigmoid and bias (the bytes: 11 us): 58 us with 4 of 8 groups (231
+// with exact scores and a search over eight values a round, 63 when twice as many tokens as need be
+// were chosen anew), 41 without groups; softmax scores and bias, 4 of 8 groups 59 us, softmax
+// probabilities without groups 46. Groups that are not whole lanes go by definition: 65536 x 160, 3 of
+// 8 groups, top 6, 182 us by softmax, 211 by sigmoid and bias; 65536 x 192, 4 of 8, top 8, 229 us. A
+// thread a token: 65536 x 8, top 2, 5.2 us; 65536 x 16, top 4, 9.0 us. 16384 x 128 bf16, top 4: 7.5 us,
+// two launches; one token 4.0 us, the host's. The gradient writes a row a token, and reads one where it
+// adds: 65536 x 256 added 32 us, 4.4 TB/s; of all probabilities 29 us, added 34.
 #include "kernels.cuh"
 
 namespace moe {
@@ -342,7 +348,10 @@ constexpr float kFar = 3e38f;  // an infinite bias, and what lies past E, among 
 // goes by sorted lists, one a lane, whose heads the warp's maximum takes one by one. kSigmoid: 4
 // instructions a score against some 17, and three bits of a value hold its place in the lane. A
 // token with two deciding values too near to tell, with an infinite value among its k, or with a
-// lane that holds equal ones or more than its list, is chosen anew by definition.
+// lane that holds equal ones or more than its list, is chosen anew by definition. Four blocks an SM,
+// whose 64 registers spill 8 to 180 bytes with eight experts a lane, the most with groups and softmax:
+// three, which spill at most 32, took 60.5 us in the place of 58.0 (65536 x 256, groups, sigmoid and
+// bias), 61.1 of 59.2 (softmax and bias), 43.4 of 40.4 without groups.
 template <int VPL, bool GROUPS, int KIND, int KMAX, typename LT>
 __global__ void __launch_bounds__(kThreads, 4) router_topk_kernel(
     const LT* __restrict__ logits, int64_t ld, const float* __restrict__ bias,
@@ -903,7 +912,7 @@ void with_shape(int E, int32_t dtype, F&& fn) {
   else typed(I<8>());
 }
 int experts_a_lane(int E) { return E <= 32 ? 1 : E <= 64 ? 2 : E <= 128 ? 4 : 8; }
-// Calls fn with the experts a thread (2, 4, 8 or 16) and a value of the logits' type.
+// Calls fn with the experts a thread (4, 8 or 16) and a value of the logits' type.
 template <class F>
 void with_small(int E, int32_t dtype, F&& fn) {
   auto typed = [&](auto n) {
@@ -969,7 +978,9 @@ moe_status_t moe_router_topk_fwd(const void* logits, int64_t ld_logits, int32_t 
     return fail(MOE_ERR_INVALID_ARG, "tensors must be aligned to their elements");
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const bool small = E <= kSmall && n_group == 1;
-  const int grid = topk_blocks(T, small ? kThreads : kWarps, 4);  // as many as fit at once
+  // as many as fit at once (three of router_topk_any_kernel above 128 experts: 65536 x 160 182 us,
+  // with a grid of three an SM 144)
+  const int grid = topk_blocks(T, small ? kThreads : kWarps, 4);
   cudaError_t e = cudaSuccess;
   if (T == 0 || grid > 1) {  // a single block writes the counts, several add to them
     if (counts) {
