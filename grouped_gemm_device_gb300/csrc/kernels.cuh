@@ -61,6 +61,31 @@ cudaError_t launch_pdl(void (*k)(KArgs...), dim3 grid, dim3 block, size_t smem, 
   cfg.numAttrs = cluster > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, k, std::forward<Args>(args)...);
 }
+// Rows in memory: first byte, bytes of a row, bytes from one row to the next, bytes of an element.
+struct Span {
+  const void* at;
+  int64_t width, pitch;
+  int element;
+};
+inline Span span(const void* p, int64_t N, int64_t ld, int element) {
+  return {p, N * element, ld * element, element};
+}
+// Whether `out`, being written, would spoil `in`, being read, for a kernel that reads an element before it
+// writes the same one: M rows of each share memory and are not the same ones. NULL shares none.
+inline bool spoils(const Span& out, const Span& in, int64_t M) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(out.at), b = reinterpret_cast<uintptr_t>(in.at);
+  if (!a || !b || M < 1) return false;
+  const bool alike = out.pitch == in.pitch;
+  if (a == b && out.element == in.element && (alike || M == 1)) return false;
+  if (a + (uintptr_t)((M - 1) * out.pitch + out.width) <= b ||
+      b + (uintptr_t)((M - 1) * in.pitch + in.width) <= a)
+    return false;
+  if (!alike || M == 1) return true;
+  // columns of one wider matrix: in's rows begin `d` bytes behind out's
+  const int64_t d = b >= a ? (int64_t)((b - a) % (uintptr_t)out.pitch)
+                           : out.pitch - 1 - (int64_t)((a - b - 1) % (uintptr_t)out.pitch);
+  return d < out.width || d + in.width > out.pitch;
+}
 // host-side helpers of the C entry points (api.cu): record this thread's error message and return
 // its status; the SM count of the current device
 void set_last_error(const char* msg);

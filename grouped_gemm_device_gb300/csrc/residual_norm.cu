@@ -742,6 +742,11 @@ moe_status_t moe_residual_norm_fwd(const void* x, int64_t ldx, const void* o, in
   if (h == o && h && ldh != ldo)
     return fail(MOE_ERR_INVALID_ARG, "h is o, with another row stride");
   const int xb = size_of(x_dtype), ob = size_of(o_dtype), wb = size_of(w_dtype);
+  const Span sx = span(x, N, ldx, xb), so = span(o, N, ldo, ob);
+  const Span sn = span(x_new, N, ldxn, xb), sh = span(h, N, ldh, ob);
+  if (spoils(sn, sx, M) || spoils(sn, so, M) || spoils(sh, sx, M) || spoils(sh, so, M) ||
+      spoils(sh, sn, M) || (h && h == x_new))
+    return fail(MOE_ERR_INVALID_ARG, "an output shares memory with another tensor's other rows");
   if (!on(x, xb) || !on(x_new, xb) || !on(o, ob) || !on(h, ob) || !on(post_weight, wb) ||
       !on(weight, wb) || !on(gate, 4) || !on(rstd_post, 4) || !on(rstd, 4))
     return fail(MOE_ERR_INVALID_ARG, "tensors must be aligned to their elements");
@@ -819,6 +824,15 @@ moe_status_t moe_residual_norm_bwd(const void* dh, int64_t lddh, const void* dx_
     if (ws_bytes < moe_residual_norm_workspace(M, N))
       return fail(MOE_ERR_WORKSPACE, "ws_bytes=%zu < required %zu", ws_bytes,
                   moe_residual_norm_workspace(M, N));
+  }
+  if (M > 0) {
+    const Span in[4] = {span(dh, N, lddh, ob), span(dx_new, N, lddxn, xb),
+                        span(dh ? x_new : nullptr, N, ldxn, xb), span(o, N, ldo, ob)};
+    const Span sx = span(dx, N, lddx, xb), so = span(d_o, N, lddo, ob);
+    bool bad = spoils(so, sx, M) || (dx && dx == d_o);
+    for (const Span& i : in) bad = bad || spoils(sx, i, M) || spoils(so, i, M);
+    if (bad)
+      return fail(MOE_ERR_INVALID_ARG, "an output shares memory with another tensor's other rows");
   }
   if (M == 0 && !weights) return MOE_OK;
   const int w32 = w_dtype == MOE_DT_FP32;

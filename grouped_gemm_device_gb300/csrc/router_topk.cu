@@ -1043,6 +1043,10 @@ moe_status_t moe_router_topk_bwd(const void* logits, int64_t ld_logits, int32_t 
     return fail(MOE_ERR_INVALID_ARG, "NULL tensor pointer");
   if (add_to == d_logits && add_to && ld_add != ld_d)
     return fail(MOE_ERR_INVALID_ARG, "add_to is d_logits, with another row stride");
+  const Span sd = span(d_logits, E, ld_d, 4);
+  if (spoils(sd, span(add_to, E, ld_add, 4), T) ||
+      spoils(sd, span(logits, E, ld_logits, logits_dtype == MOE_DT_FP32 ? 4 : 2), T))
+    return fail(MOE_ERR_INVALID_ARG, "d_logits shares memory with other rows of add_to or logits");
   if (!on(logits, logits_dtype == MOE_DT_FP32 ? 4 : 2) || !on(topk_ids, 4) || !on(d_weights, 4) ||
       !on(add_to, 4) || !on(d_logits, 4))
     return fail(MOE_ERR_INVALID_ARG, "tensors must be aligned to their elements");

@@ -423,7 +423,8 @@ moe_status_t moe_router_topk_fwd(const void *logits, int64_t ld_logits, int32_t 
  *   topk_ids    int32 [T, k], d_weights fp32 [T, k] (moe_grouped_mlp_bwd's d_probs)
  *   add_to      fp32 [T, E], row stride ld_add >= E, or NULL: added to the result (the balance
  *               loss's gradient from moe_router_loss_bwd, say); may be d_logits
- *   d_logits    fp32 [T, E] out, row stride ld_d >= E, written whole */
+ *   d_logits    fp32 [T, E] out, row stride ld_d >= E, written whole; it shares memory with no other rows
+ *               of add_to or of the logits */
 moe_status_t moe_router_topk_bwd(const void *logits, int64_t ld_logits, int32_t logits_dtype,
                                  const int32_t *topk_ids, const float *d_weights, int32_t T,
                                  int32_t E, int32_t k, int32_t score, int32_t renorm, float scale,
@@ -497,7 +498,8 @@ moe_status_t moe_layernorm_bwd(const void *dy, int64_t lddy, const void *x, int6
  *   x, x_new     [M, N] of x_dtype, row strides ldx, ldxn >= N; x_new may be x. Without a branch
  *                (o NULL) x_new is x: x_new must be NULL, and h alone is made
  *   o, h         [M, N] of o_dtype, row strides ldo, ldh >= N; o may be NULL (no branch), h may be
- *                NULL (no norm: the last block's sum); h may be o
+ *                NULL (no norm: the last block's sum); h may be o. What is written shares memory with
+ *                nothing else, but for a tensor that it is in the place of, row for row
  *   post_weight, weight  [N] of w_dtype, each may be NULL (1)
  *   gate         fp32 [M] or NULL (1)
  *   rstd_post, rstd  fp32 [M] out, each may be NULL: 1 / sqrt(mean + eps) of the two norms (rstd_post
@@ -520,7 +522,8 @@ moe_status_t moe_residual_norm_fwd(const void *x, int64_t ldx, const void *o, in
  *                follows; dx_new NULL: nothing else reads x_new; not both. o NULL: no branch (do,
  *                d_post_weight, d_gate, post_weight, gate and rstd_post are NULL too). x_new and
  *                rstd may be NULL without dh
- *   dx may be dx_new, do may be dh or o; dx NULL: not written (it is dx_new when there is no dh)
+ *   dx may be dx_new, do may be dh or o, else what is written shares no memory with other tensors (as in
+ *                the forward); dx NULL: not written (it is dx_new when there is no dh)
  *   d_weight, d_post_weight [N] of w_dtype out, each may be NULL; summed in fp32 in a fixed order
  *                (zeros for M = 0).  d_gate fp32 [M] out or NULL
  * ws: moe_residual_norm_workspace(M, N) bytes, 16-byte aligned (may be NULL when both weight

@@ -294,3 +294,33 @@ def test_a_workspace_on_any_16_byte_boundary(lib, types, N):
                                     SCALE, 1, code[xt], code[ot], code[wt], buf.data_ptr() + at, need)
             assert all(torch.equal(a, b) for a, b in zip(outs, want))
             assert (buf[:at] == 0x5A).all() and (buf[at + need:] == 0x5A).all()
+
+
+def test_rows_of_its_own_buffers(lib):
+    """The stream goes on in the class's own buffers, row for row; other rows of them are refused."""
+    gen = torch.Generator().manual_seed(9)
+    M, N = 12, 264
+    x, o, dh = (rows_of(M, N, BF, gen) for _ in range(3))
+    w = (1 + 0.1 * torch.randn(N, generator=gen)).to(BF).cuda()
+    plan, other = (g.ResidualNorm(N, M, post_norm=True) for _ in range(2))
+    first = other.forward(x, o, w, w)[0].clone()
+    want = [t.clone() for t in other.forward(first, o, w, w)]
+    got = plan.forward(plan.forward(x, o, w, w)[0], o, w, w)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    grads = [t.clone() for t in other.backward(dh, want[0], o, w, w)[:2]]
+    back = plan.backward(dh, want[0], o, w, w)[:2]
+    assert all(torch.equal(a, b) for a, b in zip(back, grads))
+    more = [t.clone() for t in other.backward(grads[1], want[0], o, w, w, dx_new=grads[0])[:2]]
+    back = plan.backward(plan.do, want[0], o, w, w, dx_new=plan.dx)[:2]
+    assert all(torch.equal(a, b) for a, b in zip(back, more))
+    for f in (lambda: plan.forward(plan.x_new[1:], o[1:], w, w),
+              lambda: plan.forward(x[3:], plan.x_new[3:], w, w),
+              lambda: plan.forward(plan.h[1:4], weight=w),
+              lambda: plan.backward(plan.do[1:], want[0][1:], o[1:], w, w),
+              lambda: plan.backward(dh[1:], want[0][1:], o[1:], w, w, dx_new=plan.dx[1:])):
+        with pytest.raises(g.MoeError):
+            f()
+    # rows behind those that are written are any
+    got = plan.forward(plan.x_new[6:], o[6:], w, w)
+    want = other.forward(want[0][6:], o[6:], w, w)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))

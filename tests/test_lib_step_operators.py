@@ -193,3 +193,62 @@ def test_overlap():
     assert g._overlap([(0, 8, True), (4, 12, False)])
     assert g._overlap([(0, 8, False), (4, 6, True)])
     assert g._overlap([(0, 8, True), (0, 8, True)])
+
+
+APART = dict(FWD, x=P, o=2 * P, x_new=3 * P, h=4 * P, post_weight=5 * P, gate=6 * P, weight=7 * P,
+             rstd_post=8 * P, rstd=9 * P)
+ROW = 64 * 2   # bytes of a row
+
+
+@pytest.mark.parametrize("change", [
+    dict(x_new=P + ROW), dict(x=3 * P + ROW), dict(x_new=P - ROW), dict(x_new=P + 16), dict(x_new=P + 3 * ROW),
+    dict(x_new=2 * P + ROW), dict(h=P + ROW), dict(h=2 * P - ROW), dict(h=3 * P), dict(h=3 * P + ROW),
+    dict(x_new=P + ROW, ldx=128, ldxn=64), dict(x_new=P + ROW - 16, ldx=128, ldxn=128),
+    dict(x_new=P + 2 * ROW, ldx=128, ldxn=128), dict(x=P, x_dtype=1, x_new=2 * P),
+    dict(M=1, x_new=P + 16), dict(M=1, x=3 * P + 16)])
+def test_residual_norm_forward_refuses_shared_memory(change):
+    refused(g.moe_residual_norm_fwd, INVALID, APART, **change)
+
+
+BACK = dict(BWD, dh=P, dx_new=2 * P, x_new=3 * P, o=4 * P, dx=5 * P, d_o=6 * P, post_weight=7 * P,
+            gate=8 * P, weight=9 * P, rstd_post=10 * P, rstd=11 * P, d_post_weight=12 * P,
+            d_weight=13 * P, d_gate=14 * P, ws=15 * P)
+
+
+@pytest.mark.parametrize("change", [
+    dict(dx=2 * P + ROW), dict(dx=3 * P - ROW), dict(dx=P + 16), dict(dx=4 * P + ROW), dict(d_o=P + ROW),
+    dict(d_o=4 * P - 16), dict(d_o=2 * P + ROW), dict(d_o=3 * P + ROW), dict(d_o=5 * P),
+    dict(d_o=5 * P + ROW), dict(dx=P, x_dtype=1), dict(d_o=4 * P + ROW - 16, ldo=128, lddo=128)])
+def test_residual_norm_backward_refuses_shared_memory(change):
+    refused(g.moe_residual_norm_bwd, INVALID, BACK, **change)
+
+
+@pytest.mark.parametrize("change", [
+    dict(add_to=4 * P + 32, ld_add=8), dict(add_to=4 * P - 32, ld_add=8), dict(logits=4 * P + 64),
+    dict(logits=4 * P, logits_dtype=0), dict(add_to=4 * P + 16, ld_add=16, ld_d=16)])
+def test_router_topk_backward_refuses_shared_memory(change):
+    base = dict(logits=P, ld_logits=8, logits_dtype=1, topk_ids=2 * P, d_weights=3 * P, T=4, E=8, k=2,
+                score=0, renorm=0, scale=1.0, add_to=None, ld_add=0, d_logits=4 * P, ld_d=8, stream=0)
+    refused(g.moe_router_topk_bwd, INVALID, base, **change)
+
+
+# The same rows, columns of one wider matrix, neighbours: not refused. Without a GPU the launch fails.
+IN_ORDER = [
+    (g.moe_residual_norm_fwd, APART, [
+        dict(), dict(x_new=P), dict(h=2 * P), dict(x_new=P, h=2 * P), dict(x_new=2 * P), dict(h=P),
+        dict(x_new=P + 4 * ROW), dict(x_new=P + ROW, ldx=128, ldxn=128),
+        dict(x=3 * P + ROW, ldx=128, ldxn=128), dict(x_new=P - ROW, ldx=128, ldxn=128),
+        dict(M=1, x_new=P, ldxn=64, ldx=64), dict(M=1, x_new=P + ROW)]),
+    (g.moe_residual_norm_bwd, BACK, [
+        dict(), dict(dx=2 * P, d_o=P), dict(dx=2 * P, d_o=4 * P), dict(dx=3 * P),
+        dict(d_o=5 * P + 4 * ROW), dict(d_o=4 * P + ROW, ldo=128, lddo=128)])]
+
+
+@pytest.mark.parametrize("fn,base,change", [(f, b, c) for f, b, cs in IN_ORDER for c in cs])
+def test_residual_norm_in_order(fn, base, change):
+    import torch
+    if torch.cuda.is_available():
+        pytest.skip("the addresses are not memory")
+    with pytest.raises(g.MoeError) as e:
+        fn(**dict(base, **change))
+    assert e.value.status not in (INVALID, UNSUPPORTED, WORKSPACE), str(e.value)
