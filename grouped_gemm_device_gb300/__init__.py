@@ -567,9 +567,10 @@ class Timeline:
 
 
 # ------------------------------------------------------------------ buffer plumbing
-def _filled(index):
-    """Ends a constructor that fills memory of GPU `index` on its current stream: a first call on any other
-    stream finds it filled. Within a capture the fills are the graph's."""
+def _made(index):
+    """Ends a constructor that takes or fills memory of GPU `index` on its current stream: a first call on any
+    other stream finds it filled, and done with what was there before. Within a capture both are the
+    graph's."""
     import torch
     if not torch.cuda.is_current_stream_capturing():
         torch.cuda.current_stream(index).synchronize()
@@ -602,7 +603,7 @@ class MoELayer:
         self.d_fc1_bias = None     # extras: [E, N1] fp32, logical order
         self.d_feat_scale = None   # extras: [E, F] fp32
         if self.ws.is_cuda:
-            _filled(self.ws.get_device())
+            _made(self.ws.get_device())
 
     # views into the workspace -------------------------------------------------------
     def ws_view(self, name, dtype, shape):
@@ -785,7 +786,7 @@ class RouterLoss:
         self._lib = _load_calls()
         self._p = {n: getattr(self, n).data_ptr() for n in
                    ("ws", "loss", "counts", "mean_prob", "n_valid", "d_logits")}
-        _filled(self._gpu)
+        _made(self._gpu)
 
     def _tokens(self, logits, topk_ids, token_mask):
         T = logits.shape[0]
@@ -862,7 +863,7 @@ class RouterTopK:
         self._lib = _load_calls()
         self._out = (self.topk_ids.data_ptr(), self.topk_weights.data_ptr(),
                      self.counts.data_ptr())
-        _filled(self._gpu)
+        _made(self._gpu)
 
     def forward(self, logits, bias=None, token_mask=None, stream=None):
         """logits [T, E], bias fp32 [E] (for the choice alone), token_mask bool [T] (False: ids -1,
@@ -932,6 +933,7 @@ class LayerNorm:
         self.M = None  # rows of the last forward
         self._lib = _load_calls()
         self._out = self.y.data_ptr(), N, self.mean.data_ptr(), self.rstd.data_ptr()
+        _made(self._gpu)
 
     def _rows(self, x, name):
         if x.dim() != 2 or x.shape[0] > self.M_max:
@@ -1014,6 +1016,7 @@ class ResidualNorm:
         self.M = self.M_post = None
         self._lib = _load_calls()
         self._out = self.h.data_ptr(), self.rstd_post.data_ptr(), self.rstd.data_ptr()
+        _made(self._gpu)
 
     def _rows(self, x, name, dtype, M=None):
         """A matrix argument's rows, address and row stride."""
@@ -1185,7 +1188,7 @@ class GradClip:
         self.ws = torch.empty(self.ws_bytes, dtype=torch.uint8, device=dev)
         self._lib = _load_calls()
         self._work = self.norm.data_ptr(), self.ws.data_ptr(), self.ws_bytes
-        _filled(self._gpu)
+        _made(self._gpu)
 
     def clip(self, max_norm, stream=None):
         """Returns the norm [1] (on the device). max_norm = inf only takes the norm."""
@@ -1266,7 +1269,7 @@ class AdamW:
             raise ValueError("a weight shares memory with another tensor")
         self._moments = None
         self._lib = _load_calls()
-        _filled(self._gpu)
+        _made(self._gpu)
 
     def step(self, norm=None, max_norm=math.inf, lr=None, stream=None):
         """One step. norm: GradClip's (fp32 [1] on the GPU): the gradients are multiplied by
@@ -1359,7 +1362,7 @@ class Fp8Linear:
             self._xt = operand(self.xqt, self.xt_scale)
             self._dy = operand(self.dyq, self.dy_scale)
             self._dyt = operand(self.dyqt, self.dyt_scale)
-        _filled(self._gpu)
+        _made(self._gpu)
 
     def set_weight(self, w, stream=None):
         """Quantise w bf16 [N, K] (both orders for training); again whenever w has changed."""

@@ -112,3 +112,27 @@ def test_layer_under_a_given_routing(lib):
         return [y, layer.counts, layer.offsets()]
 
     same(lambda: g.MoELayer(g.make_desc(E=E, k=k, H=H, F=F, T_max=T)), call)
+
+
+def test_memory_that_its_stream_still_writes(lib):
+    """Buffers made of memory that was given back while the stream still writes it."""
+    gen = torch.Generator().manual_seed(5)
+    M, N = 512, 1024
+    x, w = torch.randn(M, N, generator=gen).to(BF).cuda(), torch.ones(N, dtype=BF, device="cuda")
+
+    def norm(plan, s):
+        return [plan.forward(x, weight=w, stream=s)[1], plan.rstd]
+
+    def layer_norm(plan, s):
+        return plan.forward(x, w, stream=s)
+
+    for make, call in ((lambda: g.ResidualNorm(N, M), norm), (lambda: g.LayerNorm(N, M), layer_norm)):
+        want = [t.clone() for t in call(make(), None)]
+        torch.cuda.synchronize()
+        torch.cuda._sleep(100_000_000)
+        late = [torch.full((M, N), 7.0, dtype=BF, device="cuda")]
+        late += [torch.full((M,), 7.0, device="cuda") for _ in range(2)]
+        del late
+        plan = make()
+        got = on_another_stream(lambda s: call(plan, s))
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
